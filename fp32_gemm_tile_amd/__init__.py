@@ -12,9 +12,15 @@ Entry points (same names as the C ABI):
   fg_sgemm_splitk(...), fg_sgemm_splitk_workspace_size(M, N, S)
   fg_num_configs(), fg_get_config(i), fg_select_config(...)
   fg_last_bad_arg(), fg_last_error(), fg_status_string(s), fg_abi_version()
+  fg_quantize_fp8(...), fg_gemm_fp8(...), fg_moe(layer, ...)
 Convenience:
   sgemm(A, B, C, alpha, beta, transA, transB, config=-1, stream=None)
       for torch tensors on the GPU (PyTorch only supplies memory and stream).
+  quantize_fp8(X, Q, S, QT, ST, block), gemm_fp8(A, SA, B, SB, C, alpha, beta),
+  empty_fp8(rows, cols, block)
+      e4m3 codes with a scale for each block of 128 (include/fp32gemm_fp8.h)
+  moe(x, gate, up, down, ids, weights, out, router, ...)
+      a mixture-of-experts layer for a few tokens (include/fp32gemm_moe.h)
 """
 from __future__ import annotations
 
@@ -68,6 +74,30 @@ _QUANTS = {"none": FG_QUANT_NONE, "bf16": FG_QUANT_BF16, "int8_row": FG_QUANT_IN
 class fg_quant(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("out", ctypes.c_void_p), ("ldq", ctypes.c_int64),
                 ("row_factor", ctypes.c_void_p)]
+
+
+FG_TYPE_F32, FG_TYPE_BF16, FG_TYPE_E4M3 = 0, 1, 2
+FG_BLOCK_ROW, FG_BLOCK_TILE = 0, 1
+_BLOCKS = {"row": FG_BLOCK_ROW, "tile": FG_BLOCK_TILE}
+FG_MOE_MAX_TOKENS, FG_MOE_MAX_TOP_K, FG_MOE_MAX_EXPERTS = 64, 16, 512
+
+
+class fg_experts(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64)]
+
+
+class fg_moe_layer(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("hidden", ctypes.c_int32), ("inner", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("weight_type", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("gate", fg_experts), ("up", fg_experts), ("down", fg_experts),
+                ("router", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("router_type", ctypes.c_int32), ("ids", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64)]
 
 
 def make_quant(kind, out, ldq, row_factor=0):
@@ -159,6 +189,18 @@ def load_library(path: str = LIB_PATH):
     lib.fg_sgemm_quant.argtypes = gemm_args[:13] + [ctypes.POINTER(fg_epilogue),
                                                     ctypes.POINTER(fg_quant), vp, i32]
     lib.fg_sgemm_quant.restype = i32
+    lib.fg_quantize_fp8.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                    i64, vp]
+    lib.fg_quantize_fp8.restype = i32
+    lib.fg_gemm_fp8.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, i32, f32,
+                                vp, i64, i32, vp, ctypes.c_size_t, vp]
+    lib.fg_gemm_fp8.restype = i32
+    lib.fg_gemm_fp8_workspace_size.argtypes = [i64, i64, i64]
+    lib.fg_gemm_fp8_workspace_size.restype = ctypes.c_size_t
+    lib.fg_moe.argtypes = [ctypes.POINTER(fg_moe_layer), vp, ctypes.c_size_t, vp]
+    lib.fg_moe.restype = i32
+    lib.fg_moe_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.fg_moe_workspace_size.restype = ctypes.c_size_t
     lib.fg_estimate_seconds.argtypes = [i64, i64, i64, i32, i32, i32]
     lib.fg_estimate_seconds.restype = ctypes.c_double
     lib.fg_get_efficiency.argtypes = [i32, ctypes.POINTER(ctypes.c_double),
@@ -433,6 +475,37 @@ def fg_probe_read(x, n, workgroups, out, stream=0) -> int:
     return load_library().fg_probe_read(x or None, n, workgroups, out or None, stream or None)
 
 
+def fg_quantize_fp8(type, block, M, N, X, ldx, Q=0, ldq=0, S=0, lds=0, QT=0, ldqt=0, ST=0,
+                    ldst=0, stream=0):
+    """Raw call (device addresses as ints); see include/fp32gemm_fp8.h."""
+    return load_library().fg_quantize_fp8(type, block, M, N, X or None, ldx, Q or None, ldq,
+                                          S or None, lds, QT or None, ldqt, ST or None, ldst,
+                                          stream or None)
+
+
+def fg_gemm_fp8(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, block_b, beta, C, ldc,
+                type_c, workspace=0, workspace_bytes=0, stream=0):
+    """Raw call (device addresses as ints); see include/fp32gemm_fp8.h."""
+    return load_library().fg_gemm_fp8(M, N, K, alpha, A or None, lda, SA or None, ldsa,
+                                      B or None, ldb, SB or None, ldsb, block_b, beta, C or None,
+                                      ldc, type_c, workspace or None, workspace_bytes,
+                                      stream or None)
+
+
+def fg_gemm_fp8_workspace_size(M, N, K) -> int:
+    return load_library().fg_gemm_fp8_workspace_size(M, N, K)
+
+
+def fg_moe(layer, workspace, workspace_bytes, stream=0):
+    """Raw call with an fg_moe_layer; see include/fp32gemm_moe.h."""
+    ref = ctypes.byref(layer) if layer is not None else None
+    return load_library().fg_moe(ref, workspace or None, workspace_bytes, stream or None)
+
+
+def fg_moe_workspace_size(tokens, top_k, experts, hidden, inner) -> int:
+    return load_library().fg_moe_workspace_size(tokens, top_k, experts, hidden, inner)
+
+
 def configs() -> list:
     return [fg_get_config(i) for i in range(fg_num_configs())]
 
@@ -494,3 +567,210 @@ def sgemm(A, B, C, alpha=1.0, beta=0.0, transA="N", transB="N", config=-1, strea
                          stream, config)
     _raise_if(st)
     return C
+
+
+# ---- 8-bit matrices and mixture of experts: torch convenience --------------
+
+def _type(t, name):
+    import torch
+    if t.dtype == torch.float32:
+        return FG_TYPE_F32
+    if t.dtype == torch.bfloat16:
+        return FG_TYPE_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _gpu(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.device
+
+
+def _call_on(device, stream, fn):
+    """fn(hipStream_t) with `device` current; stream: a torch stream, an int or
+    None (torch's current stream of that device)."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if torch.cuda.current_device() == device.index:
+        _raise_if(fn(s))
+    else:
+        with torch.cuda.device(device):
+            _raise_if(fn(s))
+
+
+def _codes(t, name):
+    """Leading dimension of a 2-D tensor of codes."""
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes)")
+    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit stride along its rows")
+    # (one row: its stride is free, and codes need a multiple of 16)
+    return t.stride(0) if t.size(0) > 1 else -(-max(1, t.size(1)) // 16) * 16
+
+
+def _scales(t, name, blocks, outer):
+    """Leading dimension of a [column blocks, rows or row blocks] tensor."""
+    import torch
+    if t is None or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if t.dim() != 2 or t.shape[0] != blocks or t.shape[1] != outer:
+        raise ValueError(f"{name} must be {blocks} x {outer}, is {tuple(t.shape)}")
+    if outer > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return max(t.stride(0), outer, 1) if blocks > 1 else max(outer, 1)
+
+
+def _cdiv(a, b):
+    return -(-a // b)
+
+
+def empty_fp8(rows, cols, block="row", device="cuda"):
+    """(codes, scales) for a rows x cols matrix: uninitialised float8_e4m3fn
+    codes whose rows start at multiples of 16 bytes, and float32 scales
+    [ceil(cols / 128), rows] ("row") or [ceil(cols / 128), ceil(rows / 128)]
+    ("tile")."""
+    import torch
+    wide = _cdiv(max(1, cols), 16) * 16
+    q = torch.empty(rows, wide, dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+    outer = rows if _BLOCKS[block] == FG_BLOCK_ROW else _cdiv(rows, 128)
+    return q, torch.empty(_cdiv(cols, 128), outer, dtype=torch.float32, device=device)
+
+
+def quantize_fp8(X, Q=None, S=None, QT=None, ST=None, block="row", stream=None):
+    """X (2-D, float32 or bfloat16, unit inner stride) to e4m3 codes with a
+    float32 scale for each block of 128 columns of a row ("row") or each
+    128 x 128 block ("tile"): X's own order into Q and S, its transpose into QT
+    and ST (either pair may be None; empty_fp8 makes them). X is read once.
+    Enqueued on ``stream`` (default: torch's current stream)."""
+    dev = _gpu(X, "X")
+    _on(dev, Q=Q, S=S, QT=QT, ST=ST)
+    ty, kind, ldx = _type(X, "X"), _BLOCKS[block], _ld(X, "X")
+    M, N = X.shape
+    args = []
+    for name, q, s, r, c in (("Q", Q, S, M, N), ("QT", QT, ST, N, M)):
+        if q is None:
+            args += [0, 0, 0, 0]
+            continue
+        if tuple(q.shape) != (r, c):
+            raise ValueError(f"{name} must be {r} x {c}, is {tuple(q.shape)}")
+        outer = r if kind == FG_BLOCK_ROW else _cdiv(r, 128)
+        args += [q.data_ptr(), _codes(q, name), s.data_ptr() if s is not None else 0,
+                 _scales(s, "S" if q is Q else "ST", _cdiv(c, 128), outer)]
+    _call_on(dev, stream, lambda st: fg_quantize_fp8(ty, kind, M, N, X.data_ptr(), ldx, *args, st))
+
+
+def gemm_fp8(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
+    """C <- alpha * A @ B.T + beta * C for e4m3 codes A (M x K, scales SA
+    [ceil(K / 128), M]) and B (N x K, scales SB [ceil(K / 128), N] or
+    [ceil(K / 128), ceil(N / 128)]) into float32 or bfloat16 C. workspace: a
+    contiguous GPU tensor that no call running at the same time uses
+    (fg_gemm_fp8_workspace_size bytes are useful), or None. Returns C.
+    Enqueued on ``stream`` (default: torch's current stream)."""
+    dev = _gpu(C, "C")
+    _on(dev, A=A, SA=SA, B=B, SB=SB, workspace=workspace)
+    M, N = C.shape
+    K = A.shape[1]
+    if A.shape[0] != M or B.shape[0] != N or B.shape[1] != K:
+        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not give C {tuple(C.shape)}")
+    lda, ldb, ldc, tc = _codes(A, "A"), _codes(B, "B"), _ld(C, "C"), _type(C, "C")
+    kb = _cdiv(K, 128)
+    ldsa = _scales(SA, "SA", kb, M)
+    tile = SB.dim() == 2 and SB.shape[1] != N
+    ldsb = _scales(SB, "SB", kb, _cdiv(N, 128) if tile else N)
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call_on(dev, stream, lambda st: fg_gemm_fp8(
+        M, N, K, alpha, A.data_ptr(), lda, SA.data_ptr(), ldsa, B.data_ptr(), ldb, SB.data_ptr(),
+        ldsb, FG_BLOCK_TILE if tile else FG_BLOCK_ROW, beta, C.data_ptr(), ldc, tc, ws, ws_bytes,
+        st))
+    return C
+
+
+def _experts(w, scales, name, E, rows, cols):
+    """fg_experts and fg_type of an [E, rows, cols] tensor."""
+    import torch
+    if tuple(w.shape) != (E, rows, cols):
+        raise ValueError(f"{name} must be {E} x {rows} x {cols}, is {tuple(w.shape)}")
+    if cols > 1 and w.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    per = 16 // w.element_size()
+    ld = w.stride(1) if rows > 1 else _cdiv(cols, per) * per
+    stride = w.stride(0) if E > 1 else 0
+    if w.dtype in (torch.float8_e4m3fn, torch.uint8):
+        if scales is None or scales.dtype != torch.float32:
+            raise TypeError(f"{name} needs float32 scales")
+        kb, rb = _cdiv(cols, 128), _cdiv(rows, 128)
+        if tuple(scales.shape) != (E, kb, rb) or (rb > 1 and scales.stride(2) != 1):
+            raise ValueError(f"scales of {name} must be {E} x {kb} x {rb} with unit inner stride")
+        return FG_TYPE_E4M3, fg_experts(w.data_ptr(), ld, stride, scales.data_ptr(),
+                                        scales.stride(1) if kb > 1 else rb,
+                                        scales.stride(0) if E > 1 else 0)
+    return _type(w, name), fg_experts(w.data_ptr(), ld, stride, None, 0, 0)
+
+
+def moe(x, gate, up, down, ids, weights, out, router=None, renormalize=True, scales=None,
+        activation="silu", workspace=None, stream=None):
+    """out[t] <- sum_s weights[t, s] * down_e @ (act(gate_e @ x[t]) * (up_e @ x[t])),
+    e = ids[t, s], for at most 64 tokens x [T, H] (float32 or bfloat16).
+    gate and up [E, I, H], down [E, H, I]: float32, bfloat16, or e4m3 codes
+    with scales = (gate's, up's, down's), each [E, ceil(columns / 128),
+    ceil(rows / 128)]. ids (int32) and weights (float32) are contiguous
+    [T, k]: with a router [E, H] they are written (the k largest logits,
+    softmax over those or, without renormalize, over all), else read, and an id
+    outside 0 .. E - 1 is an empty slot. workspace: a contiguous GPU tensor of
+    at least fg_moe_workspace_size(T, k, E, H, I) bytes that no call running at
+    the same time uses; None allocates one with torch. Returns out. Enqueued on
+    ``stream`` (default: torch's current stream)."""
+    import torch
+    dev = _gpu(x, "x")
+    T, H = x.shape
+    E, I = gate.shape[0], gate.shape[1]
+    sg, su, sd = scales if scales is not None else (None, None, None)
+    _on(dev, gate=gate, up=up, down=down, ids=ids, weights=weights, out=out, router=router,
+        workspace=workspace, **{"scales[0]": sg, "scales[1]": su, "scales[2]": sd})
+    wt, g = _experts(gate, sg, "gate", E, I, H)
+    ut, u = _experts(up, su, "up", E, I, H)
+    dt, d = _experts(down, sd, "down", E, H, I)
+    if not wt == ut == dt:
+        raise TypeError("gate, up and down must have one type")
+    if tuple(out.shape) != (T, H) or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor of T rows")
+    k = ids.shape[1]
+    if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32 \
+            or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor of ids' shape")
+    if router is not None and tuple(router.shape) != (E, H):
+        raise ValueError(f"router must be {E} x {H}")
+    layer = fg_moe_layer(T, E, k, H, I, _type(x, "x"), wt, activation_code(activation),
+                         int(bool(renormalize)), x.data_ptr() or None, _ld(x, "x"), g, u, d,
+                         router.data_ptr() if router is not None else None,
+                         _ld(router, "router") if router is not None else 0,
+                         _type(router, "router") if router is not None else 0,
+                         ids.data_ptr() or None, weights.data_ptr() or None,
+                         out.data_ptr() or None, _ld(out, "out"))
+    if workspace is None:
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            raise ValueError("a raw stream handle needs a workspace")
+        need = fg_moe_workspace_size(T, k, E, H, I)
+        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                               else torch.cuda.current_stream(dev)):
+            workspace = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call_on(dev, stream, lambda st: fg_moe(layer, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(), st))
+    return out

@@ -24,6 +24,7 @@
 #include "../../include/fp32gemm.h"
 #include "../../include/fp32gemm_probe.h"
 #include "../../include/fp32gemm_tune.h"
+#include "fg_host.h"
 #include "fg_kernels.h"
 
 // The instance list and the fitted efficiencies; a tuner builds a search
@@ -43,6 +44,10 @@ namespace {
 thread_local int32_t t_bad_arg = 0;
 thread_local char t_error[256] = "";
 
+}  // namespace
+
+namespace fg {
+
 fg_status fail(fg_status s, int32_t bad_arg, const char* fmt, ...) {
     t_bad_arg = bad_arg;
     va_list ap;
@@ -56,6 +61,15 @@ void clear_error() {
     t_bad_arg = 0;
     t_error[0] = '\0';
 }
+
+}  // namespace fg
+
+using fg::cdiv;
+using fg::check_device;
+using fg::clear_error;
+using fg::fail;
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Tile-configuration table.
@@ -210,8 +224,6 @@ Efficiency* efficiencies() {
     });
     return e;
 }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Estimated time in seconds of the call with MFMA entry e and `splits`
 // split-K slices: the rounds of resident waves the grid needs, plus, with
@@ -407,6 +419,10 @@ std::atomic<int> g_xcd_remap{1};
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_arch_ok[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
 
+}  // namespace
+
+namespace fg {
+
 fg_status check_device() {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -427,6 +443,10 @@ fg_status check_device() {
         return fail(FG_ERR_UNSUPPORTED, 0, "device %d is not gfx950", dev);
     return FG_OK;
 }
+
+}  // namespace fg
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 

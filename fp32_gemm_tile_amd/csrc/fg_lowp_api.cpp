@@ -1,0 +1,371 @@
+// Host side of include/fp32gemm_fp8.h and include/fp32gemm_moe.h: argument
+// validation, quick returns, the choice of kernel and launches on the
+// caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "../../include/fp32gemm_fp8.h"
+#include "../../include/fp32gemm_moe.h"
+#include "fg_host.h"
+#include "fg_lowp_kernels.h"
+
+using fg::cdiv;
+using fg::check_device;
+using fg::clear_error;
+using fg::fail;
+
+namespace {
+
+constexpr int64_t kMaxDim = 1ll << 30;  // as fg_sgemm
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+fg_status launched(hipError_t e, const char* what) {
+    if (e != hipSuccess) return fail(FG_ERR_HIP, 0, "%s: %s", what, hipGetErrorString(e));
+    return FG_OK;
+}
+
+// A matrix of codes: rows of at least `cols` bytes at multiples of 16.
+fg_status check_codes(const void* w, int64_t ld, int64_t cols, int arg, const char* name) {
+    if (ld < std::max<int64_t>(1, cols))
+        return fail(FG_ERR_INVALID_ARG, arg + 1, "leading dimension of %s: %lld < %lld", name,
+                    (long long)ld, (long long)cols);
+    if (ld % 16 || !aligned(w, 16))
+        return fail(FG_ERR_INVALID_ARG, ld % 16 ? arg + 1 : arg,
+                    "rows of %s must start at multiples of 16 bytes", name);
+    if (ld > FG_MAX_LD)
+        return fail(FG_ERR_UNSUPPORTED, arg + 1, "leading dimension of %s above FG_MAX_LD", name);
+    return FG_OK;
+}
+
+fg_status check_scales(const float* s, int64_t ld, int64_t outer, int arg, const char* name) {
+    if (!s) return fail(FG_ERR_INVALID_ARG, arg, "%s is NULL", name);
+    if (!aligned(s, 4)) return fail(FG_ERR_INVALID_ARG, arg, "%s is not 4-byte aligned", name);
+    if (ld < std::max<int64_t>(1, outer))
+        return fail(FG_ERR_INVALID_ARG, arg + 1, "leading dimension of %s: %lld < %lld", name,
+                    (long long)ld, (long long)outer);
+    return FG_OK;
+}
+
+int type_size(int t) { return t == FG_TYPE_F32 ? 4 : (t == FG_TYPE_BF16 ? 2 : 1); }
+
+// ---- block-scaled product ----------------------------------------------------
+
+// Shape of the tile kernel and number of slices of K.
+struct Plan {
+    int shape;
+    int64_t splits;
+};
+
+Plan plan_gemm(int64_t M, int64_t N, int64_t K, size_t ws_bytes) {
+    constexpr int64_t kCUs = 256;
+    Plan p;
+    p.shape = cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2 ? 1 : 0;
+    const fg::Fp8Shape s = fg::fp8_shape(p.shape);
+    const int64_t tiles = cdiv(M, s.bm) * cdiv(N, s.bn), kb = cdiv(K, fg::kScaleBlock);
+    int64_t want = tiles >= kCUs ? 1 : std::min<int64_t>({cdiv(2 * kCUs, tiles), kb, 32});
+    const int64_t slice = M * N * 4;
+    want = std::min<int64_t>(want, slice > 0 ? (int64_t)(ws_bytes / (size_t)slice) : 1);
+    if (want <= 1) {
+        p.splits = 1;
+    } else {
+        const int64_t per = cdiv(kb, want);
+        p.splits = cdiv(kb, per);
+    }
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, const void* X,
+                          int64_t ldx, uint8_t* Q, int64_t ldq, float* S, int64_t lds,
+                          uint8_t* QT, int64_t ldqt, float* ST, int64_t ldst,
+                          hipStream_t stream) {
+    clear_error();
+    if (type != FG_TYPE_F32 && type != FG_TYPE_BF16)
+        return fail(FG_ERR_INVALID_ARG, 1, "type must be FG_TYPE_F32 or FG_TYPE_BF16");
+    if (block != FG_BLOCK_ROW && block != FG_BLOCK_TILE)
+        return fail(FG_ERR_INVALID_ARG, 2, "unknown block kind %d", (int)block);
+    if (M < 0) return fail(FG_ERR_INVALID_ARG, 3, "M < 0");
+    if (N < 0) return fail(FG_ERR_INVALID_ARG, 4, "N < 0");
+    if (M > 0 && N > 0 && !X) return fail(FG_ERR_INVALID_ARG, 5, "X is NULL");
+    if (!aligned(X, (uintptr_t)type_size(type)))
+        return fail(FG_ERR_INVALID_ARG, 5, "X is not aligned to its type");
+    if (ldx < std::max<int64_t>(1, N))
+        return fail(FG_ERR_INVALID_ARG, 6, "ldx=%lld < N=%lld", (long long)ldx, (long long)N);
+    if (!Q && !QT) return fail(FG_ERR_INVALID_ARG, 7, "neither Q nor QT given");
+    const bool tile = block == FG_BLOCK_TILE;
+    fg_status st;
+    if (Q) {
+        if ((st = check_codes(Q, ldq, N, 7, "Q")) != FG_OK) return st;
+        if ((st = check_scales(S, lds, tile ? cdiv(M, 128) : M, 9, "S")) != FG_OK) return st;
+    }
+    if (QT) {
+        if ((st = check_codes(QT, ldqt, M, 11, "QT")) != FG_OK) return st;
+        if ((st = check_scales(ST, ldst, tile ? cdiv(N, 128) : N, 13, "ST")) != FG_OK) return st;
+    }
+    if (M > kMaxDim || N > kMaxDim)
+        return fail(FG_ERR_UNSUPPORTED, 0, "M and N are limited to 2^30");
+    if (M == 0 || N == 0) return FG_OK;
+    if ((st = check_device()) != FG_OK) return st;
+
+    fg::QuantParams p;
+    memset(&p, 0, sizeof p);
+    p.x = X;
+    p.ldx = ldx;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.q = Q;
+    p.ldq = ldq;
+    p.s = S;
+    p.lds = lds;
+    p.qt = QT;
+    p.ldqt = ldqt;
+    p.st = ST;
+    p.ldst = ldst;
+    p.bf16 = type == FG_TYPE_BF16;
+    p.tile = tile;
+    p.vec = ldx % 4 == 0 && aligned(X, 4 * (uintptr_t)type_size(type));
+    return launched(fg::launch_quantize_fp8(p, stream), "quantisation kernel");
+}
+
+size_t fg_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
+    const Plan p = plan_gemm(M, N, K, (size_t)-1 / 2);
+    return p.splits > 1 ? (size_t)(p.splits * M * N) * 4 : 0;
+}
+
+fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t* A,
+                      int64_t lda, const float* SA, int64_t ldsa, const uint8_t* B, int64_t ldb,
+                      const float* SB, int64_t ldsb, fg_block block_b, float beta, void* C,
+                      int64_t ldc, fg_type type_c, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+    clear_error();
+    if (M < 0) return fail(FG_ERR_INVALID_ARG, 1, "M < 0");
+    if (N < 0) return fail(FG_ERR_INVALID_ARG, 2, "N < 0");
+    if (K < 0) return fail(FG_ERR_INVALID_ARG, 3, "K < 0");
+    if (block_b != FG_BLOCK_ROW && block_b != FG_BLOCK_TILE)
+        return fail(FG_ERR_INVALID_ARG, 13, "unknown block kind %d", (int)block_b);
+    if (type_c != FG_TYPE_F32 && type_c != FG_TYPE_BF16)
+        return fail(FG_ERR_INVALID_ARG, 17, "type_c must be FG_TYPE_F32 or FG_TYPE_BF16");
+    const bool product = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    const bool tile = block_b == FG_BLOCK_TILE;
+    fg_status st;
+    if (product) {
+        if (!A) return fail(FG_ERR_INVALID_ARG, 5, "A is NULL");
+        if ((st = check_codes(A, lda, K, 5, "A")) != FG_OK) return st;
+        if ((st = check_scales(SA, ldsa, M, 7, "SA")) != FG_OK) return st;
+        if (!B) return fail(FG_ERR_INVALID_ARG, 9, "B is NULL");
+        if ((st = check_codes(B, ldb, K, 9, "B")) != FG_OK) return st;
+        if ((st = check_scales(SB, ldsb, tile ? cdiv(N, 128) : N, 11, "SB")) != FG_OK) return st;
+    }
+    if (M > 0 && N > 0) {
+        if (!C) return fail(FG_ERR_INVALID_ARG, 15, "C is NULL");
+        if (!aligned(C, (uintptr_t)type_size(type_c)))
+            return fail(FG_ERR_INVALID_ARG, 15, "C is not aligned to its type");
+    }
+    if (ldc < std::max<int64_t>(1, N))
+        return fail(FG_ERR_INVALID_ARG, 16, "ldc=%lld < N=%lld", (long long)ldc, (long long)N);
+    if (workspace && !aligned(workspace, 16))
+        return fail(FG_ERR_INVALID_ARG, 18, "workspace is not 16-byte aligned");
+    if (M > kMaxDim || N > kMaxDim)
+        return fail(FG_ERR_UNSUPPORTED, 0, "M and N are limited to 2^30");
+    if (ldc > FG_MAX_LD) return fail(FG_ERR_UNSUPPORTED, 16, "ldc above FG_MAX_LD");
+    if (M == 0 || N == 0) return FG_OK;
+    if (!product && beta == 1.0f) return FG_OK;
+
+    fg::Fp8Params p;
+    memset(&p, 0, sizeof p);
+    p.A = A;
+    p.B = B;
+    p.SA = SA;
+    p.SB = SB;
+    p.C = C;
+    p.lda = lda;
+    p.ldsa = ldsa;
+    p.ldb = ldb;
+    p.ldsb = ldsb;
+    p.ldc = ldc;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.K = (int32_t)K;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.c_bf16 = type_c == FG_TYPE_BF16;
+    p.vec_c = ldc % 4 == 0 && aligned(C, 4 * (uintptr_t)type_size(type_c));
+    if (!product) {
+        if ((st = check_device()) != FG_OK) return st;
+        p.alpha = 0.f;
+        return launched(fg::launch_fp8_finish(p, stream), "scaling kernel");
+    }
+    const Plan plan = plan_gemm(M, N, K, workspace ? workspace_bytes : 0);
+    const fg::Fp8Shape s = fg::fp8_shape(plan.shape);
+    if (cdiv(M, s.bm) * cdiv(N, s.bn) > 0x7FFFFFFFll)
+        return fail(FG_ERR_UNSUPPORTED, 0, "more than 2^31 - 1 output tiles");
+    if ((st = check_device()) != FG_OK) return st;
+    p.kb = (int32_t)cdiv(K, fg::kScaleBlock);
+    p.splits = (int32_t)plan.splits;
+    p.kb_per_split = (int32_t)cdiv(p.kb, plan.splits);
+    p.ws = static_cast<float*>(workspace);
+    st = launched(fg::launch_gemm_fp8(plan.shape, tile, p, stream), "fp8 product kernel");
+    if (st == FG_OK && p.splits > 1)
+        st = launched(fg::launch_fp8_finish(p, stream), "fp8 reduction kernel");
+    return st;
+}
+
+}  // extern "C"
+
+// ---- mixture-of-experts layer ------------------------------------------------
+
+namespace {
+
+int64_t round_up(int64_t v, int64_t a) { return cdiv(v, a) * a; }
+
+// Byte offsets of the workspace's parts: logits, then h (at most 6 bytes per
+// pair and inner element: three bfloat16 terms).
+size_t moe_logit_bytes(int64_t T, int64_t E) { return (size_t)round_up(T * E * 8, 256); }
+int64_t moe_h_ld(int64_t I) { return round_up(I, 16); }
+size_t moe_h_bytes(int64_t T, int64_t k, int64_t I) {
+    return (size_t)round_up(T * k * moe_h_ld(I) * 6, 256);
+}
+
+bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+    return T >= 0 && T <= FG_MOE_MAX_TOKENS && E >= 1 && E <= FG_MOE_MAX_EXPERTS && k >= 1 &&
+           k <= E && k <= FG_MOE_MAX_TOP_K && H >= 1 && H <= FG_MAX_LD && I >= 1 && I <= FG_MAX_LD;
+}
+
+fg_status check_experts(const fg_experts& m, int wtype, int64_t E, int64_t rows, int64_t cols,
+                        int arg, const char* name) {
+    const int64_t size = type_size(wtype);
+    if (!m.w) return fail(FG_ERR_INVALID_ARG, arg, "%s is NULL", name);
+    if (m.ld < cols || (E > 1 && m.stride < 0))
+        return fail(FG_ERR_INVALID_ARG, arg, "%s: leading dimension %lld < %lld, or a negative stride",
+                    name, (long long)m.ld, (long long)cols);
+    if (!aligned(m.w, 16) || m.ld * size % 16 || (E > 1 && m.stride * size % 16))
+        return fail(FG_ERR_INVALID_ARG, arg, "rows of %s must start at multiples of 16 bytes", name);
+    if (m.ld > FG_MAX_LD)
+        return fail(FG_ERR_UNSUPPORTED, arg, "leading dimension of %s above FG_MAX_LD", name);
+    if (wtype == FG_TYPE_E4M3) {
+        if (!m.scales || !aligned(m.scales, 4))
+            return fail(FG_ERR_INVALID_ARG, arg, "%s has no scales, or misaligned ones", name);
+        if (m.lds < cdiv(rows, 128) || (E > 1 && m.scale_stride < 0))
+            return fail(FG_ERR_INVALID_ARG, arg, "scales of %s: leading dimension %lld < %lld", name,
+                        (long long)m.lds, (long long)cdiv(rows, 128));
+    }
+    return FG_OK;
+}
+
+fg::ExpertMatrix expert_matrix(const fg_experts& m) {
+    return fg::ExpertMatrix{m.w, m.ld, m.stride, m.scales, m.lds, m.scale_stride};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fg_moe_workspace_size(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
+                             int32_t inner) {
+    if (!moe_sizes_ok(tokens, top_k, experts, hidden, inner)) return 0;
+    return moe_logit_bytes(tokens, experts) + moe_h_bytes(tokens, top_k, inner);
+}
+
+fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_bytes,
+                 hipStream_t stream) {
+    clear_error();
+    if (!layer) return fail(FG_ERR_INVALID_ARG, 1, "layer is NULL");
+    const fg_moe_layer& l = *layer;
+    if (l.tokens < 0 || l.tokens > FG_MOE_MAX_TOKENS)
+        return fail(FG_ERR_INVALID_ARG, 1, "tokens=%d outside 0 .. %d", l.tokens, FG_MOE_MAX_TOKENS);
+    if (l.experts < 1 || l.experts > FG_MOE_MAX_EXPERTS)
+        return fail(FG_ERR_INVALID_ARG, 2, "experts=%d outside 1 .. %d", l.experts,
+                    FG_MOE_MAX_EXPERTS);
+    if (l.top_k < 1 || l.top_k > l.experts || l.top_k > FG_MOE_MAX_TOP_K)
+        return fail(FG_ERR_INVALID_ARG, 3, "top_k=%d outside 1 .. min(experts, %d)", l.top_k,
+                    FG_MOE_MAX_TOP_K);
+    if (l.hidden < 1 || l.hidden > FG_MAX_LD)
+        return fail(FG_ERR_INVALID_ARG, 4, "hidden=%d outside 1 .. %d", l.hidden, FG_MAX_LD);
+    if (l.inner < 1 || l.inner > FG_MAX_LD)
+        return fail(FG_ERR_INVALID_ARG, 5, "inner=%d outside 1 .. %d", l.inner, FG_MAX_LD);
+    if (l.type != FG_TYPE_F32 && l.type != FG_TYPE_BF16)
+        return fail(FG_ERR_INVALID_ARG, 6, "type must be FG_TYPE_F32 or FG_TYPE_BF16");
+    if (l.weight_type != FG_TYPE_F32 && l.weight_type != FG_TYPE_BF16 &&
+        l.weight_type != FG_TYPE_E4M3)
+        return fail(FG_ERR_INVALID_ARG, 7, "unknown weight type %d", l.weight_type);
+    if (l.activation < FG_ACT_NONE || l.activation > FG_ACT_SILU)
+        return fail(FG_ERR_INVALID_ARG, 8, "unknown activation %d", l.activation);
+    if (l.renormalize != 0 && l.renormalize != 1)
+        return fail(FG_ERR_INVALID_ARG, 9, "renormalize must be 0 or 1");
+    const int64_t T = l.tokens, E = l.experts, H = l.hidden, I = l.inner;
+    const uintptr_t size = (uintptr_t)type_size(l.type);
+    if (T > 0 && (!l.x || !aligned(l.x, size)))
+        return fail(FG_ERR_INVALID_ARG, 10, "x is NULL or misaligned");
+    if (l.ldx < H) return fail(FG_ERR_INVALID_ARG, 11, "ldx=%lld < hidden", (long long)l.ldx);
+    fg_status st;
+    if (T > 0) {
+        if ((st = check_experts(l.gate, l.weight_type, E, I, H, 12, "gate")) != FG_OK) return st;
+        if ((st = check_experts(l.up, l.weight_type, E, I, H, 13, "up")) != FG_OK) return st;
+        if ((st = check_experts(l.down, l.weight_type, E, H, I, 14, "down")) != FG_OK) return st;
+    }
+    if (l.router) {
+        if (l.router_type != FG_TYPE_F32 && l.router_type != FG_TYPE_BF16)
+            return fail(FG_ERR_INVALID_ARG, 17, "router_type must be FG_TYPE_F32 or FG_TYPE_BF16");
+        if (!aligned(l.router, (uintptr_t)type_size(l.router_type)))
+            return fail(FG_ERR_INVALID_ARG, 15, "router is misaligned");
+        if (l.ldr < H) return fail(FG_ERR_INVALID_ARG, 16, "ldr=%lld < hidden", (long long)l.ldr);
+    }
+    if (T > 0 && (!l.ids || !aligned(l.ids, 4)))
+        return fail(FG_ERR_INVALID_ARG, 18, "ids is NULL or misaligned");
+    if (T > 0 && (!l.weights || !aligned(l.weights, 4)))
+        return fail(FG_ERR_INVALID_ARG, 19, "weights is NULL or misaligned");
+    if (T > 0 && (!l.out || !aligned(l.out, size)))
+        return fail(FG_ERR_INVALID_ARG, 20, "out is NULL or misaligned");
+    if (l.ldo < H) return fail(FG_ERR_INVALID_ARG, 21, "ldo=%lld < hidden", (long long)l.ldo);
+    if (T == 0) return FG_OK;
+    if (!workspace || !aligned(workspace, 16))
+        return fail(FG_ERR_INVALID_ARG, 22, "workspace is NULL or not 16-byte aligned");
+    const size_t need = fg_moe_workspace_size(l.tokens, l.top_k, l.experts, l.hidden, l.inner);
+    if (workspace_bytes < need)
+        return fail(FG_ERR_INVALID_ARG, 23, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+    if ((st = check_device()) != FG_OK) return st;
+
+    fg::MoeParams p;
+    memset(&p, 0, sizeof p);
+    p.T = l.tokens;
+    p.E = l.experts;
+    p.k = l.top_k;
+    p.H = l.hidden;
+    p.I = l.inner;
+    p.x_bf16 = l.type == FG_TYPE_BF16;
+    p.wtype = l.weight_type;
+    p.act = l.activation;
+    p.renorm = l.renormalize;
+    p.vec_x = aligned(l.x, 16) && l.ldx * (int64_t)size % 16 == 0;
+    p.x = l.x;
+    p.ldx = l.ldx;
+    p.gate = expert_matrix(l.gate);
+    p.up = expert_matrix(l.up);
+    p.down = expert_matrix(l.down);
+    p.router = l.router;
+    p.ldr = l.ldr;
+    p.router_bf16 = l.router_type == FG_TYPE_BF16;
+    p.vec_r = l.router && aligned(l.router, 16) && l.ldr * type_size(l.router_type) % 16 == 0;
+    p.ids = l.ids;
+    p.weights = l.weights;
+    p.out = l.out;
+    p.ldo = l.ldo;
+    p.logits = static_cast<double*>(workspace);
+    p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + moe_logit_bytes(T, E));
+    p.h_ld = (int32_t)moe_h_ld(I);
+    p.h_plane = T * l.top_k * moe_h_ld(I);
+    if (l.router && (st = launched(fg::launch_moe_route(p, stream), "router kernel")) != FG_OK)
+        return st;
+    return launched(fg::launch_moe_experts(p, stream), "expert kernel");
+}
+
+}  // extern "C"
