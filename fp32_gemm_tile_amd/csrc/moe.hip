@@ -422,24 +422,60 @@ __global__ void __launch_bounds__(64) topk_kernel(MoeParams p) {
 
 // ---- experts ---------------------------------------------------------------
 
-// The chosen experts as a bit set in LDS, from the ids (at most 1024).
-__device__ __forceinline__ void mark_experts(const MoeParams& p, const int* ids, uint32_t* bits) {
+// The ids in LDS and the chosen experts as a bit set (two barriers).
+__device__ __forceinline__ void mark_experts(const MoeParams& p, int* ids, uint32_t* bits) {
+    const int n = p.T * p.k;
+    const int first = (int)threadIdx.x < n ? p.ids[threadIdx.x] : -1;  // in flight over the barrier
     for (int i = threadIdx.x; i < kMaxE / 32; i += blockDim.x) bits[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) {
-        const int e = ids[i];
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int e = i < (int)blockDim.x ? first : p.ids[i];
+        ids[i] = e;
         if (e >= 0 && e < p.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
 }
 
+// Chosen experts before word `lane` of the bit set (lanes 0 .. 15), and how
+// many there are, from the words' own counts.
+__device__ __forceinline__ int experts_before(const uint32_t* bits, int lane, int& total) {
+    int own = lane < kMaxE / 32 ? __popc(bits[lane]) : 0, sum = own;
+#pragma unroll
+    for (int o = 1; o < kMaxE / 32; o <<= 1) {
+        const int v = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += v;
+    }
+    total = __shfl(sum, kMaxE / 32 - 1, 64);
+    return sum - own;
+}
+
+// The y-th chosen expert in ascending order, or -1 (the whole wave takes part).
+__device__ __forceinline__ int nth_expert(const uint32_t* bits, int lane, int y) {
+    int total;
+    const int before = experts_before(bits, lane, total);
+    int found = -1;
+    if (lane < kMaxE / 32) {
+        uint32_t w = bits[lane];
+        const int skip = y - before;
+        if (skip >= 0 && skip < __popc(w)) {
+            for (int i = 0; i < skip; ++i) w &= w - 1;
+            found = lane * 32 + __ffs(w) - 1;
+        }
+    }
+    const uint64_t m = __ballot(found >= 0);
+    return m ? __builtin_amdgcn_readfirstlane(__shfl(found, __ffsll((unsigned long long)m) - 1, 64))
+             : -1;
+}
+
 // The tokens that chose expert e: this lane's token (lane < T), whether it
-// did, the first of its slots that did, and the sum of those slots' weights.
+// did, the first of its slots that did, and (weights) the sum of those slots'
+// weights.
 struct Chosen {
     bool have;
     int pair;
     float weight;
 };
+template <bool WEIGHTS>
 __device__ __forceinline__ Chosen chosen_by(const MoeParams& p, const int* ids, int lane, int e) {
     Chosen c{false, 0, 0.f};
     if (lane < p.T)
@@ -447,131 +483,207 @@ __device__ __forceinline__ Chosen chosen_by(const MoeParams& p, const int* ids, 
             if (ids[lane * p.k + s] == e) {
                 c.have = true;
                 c.pair = lane * p.k + s;
-                c.weight += p.weights[lane * p.k + s];
+                if (WEIGHTS) c.weight += p.weights[lane * p.k + s];
             }
     return c;
 }
 
-constexpr int kGuWaves = 8;
+// Orders one wave's LDS accesses across its lanes.
+__device__ __forceinline__ void wave_lds_sync() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
 
-template <int WT, bool XBF16>
-__global__ void __launch_bounds__(64 * kGuWaves) gate_up_kernel(MoeParams p) {
+// gate and up: RT x 16 inner rows of one expert per workgroup, NW waves
+// splitting K. Each wave keeps the weights of its next step in flight while it
+// uses the present ones.
+template <int WT, bool XBF16, int RT, int NW>
+struct GateUp {
+    static constexpr int kStreams = 2 * RT;  // gate and up of each row tile
     using W = Weight<WT>;
-    constexpr int NP = XBF16 ? 2 : 3;
-    __shared__ int ids[kMaxT * kMaxK];
-    __shared__ uint32_t bits[kMaxE / 32];
-    __shared__ int tok[kMaxT], pair[kMaxT];
-    __shared__ int s_expert, s_count;
-    __shared__ __attribute__((aligned(16))) f4 red[kGuWaves][2][64];
+    const MoeParams& p;
+    const int lane, wave, n16, g, row0, steps;
+    const uint8_t* w[kStreams];
+    const float* s[kStreams];
 
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n16 = lane & 15, g = lane >> 4;
-    const int row0 = blockIdx.x * 16;
-    for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) ids[i] = p.ids[i];
-    if (threadIdx.x == 0) s_expert = -1;
-    mark_experts(p, ids, bits);
-    // the blockIdx.y-th chosen expert
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        if (bits[e >> 5] >> (e & 31) & 1) {
-            int before = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1u));
-            for (int w = 0; w < (e >> 5); ++w) before += __popc(bits[w]);
-            if (before == (int)blockIdx.y) s_expert = e;
-        }
-    }
-    __syncthreads();
-    const int e = s_expert;
-    if (e < 0) return;
-    if (wave == 0) {
-        const Chosen c = chosen_by(p, ids, lane, e);
-        const uint64_t m = __ballot(c.have);
-        if (c.have) {
-            const int at = __popcll(m & ((1ull << lane) - 1ull));
-            tok[at] = lane;
-            pair[at] = c.pair;
-        }
-        if (lane == 0) s_count = __popcll(m);
-    }
-    __syncthreads();
-    const int count = s_count;
-
-    // weight row of this lane (rows past I read the last one; not stored)
-    const int row = row0 + n16 < p.I ? row0 + n16 : p.I - 1;
-    const uint8_t* const wg = static_cast<const uint8_t*>(p.gate.w) +
-                              (e * p.gate.stride + row * p.gate.ld) * W::kSize;
-    const uint8_t* const wu =
-        static_cast<const uint8_t*>(p.up.w) + (e * p.up.stride + row * p.up.ld) * W::kSize;
-    const float* sg = WT == TYPE_E4M3 ? p.gate.s + e * p.gate.s_stride + (row0 >> 7) : nullptr;
-    const float* su = WT == TYPE_E4M3 ? p.up.s + e * p.up.s_stride + (row0 >> 7) : nullptr;
-    const int steps = (p.H + 127) / 128;
-
-    for (int c0 = 0; c0 < count; c0 += 16) {
-        const bool have = c0 + n16 < count;
-        const void* const x = static_cast<const uint8_t*>(p.x) +
-                              (have ? tok[c0 + n16] : 0) * p.ldx * (XBF16 ? 2 : 4);
-        f4 ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
-        for (int kb = wave; kb < steps; kb += kGuWaves) {
-            WeightStep<WT> a, b;
-            a.load(wg, kb * 128, p.H, g);
-            b.load(wu, kb * 128, p.H, g);
-            XStep<WT, XBF16> xs;
-            xs.load(x, have, kb * 128, p.H, p.vec_x, g);
-            if constexpr (WT == TYPE_E4M3) {
-                const f4 z = {0.f, 0.f, 0.f, 0.f};
-                const f4 tg = xs.times(a, z), tu = xs.times(b, z);
-                const float fg = sg[kb * p.gate.lds], fu = su[kb * p.up.lds];
+    __device__ __forceinline__ GateUp(const MoeParams& p, int e, int row0)
+        : p(p), lane(threadIdx.x & 63),
+          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), n16(lane & 15), g(lane >> 4),
+          row0(row0), steps((p.H + 127) / 128) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ag[i] = fmaf(fg, tg[i], ag[i]);
-                    au[i] = fmaf(fu, tu[i], au[i]);
-                }
-            } else {
-                ag = xs.times(a, ag);
-                au = xs.times(b, au);
+        for (int r = 0; r < RT; ++r) {
+            // (rows past I read the last one; their h is 0 or not stored)
+            const int first = row0 + 16 * r < p.I ? row0 + 16 * r : p.I - 1;
+            const int row = first + n16 < p.I ? first + n16 : p.I - 1;
+            w[2 * r] = static_cast<const uint8_t*>(p.gate.w) +
+                       (e * p.gate.stride + row * p.gate.ld) * W::kSize;
+            w[2 * r + 1] = static_cast<const uint8_t*>(p.up.w) +
+                           (e * p.up.stride + row * p.up.ld) * W::kSize;
+            if (WT == TYPE_E4M3) {
+                s[2 * r] = p.gate.s + e * p.gate.s_stride + (first >> 7);
+                s[2 * r + 1] = p.up.s + e * p.up.s_stride + (first >> 7);
             }
         }
-        red[wave][0][lane] = ag;
-        red[wave][1][lane] = au;
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            const int r = wave;  // component: inner row row0 + 4 g + r
-            float gs = 0.f, us = 0.f;
-            for (int w = 0; w < kGuWaves; ++w) {
-                gs += red[w][0][lane][r];
-                us += red[w][1][lane][r];
-            }
-            if (have) {
-                const int i = row0 + 4 * g + r;
-                const float h = i < p.I ? act_exact(gs, p.act) * us : 0.f;
-                const int64_t at = (int64_t)pair[c0 + n16] * p.h_ld + i;
-                if constexpr (WT == TYPE_F32) {
-                    reinterpret_cast<float*>(p.h)[at] = h;
-                } else {
-                    float left = h;
+    }
+
+    __device__ __forceinline__ void fetch(WeightStep<WT> (&v)[kStreams], int kb) const {
+        if (kb >= steps) return;
 #pragma unroll
-                    for (int s = 0; s < NP; ++s) {
-                        const __bf16 b = (__bf16)left;
-                        p.h[s * p.h_plane + at] = __builtin_bit_cast(uint16_t, b);
-                        left -= (float)b;
-                        if (s == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
+        for (int i = 0; i < kStreams; ++i) v[i].load(w[i], kb * 128, p.H, g);
+    }
+
+    // NT groups of 16 tokens (tok: their indices, `count` of them)
+    template <int NT>
+    __device__ __forceinline__ void sums(const int* tok, int count, f4 (&acc)[NT][kStreams]) const {
+        const void* x[NT];
+        bool have[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            have[t] = 16 * t + n16 < count;
+            x[t] = static_cast<const uint8_t*>(p.x) +
+                   (have[t] ? tok[16 * t + n16] : 0) * p.ldx * (XBF16 ? 2 : 4);
+#pragma unroll
+            for (int i = 0; i < kStreams; ++i) acc[t][i] = f4{0.f, 0.f, 0.f, 0.f};
+        }
+        auto use = [&](const WeightStep<WT>(&v)[kStreams], int kb) {
+            float f[kStreams];
+#pragma unroll
+            for (int i = 0; i < kStreams; ++i)
+                f[i] = WT == TYPE_E4M3 ? s[i][kb * (i & 1 ? p.up.lds : p.gate.lds)] : 1.f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                XStep<WT, XBF16> xs;
+                xs.load(x[t], have[t], kb * 128, p.H, p.vec_x, g);
+#pragma unroll
+                for (int i = 0; i < kStreams; ++i) {
+                    if constexpr (WT == TYPE_E4M3) {
+                        const f4 b = xs.times(v[i], f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[t][i][e] = fmaf(f[i], b[e], acc[t][i][e]);
+                    } else {
+                        acc[t][i] = xs.times(v[i], acc[t][i]);
                     }
                 }
             }
+        };
+        if constexpr (NT > 2) {  // (many tokens: no registers for a second step)
+            for (int kb = wave; kb < steps; kb += NW) {
+                WeightStep<WT> v[kStreams];
+                fetch(v, kb);
+                use(v, kb);
+            }
+            return;
         }
-        __syncthreads();
+        WeightStep<WT> v0[kStreams], v1[kStreams];
+        fetch(v0, wave);
+        for (int kb = wave; kb < steps; kb += 2 * NW) {
+            fetch(v1, kb + NW);
+            use(v0, kb);
+            if (kb + NW >= steps) break;
+            fetch(v0, kb + 2 * NW);
+            use(v1, kb + NW);
+        }
+    }
+
+    // Joins the waves' sums in wave order and stores h of the groups.
+    template <int NT>
+    __device__ __forceinline__ void finish(const int* pair, int count, f4 (&acc)[NT][kStreams],
+                                           f4 (*red)[2][64]) const {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                red[wave][0][lane] = acc[t][2 * r];
+                red[wave][1][lane] = acc[t][2 * r + 1];
+                __syncthreads();
+                if (threadIdx.x < 256) {
+                    float gs = 0.f, us = 0.f;  // component `wave` of the four
+                    for (int v = 0; v < NW; ++v) {
+                        gs += red[v][0][lane][wave];
+                        us += red[v][1][lane][wave];
+                    }
+                    const int i = row0 + 16 * r + 4 * g + wave;
+                    if (16 * t + n16 < count && i < p.h_ld)
+                        store_h(pair[16 * t + n16], i, i < p.I ? act_exact(gs, p.act) * us : 0.f);
+                }
+                __syncthreads();
+            }
+    }
+
+    __device__ __forceinline__ void store_h(int pair, int i, float h) const {
+        const int64_t at = (int64_t)pair * p.h_ld + i;
+        if constexpr (WT == TYPE_F32) {
+            reinterpret_cast<float*>(p.h)[at] = h;
+        } else {
+            float left = h;
+#pragma unroll
+            for (int s = 0; s < (XBF16 ? 2 : 3); ++s) {
+                const __bf16 b = (__bf16)left;
+                p.h[s * p.h_plane + at] = __builtin_bit_cast(uint16_t, b);
+                left -= (float)b;
+                if (s == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
+            }
+        }
+    }
+
+    template <int NT>
+    __device__ __forceinline__ void run(const int* tok, const int* pair, int count,
+                                        f4 (*red)[2][64]) const {
+        f4 acc[NT][kStreams];
+        sums<NT>(tok, count, acc);
+        finish<NT>(pair, count, acc, red);
+    }
+};
+
+template <int WT, bool XBF16, int RT, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) gate_up_kernel(MoeParams p) {
+    static_assert(NW >= 4, "the joining of the waves' sums takes 256 threads");
+    __shared__ int ids[kMaxT * kMaxK];
+    __shared__ uint32_t bits[kMaxE / 32];
+    __shared__ int tok[NW][kMaxT], pair[NW][kMaxT];
+    __shared__ __attribute__((aligned(16))) f4 red[NW][2][64];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    mark_experts(p, ids, bits);
+    const int e = nth_expert(bits, lane, blockIdx.y);
+    if (e < 0) return;
+    // every wave makes its own copy of the expert's list: no barrier
+    const Chosen c = chosen_by<false>(p, ids, lane, e);
+    const uint64_t m = __ballot(c.have);
+    const int count = __popcll(m);
+    if (c.have) {
+        const int at = __popcll(m & ((1ull << lane) - 1ull));
+        tok[wave][at] = lane;
+        pair[wave][at] = c.pair;
+    }
+    wave_lds_sync();
+    const GateUp<WT, XBF16, RT, NW> gu(p, e, blockIdx.x * 16 * RT);
+    // (binary32 x by 32 rows: four groups of tokens do not fit the registers,
+    // and the second pass over the weights mostly hits the L2)
+    constexpr int kMost = !XBF16 && RT > 1 ? 2 : 4;
+    if (count <= 16) {
+        gu.template run<1>(tok[wave], pair[wave], count, red);
+    } else if (count <= 32) {
+        gu.template run<2>(tok[wave], pair[wave], count, red);
+    } else {
+        for (int c0 = 0; c0 < count; c0 += 16 * kMost)
+            gu.template run<kMost>(tok[wave] + c0, pair[wave] + c0, count - c0, red);
     }
 }
 
+// down: 16 output rows per workgroup. The (expert, block of K) units of all
+// chosen experts are dealt to the waves in contiguous runs; a wave keeps the
+// weights of its next D units in flight, over the border of two experts too.
 constexpr int kDownWaves = 8;
 
 template <int WT, bool XBF16>
 __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeParams p) {
     using W = Weight<WT>;
     constexpr int NP = XBF16 ? 2 : 3;
+    constexpr int D = WT == TYPE_E4M3 ? 4 : 2;
     __shared__ int ids[kMaxT * kMaxK];
     __shared__ uint32_t bits[kMaxE / 32];
     __shared__ int active[kMaxE];
-    __shared__ int s_n;
     __shared__ int tok[kDownWaves][kMaxT], pair[kDownWaves][kMaxT];
     __shared__ float wt[kDownWaves][kMaxT];
     __shared__ float sum[kDownWaves][kMaxT][16];
@@ -580,92 +692,117 @@ __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, g = lane >> 4;
     const int row0 = blockIdx.x * 16;
-    for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) ids[i] = p.ids[i];
-    for (int i = lane; i < p.T * 16; i += 64) sum[wave][i >> 4][i & 15] = 0.f;
     mark_experts(p, ids, bits);
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        if (bits[e >> 5] >> (e & 31) & 1) {
-            int before = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1u));
-            for (int w = 0; w < (e >> 5); ++w) before += __popc(bits[w]);
-            active[before] = e;
-        }
+    int chosen;
+    {
+        int before = experts_before(bits, lane, chosen);
+        if (wave == 0 && lane < kMaxE / 32)
+            for (uint32_t w = bits[lane]; w; w &= w - 1) active[before++] = lane * 32 + __ffs(w) - 1;
     }
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < kMaxE / 32; ++w) n += __popc(bits[w]);
-        s_n = n;
-    }
+    for (int i = lane; i < p.T * 16; i += 64) sum[wave][i >> 4][i & 15] = 0.f;
     __syncthreads();
     const int steps = (p.I + 127) / 128;
-    const int64_t units = (int64_t)s_n * steps;
-    const int K16 = (p.I + 15) & ~15;
-    int64_t u = units * wave / kDownWaves;
-    const int64_t u1 = units * (wave + 1) / kDownWaves;
+    const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(chosen) * steps;
+    const int K16 = p.h_ld;
+    const int64_t u0 = units * wave / kDownWaves, u1 = units * (wave + 1) / kDownWaves;
     const int row = row0 + n16 < p.H ? row0 + n16 : p.H - 1;
-    while (u < u1) {
-        const int a = (int)(u / steps);
-        const int kb0 = (int)(u - (int64_t)a * steps);
-        const int kb1 = u1 - u < steps - kb0 ? kb0 + (int)(u1 - u) : steps;
-        u += kb1 - kb0;
-        const int e = active[a];
-        const Chosen c = chosen_by(p, ids, lane, e);
-        const uint64_t m = __ballot(c.have);
-        const int count = __popcll(m);
-        if (c.have) {
-            const int at = __popcll(m & ((1ull << lane) - 1ull));
-            tok[wave][at] = lane;
-            pair[wave][at] = c.pair;
-            wt[wave][at] = c.weight;
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's own LDS lists
-        const uint8_t* const w =
-            static_cast<const uint8_t*>(p.down.w) + (e * p.down.stride + row * p.down.ld) * W::kSize;
-        const float* const sw =
-            WT == TYPE_E4M3 ? p.down.s + e * p.down.s_stride + (row0 >> 7) : nullptr;
-        for (int c0 = 0; c0 < count; c0 += 16) {
-            const bool have = c0 + n16 < count;
-            const int pr = have ? pair[wave][c0 + n16] : 0;
-            f4 acc = {0.f, 0.f, 0.f, 0.f};
-            for (int kb = kb0; kb < kb1; ++kb) {
-                WeightStep<WT> b;
-                b.load(w, kb * 128, p.I, g);
-                HStep<WT, NP> hs;
-                hs.load(p, pr, have, kb * 128, K16, g);
-                if constexpr (WT == TYPE_E4M3) {
-                    const f4 t = hs.times(b, f4{0.f, 0.f, 0.f, 0.f});
-                    const float f = sw[kb * p.down.lds];
+    const uint8_t* const w0 = static_cast<const uint8_t*>(p.down.w) + row * p.down.ld * W::kSize;
+
+    // the unit to fetch next and the one to use next
+    int fa = (int)(u0 / steps), fk = (int)(u0 - (int64_t)fa * steps);
+    int ua = fa, uk = fk;
+    auto fetch = [&](WeightStep<WT>& v) {
+        const int e = __builtin_amdgcn_readfirstlane(active[fa]);
+        v.load(w0 + e * p.down.stride * W::kSize, fk * 128, p.I, g);
+        if (++fk == steps) fk = 0, ++fa;
+    };
+    f4 acc[4];
+    int count = 0;
+    const float* sw = nullptr;
+    auto flush = [&] {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, t[i], acc[i]);
-                } else {
-                    acc = hs.times(b, acc);
-                }
-            }
-            if (have) {
-                const int t = tok[wave][c0 + n16];
-                const float f = wt[wave][c0 + n16];
+        for (int t = 0; t < 4; ++t)
+            if (16 * t + n16 < count) {
+                const int at = tok[wave][16 * t + n16];
+                const float f = wt[wave][16 * t + n16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[wave][t][4 * g + i] += f * acc[i];
+                for (int i = 0; i < 4; ++i) sum[wave][at][4 * g + i] += f * acc[t][i];
+            }
+    };
+    auto use = [&](const WeightStep<WT>& v, bool first) {
+        if (first || uk == 0) {
+            flush();
+            wave_lds_sync();
+            const int e = __builtin_amdgcn_readfirstlane(active[ua]);
+            const Chosen c = chosen_by<true>(p, ids, lane, e);
+            const uint64_t m = __ballot(c.have);
+            count = __popcll(m);
+            if (c.have) {
+                const int at = __popcll(m & ((1ull << lane) - 1ull));
+                tok[wave][at] = lane;
+                pair[wave][at] = c.pair;
+                wt[wave][at] = c.weight;
+            }
+            wave_lds_sync();
+            if (WT == TYPE_E4M3) sw = p.down.s + e * p.down.s_stride + (row0 >> 7);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+        }
+        const float f = WT == TYPE_E4M3 ? sw[uk * p.down.lds] : 1.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (16 * t >= count) break;
+            const bool have = 16 * t + n16 < count;
+            HStep<WT, NP> hs;
+            hs.load(p, have ? pair[wave][16 * t + n16] : 0, have, uk * 128, K16, g);
+            if constexpr (WT == TYPE_E4M3) {
+                const f4 b = hs.times(v, f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(f, b[i], acc[t][i]);
+            } else {
+                acc[t] = hs.times(v, acc[t]);
             }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // before the lists are rewritten
+        if (++uk == steps) uk = 0, ++ua;
+    };
+    WeightStep<WT> v[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (u0 + d < u1) fetch(v[d]);
+    for (int64_t u = u0; u < u1; u += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (u + d < u1) use(v[d], u + d == u0);
+            if (u + d + D < u1) fetch(v[d]);
+        }
     }
+    flush();
     __syncthreads();
     for (int i = threadIdx.x; i < p.T * 16; i += blockDim.x) {
         const int t = i >> 4, n = i & 15;
         if (row0 + n >= p.H) continue;
-        float v = 0.f;
-        for (int w = 0; w < kDownWaves; ++w) v += sum[w][t][n];
+        float s = 0.f;
+        for (int w = 0; w < kDownWaves; ++w) s += sum[w][t][n];
         const int64_t at = (int64_t)t * p.ldo + row0 + n;
-        if (XBF16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)bf16_code(v);
-        else static_cast<float*>(p.out)[at] = v;
+        if (XBF16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)bf16_code(s);
+        else static_cast<float*>(p.out)[at] = s;
     }
 }
 
 template <int WT, bool XBF16>
 hipError_t launch_experts(const MoeParams& p, hipStream_t stream) {
     const int most = p.E < p.T * p.k ? p.E : p.T * p.k;
-    hipLaunchKernelGGL((gate_up_kernel<WT, XBF16>), dim3((p.I + 15) / 16, most),
-                       dim3(64 * kGuWaves), 0, stream, p);
+    // Two workgroups of 4 waves on a CU, so that one streams while the other
+    // finds its expert; 8 waves while that leaves CUs idle. 32 inner rows per
+    // workgroup where the weights of two steps fit the registers.
+    constexpr int RT = WT == TYPE_F32 ? 1 : 2;
+    const int tiles = (p.I + 16 * RT - 1) / (16 * RT);
+    if ((int64_t)tiles * most >= 512)
+        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, RT, 4>), dim3(tiles, most), dim3(256), 0,
+                           stream, p);
+    else
+        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, 1, 8>), dim3((p.I + 15) / 16, most),
+                           dim3(512), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((down_kernel<WT, XBF16>), dim3((p.H + 15) / 16), dim3(64 * kDownWaves), 0,
