@@ -227,17 +227,44 @@ namespace {
 
 int64_t round_up(int64_t v, int64_t a) { return cdiv(v, a) * a; }
 
-// Byte offsets of the workspace's parts: logits, then h (at most 6 bytes per
-// pair and inner element: three bfloat16 terms).
-size_t moe_logit_bytes(int64_t T, int64_t E) { return (size_t)round_up(T * E * 8, 256); }
 int64_t moe_h_ld(int64_t I) { return round_up(I, 16); }
-size_t moe_h_bytes(int64_t T, int64_t k, int64_t I) {
-    return (size_t)round_up(T * k * moe_h_ld(I) * 6, 256);
+int64_t moe_xs_ld(int64_t H) { return round_up(H, fg::kScaleBlock); }
+
+// Groups of G tokens: no more than pairs, and no more than one partial group
+// per expert.
+int64_t most_groups(int64_t T, int64_t k, int64_t E, int64_t G) {
+    return std::min(T * k, T <= G ? E : E + T * k / G);
 }
+
+// Offsets of the workspace's parts, for any types (h and x: at most three
+// bfloat16 terms; groups of at least five tokens).
+struct MoeSpace {
+    size_t plan, logits, groups_x, groups_h, tickets, pieces, h, xs, end;
+    MoeSpace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+        size_t at = 0;
+        auto take = [&](int64_t bytes) {
+            const size_t here = at;
+            at += (size_t)round_up(bytes, 256);
+            return here;
+        };
+        const int64_t groups = most_groups(T, k, E, 5);
+        plan = take(sizeof(fg::MoePlan));
+        logits = take(T * E * 8);
+        groups_x = take(groups * (int64_t)sizeof(fg::MoeGroup));
+        groups_h = take(groups * (int64_t)sizeof(fg::MoeGroup));
+        tickets = take(cdiv(H, 16) * 4);
+        pieces = take(round_up(H, 32) * 4 * T *
+                      fg::moe_down_workgroups(fg::TYPE_E4M3, (int)H, (int)I, (int)groups));
+        h = take(T * k * moe_h_ld(I) * 6);
+        xs = take(T * moe_xs_ld(H) * 6);
+        end = at;
+    }
+};
 
 bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     return T >= 0 && T <= FG_MOE_MAX_TOKENS && E >= 1 && E <= FG_MOE_MAX_EXPERTS && k >= 1 &&
-           k <= E && k <= FG_MOE_MAX_TOP_K && H >= 1 && H <= FG_MAX_LD && I >= 1 && I <= FG_MAX_LD;
+           k <= E && k <= FG_MOE_MAX_TOP_K && H >= 1 && H <= FG_MOE_MAX_DIM && I >= 1 &&
+           I <= FG_MOE_MAX_DIM;
 }
 
 fg_status check_experts(const fg_experts& m, int wtype, int64_t E, int64_t rows, int64_t cols,
@@ -272,7 +299,7 @@ extern "C" {
 size_t fg_moe_workspace_size(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
                              int32_t inner) {
     if (!moe_sizes_ok(tokens, top_k, experts, hidden, inner)) return 0;
-    return moe_logit_bytes(tokens, experts) + moe_h_bytes(tokens, top_k, inner);
+    return MoeSpace(tokens, top_k, experts, hidden, inner).end;
 }
 
 fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_bytes,
@@ -288,10 +315,10 @@ fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_by
     if (l.top_k < 1 || l.top_k > l.experts || l.top_k > FG_MOE_MAX_TOP_K)
         return fail(FG_ERR_INVALID_ARG, 3, "top_k=%d outside 1 .. min(experts, %d)", l.top_k,
                     FG_MOE_MAX_TOP_K);
-    if (l.hidden < 1 || l.hidden > FG_MAX_LD)
-        return fail(FG_ERR_INVALID_ARG, 4, "hidden=%d outside 1 .. %d", l.hidden, FG_MAX_LD);
-    if (l.inner < 1 || l.inner > FG_MAX_LD)
-        return fail(FG_ERR_INVALID_ARG, 5, "inner=%d outside 1 .. %d", l.inner, FG_MAX_LD);
+    if (l.hidden < 1 || l.hidden > FG_MOE_MAX_DIM)
+        return fail(FG_ERR_INVALID_ARG, 4, "hidden=%d outside 1 .. %d", l.hidden, FG_MOE_MAX_DIM);
+    if (l.inner < 1 || l.inner > FG_MOE_MAX_DIM)
+        return fail(FG_ERR_INVALID_ARG, 5, "inner=%d outside 1 .. %d", l.inner, FG_MOE_MAX_DIM);
     if (l.type != FG_TYPE_F32 && l.type != FG_TYPE_BF16)
         return fail(FG_ERR_INVALID_ARG, 6, "type must be FG_TYPE_F32 or FG_TYPE_BF16");
     if (l.weight_type != FG_TYPE_F32 && l.weight_type != FG_TYPE_BF16 &&
@@ -359,12 +386,46 @@ fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_by
     p.weights = l.weights;
     p.out = l.out;
     p.ldo = l.ldo;
-    p.logits = static_cast<double*>(workspace);
-    p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + moe_logit_bytes(T, E));
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    const MoeSpace space(T, l.top_k, E, H, I);
+    p.plan = reinterpret_cast<fg::MoePlan*>(ws + space.plan);
+    p.logits = reinterpret_cast<double*>(ws + space.logits);
+    p.tickets = reinterpret_cast<int32_t*>(ws + space.tickets);
+    p.pieces = reinterpret_cast<float*>(ws + space.pieces);
+    p.h = reinterpret_cast<uint16_t*>(ws + space.h);
+    const bool wide = p.wtype == fg::TYPE_F32;  // x and h stay binary32
     p.h_ld = (int32_t)moe_h_ld(I);
     p.h_plane = T * l.top_k * moe_h_ld(I);
-    if (l.router && (st = launched(fg::launch_moe_route(p, stream), "router kernel")) != FG_OK)
-        return st;
+    p.h_bytes = p.h_plane * (wide ? 4 : (p.x_bf16 ? 4 : 6));
+    // x is read in place where its rows are aligned and of the operands' type
+    const int64_t extent = ((T - 1) * l.ldx + H) * (int64_t)size;
+    if (p.vec_x && wide != (p.x_bf16 != 0) && (wide || p.x_bf16) && H % 8 == 0 &&
+        extent < (1ll << 31) && l.ldx <= FG_MAX_LD) {
+        p.xs = const_cast<void*>(l.x);
+        p.xs_ld = (int32_t)l.ldx;
+        p.xs_cols = (int32_t)H;
+        p.xs_bytes = extent;
+    } else {
+        p.xs = ws + space.xs;
+        p.xs_made = 1;
+        p.xs_ld = p.xs_cols = (int32_t)moe_xs_ld(H);
+        p.xs_plane = T * moe_xs_ld(H);
+        p.xs_bytes = p.xs_plane * (wide ? 4 : (p.x_bf16 ? 2 : 6));
+    }
+    // groups: as many tokens as fill 16 columns with the terms of x and of h
+    p.gx = fg::moe_group_size(wide || p.x_bf16 ? 1 : 3);
+    p.gh = fg::moe_group_size(wide ? 1 : (p.x_bf16 ? 2 : 3));
+    p.most_x = (int32_t)most_groups(T, l.top_k, E, p.gx);
+    p.most_h = (int32_t)most_groups(T, l.top_k, E, p.gh);
+    p.groups_x = reinterpret_cast<fg::MoeGroup*>(ws + space.groups_x);
+    p.groups_h =
+        p.gh == p.gx ? p.groups_x : reinterpret_cast<fg::MoeGroup*>(ws + space.groups_h);
+    p.down_wgs = fg::moe_down_workgroups(p.wtype, p.H, p.I, p.most_h);
+    if (l.router)
+        st = launched(fg::launch_moe_route(p, stream), "router kernel");
+    else
+        st = launched(fg::launch_moe_plan(p, stream), "kernel that groups the tokens");
+    if (st != FG_OK) return st;
     return launched(fg::launch_moe_experts(p, stream), "expert kernel");
 }
 

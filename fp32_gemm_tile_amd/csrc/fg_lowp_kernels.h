@@ -67,6 +67,19 @@ struct ExpertMatrix {
     const float* s;
     int64_t lds, s_stride;
 };
+// A group of tokens that share an expert: their pairs (token * k + first slot
+// that chose it) and weights (summed over the slots that did).
+struct MoeGroup {
+    int32_t expert, count;
+    int16_t pair[16];
+    float weight[16];
+    int32_t unused[2];  // (whole 16-byte pieces)
+};
+static_assert(sizeof(MoeGroup) == 112, "copied in 16-byte pieces");
+struct MoePlan {
+    int32_t total_x, total_h;  // groups in the two lists
+    int32_t ticket;            // top-k workgroups that have finished
+};
 struct MoeParams {
     int32_t T, E, k, H, I;
     int32_t x_bf16, wtype, act, renorm;
@@ -82,12 +95,34 @@ struct MoeParams {
     void* out;
     int64_t ldo;
     double* logits;             // T x E
-    uint16_t* h;                // act(gate x) * (up x) as bfloat16 terms: plane s,
-    int64_t h_plane;            // pair (token * k + slot), inner index
+    // act(gate x) * (up x) of pair (token * k + slot): rows of h_ld elements
+    // (zeros past I) in planes of bfloat16 terms, or binary32 for binary32 weights
+    uint16_t* h;
+    int64_t h_plane, h_bytes;
     int32_t h_ld;
+    // x as the experts' products read it: rows of xs_ld elements, xs_cols of them
+    // (a multiple of 8; zeros past H) valid, in planes of bfloat16 terms, or
+    // binary32 for binary32 weights. x itself, or made by the call (xs_made).
+    void* xs;
+    int64_t xs_plane, xs_bytes;
+    int32_t xs_ld, xs_cols, xs_made;
+    // The plan: groups of at most gx (for gate and up) and gh tokens (for down;
+    // the same list when gh == gx), and upper bounds on their numbers.
+    MoePlan* plan;
+    MoeGroup *groups_x, *groups_h;
+    int32_t gx, gh, most_x, most_h;
+    // down: workgroups per 16 output rows, which ones have finished, their pieces
+    int32_t down_wgs;
+    int32_t* tickets;
+    float* pieces;
 };
-int moe_planes(int x_bf16);     // bfloat16 terms that hold one value of h
+// Tokens in a group whose values have `terms` terms; workgroups per output tile.
+int moe_group_size(int terms);
+int moe_down_workgroups(int wtype, int H, int I, int most_groups);
+// Router logits, top-k and the plan; prepares x too when p.xs_made is set.
 hipError_t launch_moe_route(const MoeParams& p, hipStream_t stream);
+// The plan, and x (a call without a router).
+hipError_t launch_moe_plan(const MoeParams& p, hipStream_t stream);
 hipError_t launch_moe_experts(const MoeParams& p, hipStream_t stream);
 
 }  // namespace fg

@@ -3,22 +3,27 @@
 //
 //   route    logits = x R^T summed in binary64 (float products are exact
 //            there), so that experts with near logits are not exchanged;
-//   top-k    one wave per token;
-//   gate/up  one workgroup per 16 inner rows of one chosen expert: waves split
-//            K, sums joined in LDS in wave order, h = act(g) * u;
-//   down     one workgroup per 16 output rows and all chosen experts: waves
-//            split the (expert, block of K) pairs, each adds its weighted
-//            results to a private tokens x 16 piece in LDS, and the pieces are
-//            joined in wave order. No atomics: repeated calls are identical.
+//   top-k    one workgroup per token; the last one writes the plan: the groups
+//            of tokens that share an expert (a call without a router runs the
+//            plan alone);
+//   gate/up  one workgroup per 16 or 32 inner rows of one group: waves take
+//            the steps of K in turn, sums joined in wave order, h = act(g) * u;
+//   down     16 output rows and all groups per workgroup: waves take the
+//            (group, step) units in turn, each adds its weighted results to a
+//            private tokens x 16 piece in LDS, and the pieces are joined in
+//            wave order, those of several workgroups by the last to finish. No
+//            atomics on values: repeated calls are identical.
 //
 // The products run on v_mfma_f32_16x16x32_bf16 with the 16 weight rows as the
-// instruction's rows and the expert's tokens as its columns (padded to 16; the
-// matrix cores have time to spare). e4m3 and bfloat16 weights are exact in
-// bfloat16; a binary32 x or h is split into bfloat16 terms, x = hi + mid + lo,
-// which hold its 24 bits, so the products lose nothing. binary32 weights use
-// v_mfma_f32_16x16x4_f32. A lane owns 32 of the 128 k of a step; which ones
-// does not matter to the sum as long as both operands agree, so each weight
-// type takes the order in which 16 lanes' 16-byte loads cover whole sectors.
+// instruction's rows and the group's tokens as its columns. e4m3 and bfloat16
+// weights are exact in bfloat16; a binary32 x or h is split into bfloat16
+// terms, x = hi + mid + lo, which hold its 24 bits, so the products lose
+// nothing. binary32 weights use v_mfma_f32_16x16x4_f32. A lane owns 32 of the
+// 128 k of a step; which ones does not matter to the sum as long as both
+// operands agree, so each weight type takes the order in which 16 lanes'
+// 16-byte loads cover whole sectors.
+#include <algorithm>
+
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
 
@@ -102,33 +107,41 @@ struct Weight<TYPE_F32> {
     static __device__ __forceinline__ int first(int j, int g) { return j * 16 + g * 4; }
 };
 
-// A lane's 32 weights of one row in step [k0, k0 + 128); past K they are 0.
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer's end: reads as 0
+
+__device__ __forceinline__ i4v load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(i4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// A lane's 32 weights of one row in step kb. Every load of the loops below is
+// unconditional (past the row or the last step it reads nowhere), so that the
+// number of loads in flight is known at every point and a wait for one step
+// does not drain the next ones.
 template <int WT>
 struct WeightStep {
     i4v v[Weight<WT>::kPieces];
 
-    __device__ __forceinline__ void load(const uint8_t* row, int k0, int K, int g) {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int kb, int K,
+                                         int g) {
         using W = Weight<WT>;
-        const uint8_t* const at = row + (int64_t)k0 * W::kSize;
-        if (k0 + 128 <= K) {
 #pragma unroll
-            for (int j = 0; j < W::kPieces; ++j)
-                v[j] = *reinterpret_cast<const i4v*>(at + W::first(j, g) * W::kSize);
-        } else {
+        for (int j = 0; j < W::kPieces; ++j) {
+            const int k = kb * 128 + W::first(j, g);
+            v[j] = load16(r, k < K ? row + (uint32_t)(k * W::kSize) : kNowhere);
+        }
+    }
+    // clears what the last step's pieces hold past K
+    __device__ __forceinline__ void clear_tail(int kb, int K, int g) {
+        using W = Weight<WT>;
+        if (K - kb * 128 >= 128) return;
 #pragma unroll
-            for (int j = 0; j < W::kPieces; ++j) {
-                const int left = (K - k0 - W::first(j, g)) * W::kSize;  // bytes inside the row
-                v[j] = i4v{0, 0, 0, 0};
-                if (left > 0) {
-                    v[j] = *reinterpret_cast<const i4v*>(at + W::first(j, g) * W::kSize);
+        for (int j = 0; j < W::kPieces; ++j) {
+            const int left = (K - kb * 128 - W::first(j, g)) * W::kSize;  // bytes inside the row
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        const int n = left - 4 * d;
-                        const uint32_t m =
-                            n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
-                        v[j][d] &= (int)m;
-                    }
-                }
+            for (int d = 0; d < 4; ++d) {
+                const int n = left - 4 * d;
+                const uint32_t m = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+                v[j][d] &= (int)m;
             }
         }
     }
@@ -148,6 +161,69 @@ template <int WT>
 __device__ __forceinline__ int frag_first(int j, int g) {
     return WT == TYPE_E4M3 ? Weight<TYPE_E4M3>::first(j >> 1, g) + 8 * (j & 1)
                            : Weight<TYPE_BF16>::first(j, g);
+}
+
+// The other operand of one step: a lane's part of one term of a row of x or h,
+// bfloat16, or binary32 for binary32 weights. `cols` (a multiple of a piece)
+// bounds the row; what lies past the matrix's own columns in it is 0.
+template <int WT>
+struct TokenStep {
+    i4v t[4];
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int kb, int cols,
+                                         int g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = kb * 128 + frag_first<WT>(j, g);
+            t[j] = load16(r, row == kNowhere || k >= cols ? kNowhere : row + (uint32_t)k * 2u);
+        }
+    }
+    __device__ __forceinline__ f4 times(const WeightStep<WT>& w, f4 c) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = mfma_bf16(w.frag(j), __builtin_bit_cast(bf8, t[j]), c);
+        return c;
+    }
+};
+template <>
+struct TokenStep<TYPE_F32> {
+    i4v x[8];
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int kb, int cols,
+                                         int g) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = kb * 128 + Weight<TYPE_F32>::first(j, g);
+            x[j] = load16(r, row == kNowhere || k >= cols ? kNowhere : row + (uint32_t)k * 4u);
+        }
+    }
+    __device__ __forceinline__ f4 times(const WeightStep<TYPE_F32>& w, f4 c) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const f4 a = __builtin_bit_cast(f4, w.v[j]), b = __builtin_bit_cast(f4, x[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c = mfma_f32(a[e], b[e], c);
+        }
+        return c;
+    }
+};
+
+// Terms of one value of x and of h, and bytes of one of them. The terms of a
+// token are columns of the matrix instruction next to each other, summed at
+// the end: one load and one instruction serve 16 columns whatever they hold,
+// and few tokens leave columns free (a load and an instruction per term cost
+// the vector memory unit 12 loads instead of 4 per step of binary32 x, which
+// bounded the kernels).
+template <int WT, bool XBF16>
+struct Terms {
+    static constexpr int kX = WT == TYPE_F32 || XBF16 ? 1 : 3;
+    static constexpr int kH = WT == TYPE_F32 ? 1 : (XBF16 ? 2 : 3);
+    static constexpr int kSize = WT == TYPE_F32 ? 4 : 2;
+};
+
+// A uniform scale, through the scalar cache.
+__device__ __forceinline__ float scale_at(const float* s, int64_t i) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) float*>(
+        reinterpret_cast<uintptr_t>(s + i));
 }
 
 // N consecutive elements of a row of x (binary32 or bfloat16) as floats, 0
@@ -191,114 +267,6 @@ __device__ __forceinline__ void load_row(const void* row, bool have, int k, int 
     }
 }
 
-// One token row as the operands of one step, from x.
-template <int WT, bool XBF16>
-struct XStep {
-    static constexpr int kTerms = XBF16 ? 1 : 3;
-    bf8 t[4][kTerms];
-
-    __device__ __forceinline__ void load(const void* row, bool have, int k0, int K, bool vec,
-                                         int g) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + frag_first<WT>(j, g);
-            if constexpr (XBF16) {
-                if (vec && have && k + 8 <= K) {
-                    t[j][0] = *reinterpret_cast<const bf8*>(static_cast<const uint16_t*>(row) + k);
-                    continue;
-                }
-            }
-            float x[8];
-            load_row<8, XBF16>(row, have, k, K, vec, x);
-            split_bf16<kTerms>(x, t[j]);
-        }
-    }
-    __device__ __forceinline__ f4 times(const WeightStep<WT>& w, f4 c) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bf8 a = w.frag(j);
-#pragma unroll
-            for (int s = 0; s < kTerms; ++s) c = mfma_bf16(a, t[j][s], c);
-        }
-        return c;
-    }
-};
-template <bool XBF16>
-struct XStep<TYPE_F32, XBF16> {
-    float x[8][4];
-
-    __device__ __forceinline__ void load(const void* row, bool have, int k0, int K, bool vec,
-                                         int g) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            load_row<4, XBF16>(row, have, k0 + Weight<TYPE_F32>::first(j, g), K, vec, x[j]);
-    }
-    __device__ __forceinline__ f4 times(const WeightStep<TYPE_F32>& w, f4 c) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const f4 a = __builtin_bit_cast(f4, w.v[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c = mfma_f32(a[e], x[j][e], c);
-        }
-        return c;
-    }
-};
-
-// One pair's h as the operands of one step: bfloat16 terms in planes (binary32
-// for binary32 weights), rows of h_ld elements, valid up to a multiple of 16.
-template <int WT, int NP>
-struct HStep {
-    bf8 t[4][NP];
-
-    __device__ __forceinline__ void load(const MoeParams& p, int pair, bool have, int k0, int K16,
-                                         int g) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + frag_first<WT>(j, g);
-#pragma unroll
-            for (int s = 0; s < NP; ++s) {
-                t[j][s] = bf8{};
-                if (have && k < K16)
-                    t[j][s] = *reinterpret_cast<const bf8*>(p.h + s * p.h_plane +
-                                                            (int64_t)pair * p.h_ld + k);
-            }
-        }
-    }
-    __device__ __forceinline__ f4 times(const WeightStep<WT>& w, f4 c) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bf8 a = w.frag(j);
-#pragma unroll
-            for (int s = 0; s < NP; ++s) c = mfma_bf16(a, t[j][s], c);
-        }
-        return c;
-    }
-};
-template <int NP>
-struct HStep<TYPE_F32, NP> {
-    f4 x[8];
-
-    __device__ __forceinline__ void load(const MoeParams& p, int pair, bool have, int k0, int K16,
-                                         int g) {
-        const float* row = reinterpret_cast<const float*>(p.h) + (int64_t)pair * p.h_ld;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = k0 + Weight<TYPE_F32>::first(j, g);
-            x[j] = f4{0.f, 0.f, 0.f, 0.f};
-            if (have && k < K16) x[j] = *reinterpret_cast<const f4*>(row + k);
-        }
-    }
-    __device__ __forceinline__ f4 times(const WeightStep<TYPE_F32>& w, f4 c) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const f4 a = __builtin_bit_cast(f4, w.v[j]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c = mfma_f32(a[e], x[j][e], c);
-        }
-        return c;
-    }
-};
-
 __device__ __forceinline__ float act_exact(float x, int act) {
     // (a handful of values per workgroup: accurate library functions)
     if (act == ACT_SILU) return x / (1.f + expf(-x));
@@ -308,532 +276,698 @@ __device__ __forceinline__ float act_exact(float x, int act) {
 
 // ---- route -----------------------------------------------------------------
 
-template <int N, bool BF16>
-__device__ __forceinline__ void load_doubles(const void* row, int k, int K, bool vec,
-                                             double (&x)[N]) {
-    float f[N];
-    load_row<N, BF16>(row, true, k, K, vec, f);
+// x as the experts' products read it: bfloat16 terms, or binary32 for binary32
+// weights; eight elements per thread, of the grid's threads [first, first + all).
+template <bool XBF16>
+__device__ __forceinline__ void prepare_tokens(const MoeParams& p, int64_t first, int64_t all) {
+    const int per_row = p.xs_ld / 8;
+    for (int64_t u = first; u < (int64_t)p.T * per_row; u += all) {
+        const int t = (int)(u / per_row), k = (int)(u - (int64_t)t * per_row) * 8;
+        float x[8];
+        load_row<8, XBF16>(static_cast<const uint8_t*>(p.x) + t * p.ldx * (XBF16 ? 2 : 4), true, k,
+                           p.H, p.vec_x, x);
+        const int64_t at = (int64_t)t * p.xs_ld + k;
+        if (p.wtype == TYPE_F32) {
+            float* const o = static_cast<float*>(p.xs) + at;
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = (double)f[e];
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<f4*>(o + e) = f4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+        } else {
+            constexpr int NS = XBF16 ? 1 : 3;
+            bf8 s[NS];
+            split_bf16<NS>(x, s);
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                *reinterpret_cast<bf8*>(static_cast<uint16_t*>(p.xs) + i * p.xs_plane + at) = s[i];
+        }
+    }
 }
 
-// NT tokens by 4 experts per workgroup; 4 waves split K.
-template <int NT, bool XBF16, bool RBF16>
-__global__ void __launch_bounds__(256) route_kernel(MoeParams p) {
-    constexpr int NE = 4;
-    __shared__ double part[4][NT * NE];
+// NT tokens by 4 experts per workgroup; the waves take 256 k at a time, so that
+// all of a row of up to 4096 is in flight at once (the kernel is a chain of
+// latencies: one wave of loads, the sums' exchange, one LDS round). The last
+// workgroups of the x dimension prepare x (other_wgs of them).
+template <int NT, int NW, bool XBF16, bool RBF16>
+__global__ void __launch_bounds__(64 * NW) route_kernel(MoeParams p, int other_wgs) {
+    constexpr int NE = 4, NV = NT * NE;
+    __shared__ double part[NW][NV];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int expert_wgs = gridDim.x - other_wgs;
+    if ((int)blockIdx.x >= expert_wgs) {
+        prepare_tokens<XBF16>(
+            p, ((int64_t)(blockIdx.x - expert_wgs) * gridDim.y + blockIdx.y) * blockDim.x + threadIdx.x,
+            (int64_t)other_wgs * gridDim.y * blockDim.x);
+        return;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.plan->ticket = 0;
     const int e0 = blockIdx.x * NE, t0 = blockIdx.y * NT;
-    double acc[NT][NE] = {};
-    for (int k = wave * 256 + lane * 4; k < p.H; k += 1024) {
-        double x[NT][4], r[NE][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int row = t0 + t < p.T ? t0 + t : p.T - 1;
-            load_doubles<4, XBF16>(static_cast<const uint8_t*>(p.x) +
-                                       row * p.ldx * (XBF16 ? 2 : 4), k, p.H, p.vec_x, x[t]);
-        }
+    double acc[NV] = {};
+    for (int k = wave * 256 + lane * 4; k < p.H; k += NW * 256) {
+        float x[NT][4], r[NE][4];
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int row = e0 + e < p.E ? e0 + e : p.E - 1;
-            load_doubles<4, RBF16>(static_cast<const uint8_t*>(p.router) +
-                                       row * p.ldr * (RBF16 ? 2 : 4), k, p.H, p.vec_r, r[e]);
+            load_row<4, RBF16>(static_cast<const uint8_t*>(p.router) +
+                                   row * p.ldr * (RBF16 ? 2 : 4), true, k, p.H, p.vec_r, r[e]);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+            const int row = t0 + t < p.T ? t0 + t : p.T - 1;
+            load_row<4, XBF16>(static_cast<const uint8_t*>(p.x) + row * p.ldx * (XBF16 ? 2 : 4),
+                               true, k, p.H, p.vec_x, x[t]);
+        }
 #pragma unroll
-            for (int e = 0; e < NE; ++e)
+        for (int i = 0; i < 4; ++i) {
+            double rd[NE];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][e] = fma(x[t][i], r[e][i], acc[t][e]);
+            for (int e = 0; e < NE; ++e) rd[e] = (double)r[e][i];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const double xd = (double)x[t][i];
+#pragma unroll
+                for (int e = 0; e < NE; ++e) acc[t * NE + e] = fma(xd, rd[e], acc[t * NE + e]);
+            }
+        }
     }
+    // Sum over the lanes: while there are several values left, half of the
+    // lanes keep one half of them and the others the other half (lane bit 5
+    // decides first); then plain exchanges. Lane l ends with value `mine`.
+    int n = NV, o = 32, mine = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int h = NV / 2; h >= 1; h >>= 1) {
+        const bool upper = lane & o;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            double v = acc[t][e];
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-            if (lane == 0) part[wave][t * NE + e] = v;
+        for (int i = 0; i < h; ++i) {
+            const double keep = upper ? acc[h + i] : acc[i], give = upper ? acc[i] : acc[h + i];
+            acc[i] = keep + __shfl_xor(give, o, 64);
         }
+        if (upper) mine += h;
+        o >>= 1;
+        n = h;
+    }
+    (void)n;
+#pragma unroll
+    for (int b = 64 / NV / 2; b >= 1; b >>= 1) acc[0] += __shfl_xor(acc[0], b, 64);
+    if ((lane & (64 / NV - 1)) == 0) part[wave][mine] = acc[0];
     __syncthreads();
-    if (threadIdx.x < NT * NE) {
+    if (threadIdx.x < NV) {
         const int t = t0 + threadIdx.x / NE, e = e0 + threadIdx.x % NE;
         double v = 0.0;
-        for (int w = 0; w < 4; ++w) v += part[w][threadIdx.x];
+        for (int w = 0; w < NW; ++w) v += part[w][threadIdx.x];
         if (t < p.T && e < p.E) p.logits[t * p.E + e] = v;
     }
 }
 
-// One wave per token. A NaN logit ranks as -inf (and its weight is NaN).
-__global__ void __launch_bounds__(64) topk_kernel(MoeParams p) {
-    const int t = blockIdx.x, lane = threadIdx.x;
-    double key[kMaxE / 64];
-    const double ninf = -__builtin_inf();
-#pragma unroll
-    for (int i = 0; i < kMaxE / 64; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = ninf;
-        if (e < p.E) key[i] = p.logits[t * p.E + e];
-    }
-    uint32_t taken = 0;
-    double top = 0.0;
-    double mine = 0.0;  // lane s: the s-th chosen logit
-    int mine_id = 0;
-    for (int s = 0; s < p.k; ++s) {
-        double v = ninf;
-        int at = 0x7FFFFFFF;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 64; ++i) {
-            const int e = lane + 64 * i;
-            const double c = key[i] == key[i] ? key[i] : ninf;
-            if (e < p.E && !(taken >> i & 1) && (c > v || (c == v && e < at))) v = c, at = e;
-        }
+// ---- plan --------------------------------------------------------------------
+//
+// The unit of the experts' work is a group: tokens of one expert that fill the
+// 16 columns of a matrix instruction, G = 16 / terms of them. Groups are
+// numbered by expert, then by token; an expert with more tokens is read once
+// per group, the later ones from the caches. x and h can have different
+// numbers of terms, so there are two lists.
+
+constexpr int kPlanThreads = 1024;
+
+// Values that one workgroup leaves for another of the same launch. Agent-scope
+// accesses go past the XCDs' own L2s, so once a workgroup's stores have been
+// acknowledged they can be counted as done with a relaxed atomic; an agent-wide
+// release and acquire (which write back and invalidate a whole L2) cost the
+// 8-token layer 10 us in top-k and 60 us in the kernels that stream weights.
+template <typename V>
+__device__ __forceinline__ void leave(V* at, V v) {
+    __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V fetch_left(const V* at) {
+    return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Whether this workgroup is the last of `all` to arrive at the counter; all its
+// threads call it after their stores. s_last: in LDS.
+__device__ __forceinline__ bool last_to_arrive(int32_t* counter, int all, int* s_last) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are acknowledged
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *s_last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT) == all - 1;
+    __syncthreads();
+    return *s_last;
+}
+
+struct PlanLds {
+    int ids[kMaxT * kMaxK];
+    float w[kMaxT * kMaxK];
+    unsigned long long chose[kMaxE];  // the tokens that chose the expert
+    int base[kMaxE];                  // its first group
+    int wave_sum[kMaxE / 64];
+};
+
+// One list from l.ids and l.chose (kPlanThreads threads).
+__device__ __forceinline__ void write_groups(const MoeParams& p, PlanLds& l, int G, int* total,
+                                             MoeGroup* out) {
+    const int tid = threadIdx.x;
+    int own = 0, sum = 0;
+    if (tid < kMaxE) {
+        sum = own = (unsigned)(__popcll(l.chose[tid]) + G - 1) / (unsigned)G;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const double ov = __shfl_xor(v, o, 64);
-            const int oa = __shfl_xor(at, o, 64);
-            if (ov > v || (ov == v && oa < at)) v = ov, at = oa;
+            const int v = __shfl_up(sum, o, 64);
+            if ((tid & 63) >= o) sum += v;
         }
-        // at < E: k <= E, so some expert is left
-        if ((at & 63) == lane) taken |= 1u << (at >> 6);
-        double raw = 0.0;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 64; ++i)
-            if ((at >> 6) == i) raw = key[i];
-        raw = __shfl(raw, at & 63, 64);
-        if (s == 0) top = raw;
-        if (lane == s) mine = raw, mine_id = at;
+        if ((tid & 63) == 63) l.wave_sum[tid >> 6] = sum;
     }
-    float sum = 0.f;
-    if (p.renorm) {
-        if (lane < p.k) sum = expf((float)(mine - top));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kMaxE / 64; ++i)
-            if (lane + 64 * i < p.E) sum += expf((float)(key[i] - top));
+    __syncthreads();
+    if (tid < kMaxE) {
+#pragma unroll 1
+        for (int w = 0; w < (tid >> 6); ++w) sum += l.wave_sum[w];
+        l.base[tid] = sum - own;
+        if (tid == kMaxE - 1) *total = sum;
+#pragma unroll 1
+        for (int c = 0; c < own; ++c) {
+            MoeGroup& m = out[sum - own + c];
+            m.expert = tid;
+            const int left = __popcll(l.chose[tid]) - c * G;
+            m.count = left < G ? left : G;
+        }
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-    if (lane < p.k) {
-        p.ids[t * p.k + lane] = mine_id;
-        p.weights[t * p.k + lane] = expf((float)(mine - top)) / sum;
+    __syncthreads();
+    for (int i = tid; i < p.T * p.k; i += kPlanThreads) {
+        const int e = l.ids[i], t = (unsigned)i / (unsigned)p.k;
+        if (e < 0 || e >= p.E) continue;
+        float w = 0.f;
+        bool first = true;
+#pragma unroll 1
+        for (int s = 0; s < p.k; ++s)
+            if (l.ids[t * p.k + s] == e) {
+                first = first && t * p.k + s >= i;
+                w += l.w[t * p.k + s];
+            }
+        if (!first) continue;
+        const int rank = __popcll(l.chose[e] & ((1ull << t) - 1ull));
+        const int c = (unsigned)rank / (unsigned)G;
+        MoeGroup& m = out[l.base[e] + c];
+        m.pair[rank - c * G] = (int16_t)i;
+        m.weight[rank - c * G] = w;
     }
+    __syncthreads();
+}
+
+// The plan, from l.ids and l.w; the tickets of the down kernel are set to 0.
+__device__ __forceinline__ void write_plan(const MoeParams& p, PlanLds& l) {
+    const int tid = threadIdx.x;
+    if (tid < kMaxE) l.chose[tid] = 0;
+    for (int i = tid; i < (p.H + 15) / 16; i += kPlanThreads) p.tickets[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < p.T * p.k; i += kPlanThreads) {
+        const int e = l.ids[i];
+        if (e >= 0 && e < p.E) atomicOr(&l.chose[e], 1ull << ((unsigned)i / (unsigned)p.k));
+    }
+    __syncthreads();
+    // (one copy of the code: these kernels run each instruction about once, and
+    // fetching them is most of their time)
+    const int lists = p.groups_h != p.groups_x ? 2 : 1;
+#pragma unroll 1
+    for (int i = 0; i < lists; ++i)
+        write_groups(p, l, i ? p.gh : p.gx, i ? &p.plan->total_h : &p.plan->total_x,
+                     i ? p.groups_h : p.groups_x);
+}
+
+__device__ __forceinline__ void read_choice(const MoeParams& p, PlanLds& l) {
+    for (int i = threadIdx.x; i < p.T * p.k; i += kPlanThreads) {
+        l.ids[i] = fetch_left(p.ids + i);
+        l.w[i] = fetch_left(p.weights + i);
+    }
+    __syncthreads();
+}
+
+// Workgroup 0 writes the plan; the others prepare x.
+template <bool XBF16>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(MoeParams p) {
+    __shared__ PlanLds l;
+    if (blockIdx.x > 0) {
+        prepare_tokens<XBF16>(p, (int64_t)(blockIdx.x - 1) * kPlanThreads + threadIdx.x,
+                              (int64_t)(gridDim.x - 1) * kPlanThreads);
+        return;
+    }
+    read_choice(p, l);
+    write_plan(p, l);
+}
+
+// Top-k of `tokens` tokens at a time from the first one of the workgroup on.
+// An expert's rank is the number of experts before it in the order (larger
+// logit, then lower number; NaN as -inf), counted by `parts` threads against a
+// part of them each: threads = tokens * width * parts, width = the power of two
+// at or above E. A NaN logit's weight is NaN. Then the plan: one workgroup for
+// all tokens writes it from LDS, of one per token the last to finish does.
+__global__ void __launch_bounds__(kPlanThreads) topk_kernel(MoeParams p, int width, int tokens) {
+    __shared__ PlanLds l;
+    __shared__ double key[kPlanThreads], raw[kPlanThreads];  // [tokens][width]
+    __shared__ int rank[kPlanThreads];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int parts = kPlanThreads / (tokens * width);
+    const int e = tid % width, part = tid / width % parts, lt = tid / (width * parts);
+    const int t0 = gridDim.x == 1 ? 0 : (int)blockIdx.x;
+    const int t1 = gridDim.x == 1 ? p.T : t0 + 1;
+    for (int tb = t0; tb < t1; tb += tokens) {
+        const int t = tb + lt;
+        const bool mine = t < t1 && e < p.E;
+        double* const k = key + lt * width;
+        if (mine && part == 0) {
+            const double v = p.logits[t * p.E + e];
+            raw[lt * width + e] = v;
+            k[e] = v == v ? v : -__builtin_inf();
+            rank[lt * width + e] = 0;
+        }
+        __syncthreads();
+        if (mine) {
+            const int per = (p.E + parts - 1) / parts, f0 = part * per;
+            const int f1 = f0 + per < p.E ? f0 + per : p.E;
+            const double v = k[e];
+            int n = 0;
+#pragma unroll 4
+            for (int f = f0; f < f1; ++f) n += k[f] > v || (k[f] == v && f < e);
+            if (n) atomicAdd(&rank[lt * width + e], n);
+        }
+        __syncthreads();
+        if (mine && part == 0 && rank[lt * width + e] < p.k)
+            l.ids[t * p.k + rank[lt * width + e]] = e;
+        __syncthreads();
+        for (int q = wave; q < tokens && tb + q < t1; q += kPlanThreads / 64) {  // a wave per token
+            const double* const r = raw + q * width;
+            const int* const chosen = l.ids + (tb + q) * p.k;
+            const double top = r[chosen[0]];
+            const float mine_w = lane < p.k ? expf((float)(r[chosen[lane]] - top)) : 0.f;
+            float sum = mine_w;
+            if (!p.renorm) {
+                sum = 0.f;
+#pragma unroll 1
+                for (int f = lane; f < p.E; f += 64) sum += expf((float)(r[f] - top));
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+            if (lane < p.k) {
+                const int at = (tb + q) * p.k + lane;
+                l.w[at] = mine_w / sum;
+                leave(p.ids + at, (int32_t)chosen[lane]);
+                leave(p.weights + at, mine_w / sum);
+            }
+        }
+        __syncthreads();
+    }
+    if (gridDim.x > 1) {
+        // (the counter was set to 0 by the router kernel)
+        if (!last_to_arrive(&p.plan->ticket, gridDim.x, &s_last)) return;
+        read_choice(p, l);
+    }
+    write_plan(p, l);
 }
 
 // ---- experts ---------------------------------------------------------------
 
-// The ids in LDS and the chosen experts as a bit set (two barriers).
-__device__ __forceinline__ void mark_experts(const MoeParams& p, int* ids, uint32_t* bits) {
-    const int n = p.T * p.k;
-    const int first = (int)threadIdx.x < n ? p.ids[threadIdx.x] : -1;  // in flight over the barrier
-    for (int i = threadIdx.x; i < kMaxE / 32; i += blockDim.x) bits[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = i < (int)blockDim.x ? first : p.ids[i];
-        ids[i] = e;
-        if (e >= 0 && e < p.E) atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
+// Rows [row0, row0 + rows) of an expert's matrix as a buffer.
+template <int WT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t expert_rows(const ExpertMatrix& m, int e,
+                                                              int row0, int rows, int cols) {
+    constexpr int S = Weight<WT>::kSize;
+    const int64_t bytes = ((int64_t)(rows - 1) * m.ld + cols) * S;
+    return make_rsrc_bytes(static_cast<const uint8_t*>(m.w) + (e * m.stride + row0 * m.ld) * S,
+                           (bytes + 15) & ~15ll);
 }
 
-// Chosen experts before word `lane` of the bit set (lanes 0 .. 15), and how
-// many there are, from the words' own counts.
-__device__ __forceinline__ int experts_before(const uint32_t* bits, int lane, int& total) {
-    int own = lane < kMaxE / 32 ? __popc(bits[lane]) : 0, sum = own;
-#pragma unroll
-    for (int o = 1; o < kMaxE / 32; o <<= 1) {
-        const int v = __shfl_up(sum, o, 64);
-        if (lane >= o) sum += v;
-    }
-    total = __shfl(sum, kMaxE / 32 - 1, 64);
-    return sum - own;
-}
-
-// The y-th chosen expert in ascending order, or -1 (the whole wave takes part).
-__device__ __forceinline__ int nth_expert(const uint32_t* bits, int lane, int y) {
-    int total;
-    const int before = experts_before(bits, lane, total);
-    int found = -1;
-    if (lane < kMaxE / 32) {
-        uint32_t w = bits[lane];
-        const int skip = y - before;
-        if (skip >= 0 && skip < __popc(w)) {
-            for (int i = 0; i < skip; ++i) w &= w - 1;
-            found = lane * 32 + __ffs(w) - 1;
-        }
-    }
-    const uint64_t m = __ballot(found >= 0);
-    return m ? __builtin_amdgcn_readfirstlane(__shfl(found, __ffsll((unsigned long long)m) - 1, 64))
-             : -1;
-}
-
-// The tokens that chose expert e: this lane's token (lane < T), whether it
-// did, the first of its slots that did, and (weights) the sum of those slots'
-// weights.
-struct Chosen {
-    bool have;
-    int pair;
-    float weight;
-};
-template <bool WEIGHTS>
-__device__ __forceinline__ Chosen chosen_by(const MoeParams& p, const int* ids, int lane, int e) {
-    Chosen c{false, 0, 0.f};
-    if (lane < p.T)
-        for (int s = p.k - 1; s >= 0; --s)
-            if (ids[lane * p.k + s] == e) {
-                c.have = true;
-                c.pair = lane * p.k + s;
-                if (WEIGHTS) c.weight += p.weights[lane * p.k + s];
-            }
-    return c;
-}
-
-// Orders one wave's LDS accesses across its lanes.
-__device__ __forceinline__ void wave_lds_sync() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-}
-
-// gate and up: RT x 16 inner rows of one expert per workgroup, NW waves
-// splitting K. Each wave keeps the weights of its next step in flight while it
-// uses the present ones.
-template <int WT, bool XBF16, int RT, int NW>
-struct GateUp {
-    static constexpr int kStreams = 2 * RT;  // gate and up of each row tile
-    using W = Weight<WT>;
-    const MoeParams& p;
-    const int lane, wave, n16, g, row0, steps;
-    const uint8_t* w[kStreams];
-    const float* s[kStreams];
-
-    __device__ __forceinline__ GateUp(const MoeParams& p, int e, int row0)
-        : p(p), lane(threadIdx.x & 63),
-          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), n16(lane & 15), g(lane >> 4),
-          row0(row0), steps((p.H + 127) / 128) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            // (rows past I read the last one; their h is 0 or not stored)
-            const int first = row0 + 16 * r < p.I ? row0 + 16 * r : p.I - 1;
-            const int row = first + n16 < p.I ? first + n16 : p.I - 1;
-            w[2 * r] = static_cast<const uint8_t*>(p.gate.w) +
-                       (e * p.gate.stride + row * p.gate.ld) * W::kSize;
-            w[2 * r + 1] = static_cast<const uint8_t*>(p.up.w) +
-                           (e * p.up.stride + row * p.up.ld) * W::kSize;
-            if (WT == TYPE_E4M3) {
-                s[2 * r] = p.gate.s + e * p.gate.s_stride + (first >> 7);
-                s[2 * r + 1] = p.up.s + e * p.up.s_stride + (first >> 7);
-            }
-        }
-    }
-
-    __device__ __forceinline__ void fetch(WeightStep<WT> (&v)[kStreams], int kb) const {
-        if (kb >= steps) return;
-#pragma unroll
-        for (int i = 0; i < kStreams; ++i) v[i].load(w[i], kb * 128, p.H, g);
-    }
-
-    // NT groups of 16 tokens (tok: their indices, `count` of them)
-    template <int NT>
-    __device__ __forceinline__ void sums(const int* tok, int count, f4 (&acc)[NT][kStreams]) const {
-        const void* x[NT];
-        bool have[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            have[t] = 16 * t + n16 < count;
-            x[t] = static_cast<const uint8_t*>(p.x) +
-                   (have[t] ? tok[16 * t + n16] : 0) * p.ldx * (XBF16 ? 2 : 4);
-#pragma unroll
-            for (int i = 0; i < kStreams; ++i) acc[t][i] = f4{0.f, 0.f, 0.f, 0.f};
-        }
-        auto use = [&](const WeightStep<WT>(&v)[kStreams], int kb) {
-            float f[kStreams];
-#pragma unroll
-            for (int i = 0; i < kStreams; ++i)
-                f[i] = WT == TYPE_E4M3 ? s[i][kb * (i & 1 ? p.up.lds : p.gate.lds)] : 1.f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                XStep<WT, XBF16> xs;
-                xs.load(x[t], have[t], kb * 128, p.H, p.vec_x, g);
-#pragma unroll
-                for (int i = 0; i < kStreams; ++i) {
-                    if constexpr (WT == TYPE_E4M3) {
-                        const f4 b = xs.times(v[i], f4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[t][i][e] = fmaf(f[i], b[e], acc[t][i][e]);
-                    } else {
-                        acc[t][i] = xs.times(v[i], acc[t][i]);
-                    }
-                }
-            }
-        };
-        if constexpr (NT > 2) {  // (many tokens: no registers for a second step)
-            for (int kb = wave; kb < steps; kb += NW) {
-                WeightStep<WT> v[kStreams];
-                fetch(v, kb);
-                use(v, kb);
-            }
-            return;
-        }
-        WeightStep<WT> v0[kStreams], v1[kStreams];
-        fetch(v0, wave);
-        for (int kb = wave; kb < steps; kb += 2 * NW) {
-            fetch(v1, kb + NW);
-            use(v0, kb);
-            if (kb + NW >= steps) break;
-            fetch(v0, kb + 2 * NW);
-            use(v1, kb + NW);
-        }
-    }
-
-    // Joins the waves' sums in wave order and stores h of the groups.
-    template <int NT>
-    __device__ __forceinline__ void finish(const int* pair, int count, f4 (&acc)[NT][kStreams],
-                                           f4 (*red)[2][64]) const {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                red[wave][0][lane] = acc[t][2 * r];
-                red[wave][1][lane] = acc[t][2 * r + 1];
-                __syncthreads();
-                if (threadIdx.x < 256) {
-                    float gs = 0.f, us = 0.f;  // component `wave` of the four
-                    for (int v = 0; v < NW; ++v) {
-                        gs += red[v][0][lane][wave];
-                        us += red[v][1][lane][wave];
-                    }
-                    const int i = row0 + 16 * r + 4 * g + wave;
-                    if (16 * t + n16 < count && i < p.h_ld)
-                        store_h(pair[16 * t + n16], i, i < p.I ? act_exact(gs, p.act) * us : 0.f);
-                }
-                __syncthreads();
-            }
-    }
-
-    __device__ __forceinline__ void store_h(int pair, int i, float h) const {
-        const int64_t at = (int64_t)pair * p.h_ld + i;
-        if constexpr (WT == TYPE_F32) {
-            reinterpret_cast<float*>(p.h)[at] = h;
-        } else {
-            float left = h;
-#pragma unroll
-            for (int s = 0; s < (XBF16 ? 2 : 3); ++s) {
-                const __bf16 b = (__bf16)left;
-                p.h[s * p.h_plane + at] = __builtin_bit_cast(uint16_t, b);
-                left -= (float)b;
-                if (s == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
-            }
-        }
-    }
-
-    template <int NT>
-    __device__ __forceinline__ void run(const int* tok, const int* pair, int count,
-                                        f4 (*red)[2][64]) const {
-        f4 acc[NT][kStreams];
-        sums<NT>(tok, count, acc);
-        finish<NT>(pair, count, acc, red);
-    }
-};
-
-template <int WT, bool XBF16, int RT, int NW>
+// gate and up: RT x 16 inner rows of one group per workgroup, NW waves taking
+// the steps of K in turn. A wave keeps the operands of its next D - 1 steps in
+// flight while it uses the present ones.
+template <int WT, bool XBF16, int RT, int NW, int D>
 __global__ void __launch_bounds__(64 * NW, 2) gate_up_kernel(MoeParams p) {
     static_assert(NW >= 4, "the joining of the waves' sums takes 256 threads");
-    __shared__ int ids[kMaxT * kMaxK];
-    __shared__ uint32_t bits[kMaxE / 32];
-    __shared__ int tok[NW][kMaxT], pair[NW][kMaxT];
+    using W = Weight<WT>;
+    using N = Terms<WT, XBF16>;
+    constexpr int kStreams = 2 * RT;  // gate and up of each row tile
     __shared__ __attribute__((aligned(16))) f4 red[NW][2][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    mark_experts(p, ids, bits);
-    const int e = nth_expert(bits, lane, blockIdx.y);
-    if (e < 0) return;
-    // every wave makes its own copy of the expert's list: no barrier
-    const Chosen c = chosen_by<false>(p, ids, lane, e);
-    const uint64_t m = __ballot(c.have);
-    const int count = __popcll(m);
-    if (c.have) {
-        const int at = __popcll(m & ((1ull << lane) - 1ull));
-        tok[wave][at] = lane;
-        pair[wave][at] = c.pair;
+    const int n16 = lane & 15, g = lane >> 4;
+    // (past the last group the list holds nothing, but can be read)
+    const MoeGroup* const group = p.groups_x + blockIdx.y;
+    const int total = p.plan->total_x, e_read = group->expert, count = group->count;
+    const int16_t column_pair = group->pair[n16 / N::kX], token_pair = group->pair[n16];
+    if ((int)blockIdx.y >= total) return;
+    const int e = __builtin_amdgcn_readfirstlane(e_read);
+
+    const int row0 = blockIdx.x * 16 * RT;
+    const int rows = p.I - row0 < 16 * RT ? p.I - row0 : 16 * RT;
+    const __amdgpu_buffer_rsrc_t rg = expert_rows<WT>(p.gate, e, row0, rows, p.H);
+    const __amdgpu_buffer_rsrc_t ru = expert_rows<WT>(p.up, e, row0, rows, p.H);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc_bytes(p.xs, p.xs_bytes);
+    uint32_t at[kStreams];
+    const float* s[kStreams];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        // (rows past the matrix read its last one; their h is 0 or not stored)
+        const int row = 16 * r + n16 < rows ? 16 * r + n16 : rows - 1;
+        at[2 * r] = (uint32_t)(row * p.gate.ld) * W::kSize;
+        at[2 * r + 1] = (uint32_t)(row * p.up.ld) * W::kSize;
+        if (WT == TYPE_E4M3) {
+            const int b = (16 * r < rows ? row0 + 16 * r : row0) >> 7;
+            s[2 * r] = p.gate.s + e * p.gate.s_stride + b;
+            s[2 * r + 1] = p.up.s + e * p.up.s_stride + b;
+        }
     }
-    wave_lds_sync();
-    const GateUp<WT, XBF16, RT, NW> gu(p, e, blockIdx.x * 16 * RT);
-    // (binary32 x by 32 rows: four groups of tokens do not fit the registers,
-    // and the second pass over the weights mostly hits the L2)
-    constexpr int kMost = !XBF16 && RT > 1 ? 2 : 4;
-    if (count <= 16) {
-        gu.template run<1>(tok[wave], pair[wave], count, red);
-    } else if (count <= 32) {
-        gu.template run<2>(tok[wave], pair[wave], count, red);
-    } else {
-        for (int c0 = 0; c0 < count; c0 += 16 * kMost)
-            gu.template run<kMost>(tok[wave] + c0, pair[wave] + c0, count - c0, red);
+    uint32_t token = kNowhere;  // this lane's column: a term of a token's row
+    if (n16 / N::kX < count)
+        token = ((uint32_t)column_pair / (uint32_t)p.k) * (uint32_t)(p.xs_ld * N::kSize) +
+                (uint32_t)(n16 % N::kX) * (uint32_t)(p.xs_plane * N::kSize);
+
+    struct Step {
+        WeightStep<WT> w[kStreams];
+        TokenStep<WT> x;
+        float f[kStreams];
+    };
+    const int steps = (p.H + 127) / 128;
+    f4 acc[kStreams];
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
+    auto fetch = [&](Step& v, int kb) {
+#pragma unroll
+        for (int i = 0; i < kStreams; ++i) v.w[i].load(i & 1 ? ru : rg, at[i], kb, p.H, g);
+        v.x.load(rx, token, kb, p.xs_cols, g);
+        if constexpr (WT == TYPE_E4M3) {
+            const int b = kb < steps ? kb : steps - 1;
+#pragma unroll
+            for (int i = 0; i < kStreams; ++i)
+                v.f[i] = scale_at(s[i], b * (i & 1 ? p.up.lds : p.gate.lds));
+        }
+    };
+    auto use = [&](Step& v, int kb) {
+        if (kb == steps - 1) {
+#pragma unroll
+            for (int i = 0; i < kStreams; ++i) v.w[i].clear_tail(kb, p.H, g);
+        }
+#pragma unroll
+        for (int i = 0; i < kStreams; ++i) {
+            if constexpr (WT == TYPE_E4M3) {
+                const f4 b = v.x.times(v.w[i], f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(v.f[i], b[c], acc[i][c]);
+            } else {
+                acc[i] = v.x.times(v.w[i], acc[i]);
+            }
+        }
+    };
+    Step v[D];
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(v[d], wave + d * NW);
+    for (int kb = wave; kb < steps; kb += D * NW) {  // (past the last step: zeros)
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            fetch(v[(d + D - 1) % D], kb + (d + D - 1) * NW);
+            use(v[d], kb + d * NW);
+        }
+    }
+
+    // the sums over waves and terms, in order, 16 rows at a time; h in its terms
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        red[wave][0][lane] = acc[2 * r];
+        red[wave][1][lane] = acc[2 * r + 1];
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int i = row0 + 16 * r + 4 * g + wave;  // component `wave` of the four
+            if (n16 < count && i < p.h_ld) {             // column n16: a token here
+                float gs = 0.f, us = 0.f;
+                for (int v = 0; v < NW; ++v)
+#pragma unroll
+                    for (int t = 0; t < N::kX; ++t) {
+                        gs += red[v][0][16 * g + n16 * N::kX + t][wave];
+                        us += red[v][1][16 * g + n16 * N::kX + t][wave];
+                    }
+                const float h = i < p.I ? act_exact(gs, p.act) * us : 0.f;
+                const int64_t to = (int64_t)token_pair * p.h_ld + i;
+                if constexpr (WT == TYPE_F32) {
+                    reinterpret_cast<float*>(p.h)[to] = h;
+                } else {
+                    float left = h;
+#pragma unroll
+                    for (int t = 0; t < N::kH; ++t) {
+                        const __bf16 b = (__bf16)left;
+                        p.h[t * p.h_plane + to] = __builtin_bit_cast(uint16_t, b);
+                        left -= (float)b;
+                        if (t == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
+                    }
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
-// down: 16 output rows per workgroup. The (expert, block of K) units of all
-// chosen experts are dealt to the waves in contiguous runs; a wave keeps the
-// weights of its next D units in flight, over the border of two experts too.
+// down: RT x 16 output rows per workgroup. The (group, step of K) units of all
+// groups go to the waves of the row's gridDim.y workgroups in turn; a wave
+// keeps the weights and h of its next D units in flight, over the border of two
+// groups too, and adds each group's weighted results to its own tokens x rows
+// piece in LDS. (One CU draws about 25 GB/s whatever it keeps in flight, so
+// fewer than 256 row tiles are split among several workgroups.)
 constexpr int kDownWaves = 8;
+// Output rows of a workgroup: 32 share the reads of h (e4m3: 125 -> 102 us for
+// 82 experts of 4096 x 1536), 16 for binary32 weights (66 -> 60 us).
+constexpr int down_rows(int wtype) { return wtype == TYPE_F32 ? 16 : 32; }
 
-template <int WT, bool XBF16>
-__global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeParams p) {
+template <int WT, bool XBF16, int RT, int D>
+__global__ void __launch_bounds__(64 * kDownWaves, 4) down_kernel(MoeParams p, int most) {
+    constexpr int kRows = 16 * RT;
     using W = Weight<WT>;
-    constexpr int NP = XBF16 ? 2 : 3;
-    constexpr int D = WT == TYPE_E4M3 ? 4 : 2;
-    __shared__ int ids[kMaxT * kMaxK];
-    __shared__ uint32_t bits[kMaxE / 32];
-    __shared__ int active[kMaxE];
-    __shared__ int tok[kDownWaves][kMaxT], pair[kDownWaves][kMaxT];
-    __shared__ float wt[kDownWaves][kMaxT];
-    __shared__ float sum[kDownWaves][kMaxT][16];
+    using N = Terms<WT, XBF16>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
+    MoeGroup* const groups = reinterpret_cast<MoeGroup*>(down_lds);            // [most]
+    float* const sums = reinterpret_cast<float*>(down_lds + most * sizeof(MoeGroup));
+    __shared__ int s_last;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, g = lane >> 4;
-    const int row0 = blockIdx.x * 16;
-    mark_experts(p, ids, bits);
-    int chosen;
+    const int row0 = blockIdx.x * kRows;
+    const int piece = p.T * kRows;
+    float* const sum = sums + wave * piece;
+    const int total = __builtin_amdgcn_readfirstlane(
+        p.groups_h == p.groups_x ? p.plan->total_x : p.plan->total_h);
     {
-        int before = experts_before(bits, lane, chosen);
-        if (wave == 0 && lane < kMaxE / 32)
-            for (uint32_t w = bits[lane]; w; w &= w - 1) active[before++] = lane * 32 + __ffs(w) - 1;
+        const i4v* const from = reinterpret_cast<const i4v*>(p.groups_h);
+        i4v* const to = reinterpret_cast<i4v*>(groups);
+        for (int i = threadIdx.x; i < most * (int)(sizeof(MoeGroup) / 16); i += blockDim.x)
+            to[i] = from[i];
     }
-    for (int i = lane; i < p.T * 16; i += 64) sum[wave][i >> 4][i & 15] = 0.f;
+    for (int i = lane; i < piece; i += 64) sum[i] = 0.f;
     __syncthreads();
     const int steps = (p.I + 127) / 128;
-    const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(chosen) * steps;
-    const int K16 = p.h_ld;
-    const int64_t u0 = units * wave / kDownWaves, u1 = units * (wave + 1) / kDownWaves;
-    const int row = row0 + n16 < p.H ? row0 + n16 : p.H - 1;
-    const uint8_t* const w0 = static_cast<const uint8_t*>(p.down.w) + row * p.down.ld * W::kSize;
+    const int rows = p.H - row0 < kRows ? p.H - row0 : kRows;
+    uint32_t at[RT];
+    int sb[RT];  // row block of the scales
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int row = 16 * r + n16 < rows ? 16 * r + n16 : rows - 1;
+        at[r] = (uint32_t)(row * p.down.ld) * W::kSize;
+        sb[r] = (16 * r < rows ? row0 + 16 * r : row0) >> 7;
+    }
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc_bytes(p.h, p.h_bytes);
 
-    // the unit to fetch next and the one to use next
-    int fa = (int)(u0 / steps), fk = (int)(u0 - (int64_t)fa * steps);
+    struct Unit {
+        WeightStep<WT> w[RT];
+        TokenStep<WT> h;
+        float f[RT];
+    };
+    // the unit to fetch next (its group's number, step, expert and this lane's
+    // column, a term of a row of h) and the one to use next
+    const int first = blockIdx.y * kDownWaves + wave, stride = kDownWaves * gridDim.y;
+    const int stride_a = stride / steps, stride_k = stride - stride_a * steps;
+    int fa = first / steps, fk = first - fa * steps, fe = 0, last = -1;
     int ua = fa, uk = fk;
-    auto fetch = [&](WeightStep<WT>& v) {
-        const int e = __builtin_amdgcn_readfirstlane(active[fa]);
-        v.load(w0 + e * p.down.stride * W::kSize, fk * 128, p.I, g);
-        if (++fk == steps) fk = 0, ++fa;
+    uint32_t frow = kNowhere;
+    auto next = [&](int& a, int& k) {
+        a += stride_a;
+        k += stride_k;
+        if (k >= steps) k -= steps, ++a;
     };
-    f4 acc[4];
-    int count = 0;
-    const float* sw = nullptr;
-    auto flush = [&] {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (16 * t + n16 < count) {
-                const int at = tok[wave][16 * t + n16];
-                const float f = wt[wave][16 * t + n16];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[wave][at][4 * g + i] += f * acc[t][i];
-            }
-    };
-    auto use = [&](const WeightStep<WT>& v, bool first) {
-        if (first || uk == 0) {
-            flush();
-            wave_lds_sync();
-            const int e = __builtin_amdgcn_readfirstlane(active[ua]);
-            const Chosen c = chosen_by<true>(p, ids, lane, e);
-            const uint64_t m = __ballot(c.have);
-            count = __popcll(m);
-            if (c.have) {
-                const int at = __popcll(m & ((1ull << lane) - 1ull));
-                tok[wave][at] = lane;
-                pair[wave][at] = c.pair;
-                wt[wave][at] = c.weight;
-            }
-            wave_lds_sync();
-            if (WT == TYPE_E4M3) sw = p.down.s + e * p.down.s_stride + (row0 >> 7);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+    auto fetch = [&](Unit& v) {
+        const int a = fa < total ? fa : total - 1;
+        if (a != last) {
+            last = a;
+            fe = __builtin_amdgcn_readfirstlane(groups[a].expert);
+            frow = n16 / N::kH < groups[a].count
+                       ? (uint32_t)groups[a].pair[n16 / N::kH] * (uint32_t)(p.h_ld * N::kSize) +
+                             (uint32_t)(n16 % N::kH) * (uint32_t)(p.h_plane * N::kSize)
+                       : kNowhere;
         }
-        const float f = WT == TYPE_E4M3 ? sw[uk * p.down.lds] : 1.f;
+        const int k = fa < total ? fk : steps;  // past the last unit: reads nowhere
+        const __amdgpu_buffer_rsrc_t r = expert_rows<WT>(p.down, fe, row0, rows, p.I);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (16 * t >= count) break;
-            const bool have = 16 * t + n16 < count;
-            HStep<WT, NP> hs;
-            hs.load(p, have ? pair[wave][16 * t + n16] : 0, have, uk * 128, K16, g);
+        for (int i = 0; i < RT; ++i) v.w[i].load(r, at[i], k, p.I, g);
+        v.h.load(rh, frow, k, p.h_ld, g);
+        if constexpr (WT == TYPE_E4M3) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                v.f[i] = scale_at(p.down.s, fe * p.down.s_stride + fk * p.down.lds + sb[i]);
+        }
+        next(fa, fk);
+    };
+    f4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f4{0.f, 0.f, 0.f, 0.f};
+    auto flush = [&](int a) {
+        // a token's terms are next to each other: their sum in the first
+        const int c = n16 / N::kH;
+        const bool have = n16 % N::kH == 0 && c < groups[a].count;
+        const int to = have ? (int)((unsigned)groups[a].pair[c] / (unsigned)p.k) * kRows + 4 * g : 0;
+        const float f = groups[a].weight[c];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            f4 s = acc[r];
+#pragma unroll
+            for (int t = 1; t < N::kH; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] += __shfl(acc[r][i], (lane + t) & 63, 64);
+            if (have) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[to + 16 * r + i] += f * s[i];
+            }
+            acc[r] = f4{0.f, 0.f, 0.f, 0.f};
+        }
+    };
+    auto use = [&](Unit& v) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            if (uk == steps - 1) v.w[r].clear_tail(uk, p.I, g);
             if constexpr (WT == TYPE_E4M3) {
-                const f4 b = hs.times(v, f4{0.f, 0.f, 0.f, 0.f});
+                const f4 b = v.h.times(v.w[r], f4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(f, b[i], acc[t][i]);
+                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(v.f[r], b[i], acc[r][i]);
             } else {
-                acc[t] = hs.times(v, acc[t]);
+                acc[r] = v.h.times(v.w[r], acc[r]);
             }
         }
-        if (++uk == steps) uk = 0, ++ua;
+        const int a = ua;
+        next(ua, uk);
+        if (ua != a) flush(a);
     };
-    WeightStep<WT> v[D];
+    if (ua < total) {
+        Unit v[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (u0 + d < u1) fetch(v[d]);
-    for (int64_t u = u0; u < u1; u += D) {
+        for (int d = 0; d < D; ++d) fetch(v[d]);
+        while (ua < total) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (u + d < u1) use(v[d], u + d == u0);
-            if (u + d + D < u1) fetch(v[d]);
+            for (int d = 0; d < D; ++d) {
+                if (ua < total) use(v[d]);
+                fetch(v[d]);
+            }
         }
     }
-    flush();
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += blockDim.x) {
-        const int t = i >> 4, n = i & 15;
-        if (row0 + n >= p.H) continue;
+    auto store = [&](int i, float s) {
+        const int n = row0 + i % kRows;
+        const int64_t to = (int64_t)(i / kRows) * p.ldo + n;
+        if (n >= p.H) return;
+        if (XBF16) static_cast<uint16_t*>(p.out)[to] = (uint16_t)bf16_code(s);
+        else static_cast<float*>(p.out)[to] = s;
+    };
+    auto joined = [&](int i) {
         float s = 0.f;
-        for (int w = 0; w < kDownWaves; ++w) s += sum[w][t][n];
-        const int64_t at = (int64_t)t * p.ldo + row0 + n;
-        if (XBF16) static_cast<uint16_t*>(p.out)[at] = (uint16_t)bf16_code(s);
-        else static_cast<float*>(p.out)[at] = s;
+#pragma unroll
+        for (int w = 0; w < kDownWaves; ++w) s += sums[w * piece + i];
+        return s;
+    };
+    if (gridDim.y == 1) {
+        for (int i = threadIdx.x; i < piece; i += blockDim.x) store(i, joined(i));
+        return;
+    }
+    // Several workgroups: each leaves its piece, the last one adds them in order.
+    float* const pieces = p.pieces + (int64_t)blockIdx.x * gridDim.y * piece;
+    for (int i = threadIdx.x; i < piece; i += blockDim.x)
+        leave(pieces + blockIdx.y * piece + i, joined(i));
+    if (!last_to_arrive(p.tickets + blockIdx.x, gridDim.y, &s_last)) return;
+    for (int i = threadIdx.x; i < piece; i += blockDim.x) {
+        float s = 0.f;
+        for (int y = 0; y < (int)gridDim.y; ++y)
+            s += fetch_left(pieces + y * piece + i);
+        store(i, s);
     }
 }
 
 template <int WT, bool XBF16>
 hipError_t launch_experts(const MoeParams& p, hipStream_t stream) {
-    const int most = p.E < p.T * p.k ? p.E : p.T * p.k;
     // Two workgroups of 4 waves on a CU, so that one streams while the other
-    // finds its expert; 8 waves while that leaves CUs idle. 32 inner rows per
-    // workgroup where the weights of two steps fit the registers.
+    // starts; 8 waves while that leaves CUs idle. Steps in flight: what the
+    // registers hold.
     constexpr int RT = WT == TYPE_F32 ? 1 : 2;
+    constexpr int D = WT == TYPE_E4M3 ? 3 : 2;
     const int tiles = (p.I + 16 * RT - 1) / (16 * RT);
-    if ((int64_t)tiles * most >= 512)
-        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, RT, 4>), dim3(tiles, most), dim3(256), 0,
-                           stream, p);
+    if ((int64_t)tiles * p.most_x >= 512)
+        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, RT, 4, D>), dim3(tiles, p.most_x), dim3(256),
+                           0, stream, p);
     else
-        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, 1, 8>), dim3((p.I + 15) / 16, most),
+        hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, 1, 8, 2>), dim3((p.I + 15) / 16, p.most_x),
                            dim3(512), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((down_kernel<WT, XBF16>), dim3((p.H + 15) / 16), dim3(64 * kDownWaves), 0,
-                       stream, p);
+    constexpr int kRows = down_rows(WT), DD = WT == TYPE_E4M3 ? 2 : 1;
+    const size_t lds = p.most_h * sizeof(MoeGroup) + (size_t)kDownWaves * p.T * kRows * 4;
+    hipLaunchKernelGGL((down_kernel<WT, XBF16, kRows / 16, DD>),
+                       dim3((p.H + kRows - 1) / kRows, p.down_wgs), dim3(64 * kDownWaves),
+                       lds, stream, p, p.most_h);
     return hipGetLastError();
 }
 
-template <int NT>
+// Workgroups of `threads` that prepare x, 8 elements per thread.
+int prepare_workgroups(const MoeParams& p, int threads) {
+    if (!p.xs_made) return 0;
+    return (int)(((int64_t)p.T * (p.xs_ld / 8) + threads - 1) / threads);
+}
+
+template <int NT, int NW>
 void launch_logits(const MoeParams& p, hipStream_t stream) {
-    const dim3 g((p.E + 3) / 4, (p.T + NT - 1) / NT);
-    if (p.x_bf16 && p.router_bf16)
-        hipLaunchKernelGGL((route_kernel<NT, true, true>), g, dim3(256), 0, stream, p);
-    else if (p.x_bf16)
-        hipLaunchKernelGGL((route_kernel<NT, true, false>), g, dim3(256), 0, stream, p);
-    else if (p.router_bf16)
-        hipLaunchKernelGGL((route_kernel<NT, false, true>), g, dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL((route_kernel<NT, false, false>), g, dim3(256), 0, stream, p);
+    const int rows = (p.T + NT - 1) / NT;
+    const int other = (prepare_workgroups(p, 64 * NW) + rows - 1) / rows;
+    const dim3 g((p.E + 3) / 4 + other, rows);
+#define FG_LAUNCH(X, R)                                                                     \
+    hipLaunchKernelGGL((route_kernel<NT, NW, X, R>), g, dim3(64 * NW), 0, stream, p, other)
+    if (p.x_bf16 && p.router_bf16) FG_LAUNCH(true, true);
+    else if (p.x_bf16) FG_LAUNCH(true, false);
+    else if (p.router_bf16) FG_LAUNCH(false, true);
+    else FG_LAUNCH(false, false);
+#undef FG_LAUNCH
 }
 
 }  // namespace
 
-int moe_planes(int x_bf16) { return x_bf16 ? 2 : 3; }
-
 hipError_t launch_moe_route(const MoeParams& p, hipStream_t stream) {
-    if (p.T == 1) launch_logits<1>(p, stream);
-    else launch_logits<4>(p, stream);
+    if (p.T == 1) launch_logits<1, 8>(p, stream);
+    else launch_logits<4, 16>(p, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(topk_kernel, dim3(p.T), dim3(64), 0, stream, p);
+    // One workgroup while its comparisons (T E^2) take less time than the
+    // arrivals of several (3 us): up to 2^17.
+    int width = 8, tokens = 1;
+    while (width < p.E) width *= 2;
+    const bool one = p.T == 1 || (int64_t)p.T * width * width <= 1 << 17;
+    while (one && tokens < p.T && tokens * width < kPlanThreads) tokens *= 2;
+    hipLaunchKernelGGL(topk_kernel, dim3(one ? 1 : p.T), dim3(kPlanThreads), 0, stream, p, width,
+                       tokens);
     return hipGetLastError();
+}
+
+hipError_t launch_moe_plan(const MoeParams& p, hipStream_t stream) {
+    const dim3 g(1 + prepare_workgroups(p, kPlanThreads));
+    if (p.x_bf16) hipLaunchKernelGGL(plan_kernel<true>, g, dim3(kPlanThreads), 0, stream, p);
+    else hipLaunchKernelGGL(plan_kernel<false>, g, dim3(kPlanThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+int moe_group_size(int terms) { return 16 / terms; }
+
+int moe_down_workgroups(int wtype, int H, int I, int most_groups) {
+    // Two workgroups for every CU, each wave with at least two units.
+    const int tiles = (H + down_rows(wtype) - 1) / down_rows(wtype);
+    const int units = most_groups * ((I + 127) / 128);
+    return std::max(1, std::min((512 + tiles - 1) / tiles, units / (2 * kDownWaves)));
 }
 
 hipError_t launch_moe_experts(const MoeParams& p, hipStream_t stream) {

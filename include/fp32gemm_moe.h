@@ -25,6 +25,7 @@ extern "C" {
 #define FG_MOE_MAX_TOKENS 64   /* tokens of one call */
 #define FG_MOE_MAX_TOP_K 16    /* experts of one token */
 #define FG_MOE_MAX_EXPERTS 512 /* experts of the layer */
+#define FG_MOE_MAX_DIM 65536   /* hidden and inner size */
 
 /* The experts' matrices of one kind: expert e's is `rows` rows of `ld`
  * elements at w + e * stride. Rows start at multiples of 16 bytes (w, ld and
@@ -45,8 +46,8 @@ typedef struct fg_moe_layer {
     int32_t tokens;       /* 1: T, 0 .. FG_MOE_MAX_TOKENS */
     int32_t experts;      /* 2: E, 1 .. FG_MOE_MAX_EXPERTS */
     int32_t top_k;        /* 3: k, 1 .. min(E, FG_MOE_MAX_TOP_K) */
-    int32_t hidden;       /* 4: H, 1 .. FG_MAX_LD */
-    int32_t inner;        /* 5: I, 1 .. FG_MAX_LD */
+    int32_t hidden;       /* 4: H, 1 .. FG_MOE_MAX_DIM */
+    int32_t inner;        /* 5: I, 1 .. FG_MOE_MAX_DIM */
     int32_t type;         /* 6: x and out: FG_TYPE_F32 or FG_TYPE_BF16 */
     int32_t weight_type;  /* 7: gate, up and down: any fg_type */
     int32_t activation;   /* 8: fg_activation (FG_ACT_SILU for the usual layer) */
