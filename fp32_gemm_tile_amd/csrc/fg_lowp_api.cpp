@@ -61,10 +61,12 @@ struct Plan {
     int64_t splits;
 };
 
-Plan plan_gemm(int64_t M, int64_t N, int64_t K, size_t ws_bytes) {
+Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     constexpr int64_t kCUs = 256;
     Plan p;
-    p.shape = cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2 ? 1 : 0;
+    if (bf16 && cdiv(M, 256) * cdiv(N, 256) >= kCUs) p.shape = 2;
+    else if (!bf16 && cdiv(M, 256) * cdiv(N, 128) >= kCUs) p.shape = 3;
+    else p.shape = cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2 ? 1 : 0;
     const fg::Fp8Shape s = fg::fp8_shape(p.shape);
     const int64_t tiles = cdiv(M, s.bm) * cdiv(N, s.bn), kb = cdiv(K, fg::kScaleBlock);
     int64_t want = tiles >= kCUs ? 1 : std::min<int64_t>({cdiv(2 * kCUs, tiles), kb, 32});
@@ -137,8 +139,9 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
 
 size_t fg_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
-    const Plan p = plan_gemm(M, N, K, (size_t)-1 / 2);
-    return p.splits > 1 ? (size_t)(p.splits * M * N) * 4 : 0;
+    const int64_t splits = std::max(plan_gemm(M, N, K, false, (size_t)-1 / 2).splits,
+                                    plan_gemm(M, N, K, true, (size_t)-1 / 2).splits);
+    return splits > 1 ? (size_t)(splits * M * N) * 4 : 0;
 }
 
 fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t* A,
@@ -204,7 +207,7 @@ fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_
         p.alpha = 0.f;
         return launched(fg::launch_fp8_finish(p, stream), "scaling kernel");
     }
-    const Plan plan = plan_gemm(M, N, K, workspace ? workspace_bytes : 0);
+    const Plan plan = plan_gemm(M, N, K, p.c_bf16, workspace ? workspace_bytes : 0);
     const fg::Fp8Shape s = fg::fp8_shape(plan.shape);
     if (cdiv(M, s.bm) * cdiv(N, s.bn) > 0x7FFFFFFFll)
         return fail(FG_ERR_UNSUPPORTED, 0, "more than 2^31 - 1 output tiles");

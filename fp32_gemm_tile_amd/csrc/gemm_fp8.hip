@@ -33,6 +33,7 @@ typedef int i8v __attribute__((ext_vector_type(8)));
 typedef int i4v __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f4 mfma_fp8(i8v a, i8v b) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -73,6 +74,7 @@ __device__ __forceinline__ f4 mfma_f16(h8 a, h8 b, f4 c) {
 template <bool FP8>
 struct Operand {
     h8 v[4];
+    Operand() = default;
     __device__ __forceinline__ explicit Operand(i8v c) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = codes_to_f16(c[2 * j], c[2 * j + 1]);
@@ -87,6 +89,7 @@ struct Operand {
 template <>
 struct Operand<true> {
     i8v v;
+    Operand() = default;
     __device__ __forceinline__ explicit Operand(i8v c) : v(c) {}
     __device__ __forceinline__ f4 times(const Operand& o) const { return mfma_fp8(v, o.v); }
 };
@@ -115,26 +118,44 @@ __device__ __forceinline__ i8v read_frag(const uint8_t* tile, int r, int g, int 
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
+// Loads straight to LDS: lane l's bytes go to lds + 16 l (or 4 l). Written as
+// instructions, because the compiler makes every LDS read wait for all such
+// loads it knows of, also those into the stage that is not being read; the loop
+// below waits for them itself. They have no result registers, and offsets past
+// the buffer's end read zeros. M0 holds the LDS address (one wait state).
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ i4v buffer_words(const void* base, int64_t bytes) {
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    return i4v{(int)(uint32_t)b, (int)(uint32_t)(b >> 32) & 0xFFFF, (int)(uint32_t)bytes,
+               kBufferWord3};
+}
+__device__ __forceinline__ void dma16(i4v r, uint32_t lds, uint32_t off) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                             off, 0, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(r)
+                 : "m0");
 #else
     (void)r, (void)lds, (void)off;
 #endif
 }
-__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
+__device__ __forceinline__ void dma4(i4v r, uint32_t lds, uint32_t off) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
-                                             off, 0, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(r)
+                 : "m0");
 #else
     (void)r, (void)lds, (void)off;
 #endif
 }
 
+template <bool BF16>
 __device__ __forceinline__ void store_c(const Fp8Params& p, int64_t i, int64_t j, f4 acc) {
     const int n = p.N - j < 4 ? (int)(p.N - j) : 4;
-    if (p.c_bf16) {
+    if constexpr (BF16) {
         uint16_t* c = static_cast<uint16_t*>(p.C) + i * p.ldc + j;
         f4 o = acc * p.alpha;
         if (p.beta != 0.f)
@@ -172,26 +193,49 @@ __device__ __forceinline__ void store_ws(const Fp8Params& p, int split, int64_t 
     }
 }
 
+// A uniform scale, through the scalar cache.
+__device__ __forceinline__ float scale_at(const float* s, int64_t i) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) float*>(
+        reinterpret_cast<uintptr_t>(s + i));
+}
+
+// Workgroup id -> output tile. Consecutive ids go to the 8 XCDs in turn; XCD x
+// gets the x-th contiguous part of the tiles, numbered in bands of kBand tile
+// rows, column by column inside a band, so the tiles that run together on one
+// XCD share rows of A and of B in its L2.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_of(int bid, int n, int tiles_m, int tiles_n, int& tm,
+                                        int& tn) {
+    const int x = bid & 7, q = n >> 3, r = n & 7;
+    const int id = x * q + (x < r ? x : r) + (bid >> 3);
+    const int per_band = kBand * tiles_n;
+    const int band = id / per_band, first = band * kBand;
+    const int rows = tiles_m - first < kBand ? tiles_m - first : kBand;
+    const int in = id - band * per_band;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
 template <bool V>
 struct Flag {
     static constexpr bool value = V;
 };
 
-template <int BM, int BN, int WM, int WN, bool B_TILE, bool FP8>
+template <int BM, int BN, int WM, int WN, int NS, bool B_TILE, bool FP8>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp8Params p) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
     constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int kStage = (BM + BN) * 128;
     constexpr int kScales = BM + (B_TILE ? 0 : BN);
-    __shared__ __attribute__((aligned(128))) uint8_t lds[2 * kStage];
-    __shared__ __attribute__((aligned(16))) float scales[2 * kScales];
+    __shared__ __attribute__((aligned(128))) uint8_t lds[NS * kStage];
+    __shared__ __attribute__((aligned(16))) float scales[NS * kScales];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, g = lane >> 4;
     const int wi = (wave % NWM) * WM, wj = (wave / NWM) * WN;
-    const int tiles_m = (p.M + BM - 1) / BM;
-    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    int tm, tn;
+    tile_of(blockIdx.x, gridDim.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, tm, tn);
     const int split = blockIdx.y;
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int rows_a = p.M - m0 < BM ? (int)(p.M - m0) : BM;
@@ -200,34 +244,52 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
     const int kb1 = kb0 + p.kb_per_split < p.kb ? kb0 + p.kb_per_split : p.kb;
 
     const int64_t k16 = ((int64_t)p.K + 15) & ~15ll;
-    const __amdgpu_buffer_rsrc_t ra =
-        make_rsrc_bytes(p.A + m0 * p.lda, (int64_t)(rows_a - 1) * p.lda + k16);
-    const __amdgpu_buffer_rsrc_t rb =
-        make_rsrc_bytes(p.B + n0 * p.ldb, (int64_t)(rows_b - 1) * p.ldb + k16);
+    // (extents below 2^32: at most 256 rows of FG_MAX_LD bytes)
+    const i4v a_words = buffer_words(p.A + m0 * p.lda, (int64_t)(rows_a - 1) * p.lda + k16);
+    const i4v b_words = buffer_words(p.B + n0 * p.ldb, (int64_t)(rows_b - 1) * p.ldb + k16);
     // one wave's load: 8 rows, lane l row l / 8, chunk (l % 8) ^ (l / 8)
     const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
     const uint32_t va = (uint32_t)((lane >> 3) * p.lda) + chunk;
     const uint32_t vb = (uint32_t)((lane >> 3) * p.ldb) + chunk;
 
-    auto fetch = [&](int kb, int stage) {
-        uint8_t* const s = lds + stage * kStage;
-        float* const sc = scales + stage * kScales;
-#pragma unroll
-        for (int c = wave; c < BM / 8; c += NW)
-            dma16(ra, s + c * 1024, va + (uint32_t)(c * 8 * p.lda) + (uint32_t)kb * 128u);
-#pragma unroll
-        for (int c = wave; c < BN / 8; c += NW)
-            dma16(rb, s + BM * 128 + c * 1024, vb + (uint32_t)(c * 8 * p.ldb) + (uint32_t)kb * 128u);
-        const __amdgpu_buffer_rsrc_t rsa =
-            make_rsrc_bytes(p.SA + kb * p.ldsa + m0, (int64_t)rows_a * 4);
-        for (int c = wave; c < BM / 64; c += NW) dma4(rsa, sc + c * 64, (uint32_t)(c * 64 + lane) * 4u);
-        if constexpr (!B_TILE) {
-            const __amdgpu_buffer_rsrc_t rsb =
-                make_rsrc_bytes(p.SB + kb * p.ldsb + n0, (int64_t)rows_b * 4);
-            for (int c = NW - 1 - wave; c < BN / 64; c += NW)
-                dma4(rsb, sc + BM + c * 64, (uint32_t)(c * 64 + lane) * 4u);
+    static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && BM / 64 <= NW && BN / 64 <= NW, "");
+    // Part q of block kb's loads of this wave: 1024 bytes of A or B, or scales.
+    constexpr int kPartsA = BM / 8 / NW, kParts = kPartsA + BN / 8 / NW;
+    const uint32_t lds0 = lds_address(lds), scales0 = lds_address(scales);
+    auto fetch_part = [&](int kb, int stage, int q) {
+        // (past the last block: buffers without a byte, zeros nobody reads)
+        const uint32_t s = lds0 + stage * kStage;
+        const bool more = kb < kb1;
+        i4v ra = a_words, rb = b_words;
+        if (!more) ra[2] = rb[2] = 0;
+        if (q < kPartsA) {
+            const int c = wave + NW * q;
+            dma16(ra, s + c * 1024, va + (uint32_t)(c * 8 * p.lda + (int64_t)kb * 128));
+        } else {
+            const int c = wave + NW * (q - kPartsA);
+            dma16(rb, s + BM * 128 + c * 1024,
+                  vb + (uint32_t)(c * 8 * p.ldb + (int64_t)kb * 128));
         }
     };
+    // (every wave loads 64 scales of each operand, some of them twice, so that
+    // all have the same number of loads in flight)
+    auto fetch_scales = [&](int kb, int stage) {
+        const uint32_t sc = scales0 + stage * kScales * 4;
+        const bool more = kb < kb1;
+        const int ca = wave % (BM / 64), cb = wave % (BN / 64);
+        dma4(buffer_words(p.SA + kb * p.ldsa + m0, more ? (int64_t)rows_a * 4 : 0), sc + ca * 256,
+             (uint32_t)(ca * 64 + lane) * 4u);
+        if constexpr (!B_TILE)
+            dma4(buffer_words(p.SB + kb * p.ldsb + n0, more ? (int64_t)rows_b * 4 : 0),
+                 sc + (BM + cb * 64) * 4, (uint32_t)(cb * 64 + lane) * 4u);
+    };
+    auto fetch = [&](int kb, int stage) {
+        fetch_scales(kb, stage);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) fetch_part(kb, stage, q);
+    };
+    constexpr int kLoads = kParts + (B_TILE ? 1 : 2);  // of one wave for one block
+    static_assert((NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
 
     f4 acc[TI][TJ];
 #pragma unroll
@@ -235,69 +297,138 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
+    // The block in stage `stage`; block kb + NS - 1 is fetched into the stage of
+    // the block before.
     auto use = [&](int kb, int stage, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
         const int k_left = p.K - kb * 128;
         const uint8_t* const sa = lds + stage * kStage + wi * 128;
         const uint8_t* const sb = lds + stage * kStage + (BM + wj) * 128;
         const float* const sc = scales + stage * kScales;
-        i8v a[TI];
-        float s[TI];
+        // B_TILE: the wave's columns lie in WN / 128 blocks of columns, at least one
+        constexpr int NB = B_TILE ? (WN + 127) / 128 : 1;
+        float s[TI][NB];
+        Operand<FP8> a[TI];
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-            a[i] = read_frag<TAIL>(sa, 16 * i + n16, g, k_left);
-            s[i] = sc[wi + 16 * i + n16];
-        }
+            a[i] = Operand<FP8>(read_frag<TAIL>(sa, 16 * i + n16, g, k_left));
+            const float si = sc[wi + 16 * i + n16];
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const Operand<FP8> b(read_frag<TAIL>(sb, 16 * j + n16, g, k_left));
-            f4 t[TI];
-#pragma unroll
-            for (int i = 0; i < TI; ++i) t[i] = b.times(Operand<FP8>(a[i]));
-            if constexpr (B_TILE) {
-                const int64_t jb = (n0 + wj + 16 * j) >> 7;
-                const float sj = p.SB[kb * p.ldsb + (jb < (p.N + 127) >> 7 ? jb : 0)];
-#pragma unroll
-                for (int i = 0; i < TI; ++i) {
-                    const float f = s[i] * sj;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(f, t[i][e], acc[i][j][e]);
+            for (int b = 0; b < NB; ++b) {
+                s[i][b] = si;
+                if constexpr (B_TILE) {
+                    const int64_t jb = ((n0 + wj) >> 7) + b;
+                    s[i][b] = si * scale_at(p.SB, kb * p.ldsb + (jb < (p.N + 127) >> 7 ? jb : 0));
                 }
-            } else {
-                const f4 sj = *reinterpret_cast<const f4*>(sc + BM + wj + 16 * j + 4 * g);
-#pragma unroll
-                for (int i = 0; i < TI; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = fmaf(s[i] * sj[e], t[i][e], acc[i][j][e]);
             }
         }
+        // One matrix instruction after the other, column tile by column tile; the
+        // sum of the one kAhead before is taken over while it runs, and the codes
+        // of the next column tile are read. (The scheduler is kept to this order:
+        // left to itself it lines up all reads first and runs out of registers.)
+        constexpr int kAhead = 2, kRing = kAhead + 1, kAll = TI * TJ;
+        f4 t[kRing], sj[2];
+        Operand<FP8> b[2];
+        b[0] = Operand<FP8>(read_frag<TAIL>(sb, n16, g, k_left));
+        auto add = [&](int n) {
+            const int i = n % TI, j = n / TI;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f = B_TILE ? s[i][16 * j / 128] : s[i][0] * sj[j & 1][e];
+                acc[i][j][e] = fmaf(f, t[n % kRing][e], acc[i][j][e]);
+            }
+        };
+#pragma unroll
+        for (int n = 0; n < kAll; ++n) {
+            const int i = n % TI, j = n / TI;
+            t[n % kRing] = b[j & 1].times(a[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (n >= kAhead) add(n - kAhead);
+            if (i == (TI > kAhead ? kAhead : TI - 1)) {
+                if (j + 1 < TJ)
+                    b[(j + 1) & 1] =
+                        Operand<FP8>(read_frag<TAIL>(sb, 16 * (j + 1) + n16, g, k_left));
+            }
+            if (i == 0) {
+                if constexpr (!B_TILE)
+                    sj[j & 1] = *reinterpret_cast<const f4*>(sc + BM + wj + 16 * j + 4 * g);
+                if (j == 0) fetch(kb + NS - 1, stage == 0 ? NS - 1 : stage - 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int n = kAll - kAhead; n < kAll; ++n) add(n);
     };
-    fetch(kb0, 0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int st = (kb - kb0) & 1;
-        __builtin_amdgcn_s_waitcnt(0);  // this wave's part of stage st is in LDS
-        __syncthreads();                // everyone's is, and stage st ^ 1 is read out
-        if (kb + 1 < kb1) fetch(kb + 1, st ^ 1);
-        if (p.K - kb * 128 >= 128) use(kb, st, Flag<false>{});
-        else use(kb, st, Flag<true>{});
+
+    // Block kb is in LDS for everyone (NS - 2 later ones may still be on their
+    // way), and everyone has read the block before. Only the last block of K can
+    // be partial; it is outside the loop.
+    auto step = [&] {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
+                     : "memory");
+    };
+    const int full = p.K / 128 < kb1 ? p.K / 128 : kb1;
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d) fetch(kb0 + d, d);
+    int stage = 0;
+    for (int kb = kb0; kb < full; ++kb) {
+        step();
+        use(kb, stage, Flag<false>{});
+        stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+    if (full < kb1) {
+        step();
+        use(full, stage, Flag<true>{});
     }
 
+    // 16 rows at a time through the wave's own part of the LDS, so that a store
+    // covers consecutive elements of a row (a lane holds four of each of 16
+    // rows), and so that this code, run once, is short.
+    constexpr int kPitch = WN + 4, kLanes = WN / 4, kRows = 64 / kLanes;
+    static_assert(NW * 16 * kPitch * 4 <= NS * kStage, "the stages hold the waves' rows");
+    float* const own = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+    const bool plain = p.vec_c && p.beta == 0.f && p.splits == 1 && n0 + wj + WN <= p.N;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-        const int64_t ci = m0 + wi + 16 * i + n16;
-        if (ci >= p.M) continue;
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const int64_t cj = n0 + wj + 16 * j + 4 * g;
-            if (cj >= p.N) continue;
-            if (p.splits > 1) store_ws(p, split, ci, cj, acc[i][j]);
-            else store_c(p, ci, cj, acc[i][j]);
+        for (int j = 0; j < TJ; ++j)
+            *reinterpret_cast<f4*>(own + n16 * kPitch + 16 * j + 4 * g) = acc[i][j];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const int r0 = lane / kLanes;
+        const int64_t cj = n0 + wj + (lane % kLanes) * 4;
+        const float* const from = own + r0 * kPitch + (lane % kLanes) * 4;
+        if (plain && m0 + wi + 16 * i + 16 <= p.M) {
+            f4 v[16 / kRows];
+#pragma unroll
+            for (int r = 0; r < 16 / kRows; ++r)
+                v[r] = *reinterpret_cast<const f4*>(from + r * kRows * kPitch);
+            const int64_t at = (m0 + wi + 16 * i + r0) * p.ldc + cj;
+#pragma unroll
+            for (int r = 0; r < 16 / kRows; ++r) {
+                const f4 o = v[r] * p.alpha;
+                if constexpr (FP8)
+                    *reinterpret_cast<b4*>(static_cast<__bf16*>(p.C) + at + r * kRows * p.ldc) =
+                        __builtin_convertvector(o, b4);
+                else
+                    *reinterpret_cast<f4*>(static_cast<float*>(p.C) + at + r * kRows * p.ldc) = o;
+            }
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < 16; r += kRows) {
+                const int64_t ci = m0 + wi + 16 * i + r + r0;
+                const f4 v = *reinterpret_cast<const f4*>(from + r * kPitch);
+                if (ci >= p.M || cj >= p.N) continue;
+                if (p.splits > 1) store_ws(p, split, ci, cj, v);
+                else store_c<FP8>(p, ci, cj, v);
+            }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
 // C = alpha * (slice 0 + slice 1 + ...) + beta * C, slices in ascending order.
+template <bool BF16>
 __global__ void __launch_bounds__(256) fp8_finish_kernel(Fp8Params p) {
     const int64_t per_row = ((int64_t)p.N + 3) / 4, units = per_row * p.M;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units;
@@ -313,22 +444,26 @@ __global__ void __launch_bounds__(256) fp8_finish_kernel(Fp8Params p) {
                     if (j + e < p.N) sum[e] += w[e];
             }
         }
-        store_c(p, i, j, sum);
+        store_c<BF16>(p, i, j, sum);
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int NS, bool BF16_ONLY = false>
 hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN);
     const dim3 grid((unsigned)(((p.M + BM - 1) / BM) * (int64_t)((p.N + BN - 1) / BN)),
                     (unsigned)p.splits);
     const bool fp8 = p.c_bf16;
 #define FG_LAUNCH(BT, F)                                                                       \
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, BT, F>), grid, dim3(threads), 0, stream, p)
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, NS, BT, F>), grid, dim3(threads), 0, stream, p)
     if (b_tile && fp8) FG_LAUNCH(true, true);
-    else if (b_tile) FG_LAUNCH(true, false);
     else if (fp8) FG_LAUNCH(false, true);
-    else FG_LAUNCH(false, false);
+    else if constexpr (!BF16_ONLY) {
+        if (b_tile) FG_LAUNCH(true, false);
+        else FG_LAUNCH(false, false);
+    } else {
+        return hipErrorInvalidValue;
+    }
 #undef FG_LAUNCH
     return hipGetLastError();
 }
@@ -336,6 +471,9 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
 constexpr Fp8Shape kShapes[] = {
     {64, 64, 256},
     {128, 128, 256},
+    {256, 256, 512},  // bfloat16 C only
+    {256, 128, 512},
+    {128, 128, 512},
 };
 
 }  // namespace
@@ -345,16 +483,20 @@ Fp8Shape fp8_shape(int shape) { return kShapes[shape]; }
 
 hipError_t launch_gemm_fp8(int shape, bool b_tile, const Fp8Params& p, hipStream_t stream) {
     switch (shape) {
-        case 0: return launch_tile<64, 64, 32, 32>(b_tile, p, stream);
-        case 1: return launch_tile<128, 128, 64, 64>(b_tile, p, stream);
+        case 0: return launch_tile<64, 64, 32, 32, 4>(b_tile, p, stream);
+        case 1: return launch_tile<128, 128, 64, 64, 2>(b_tile, p, stream);
+        case 2: return launch_tile<256, 256, 64, 128, 2, true>(b_tile, p, stream);
+        case 3: return launch_tile<256, 128, 64, 64, 3>(b_tile, p, stream);
+        case 4: return launch_tile<128, 128, 64, 32, 4>(b_tile, p, stream);
         default: return hipErrorInvalidValue;
     }
 }
 
 hipError_t launch_fp8_finish(const Fp8Params& p, hipStream_t stream) {
     const int64_t units = ((int64_t)p.N + 3) / 4 * p.M, wgs = (units + 255) / 256;
-    hipLaunchKernelGGL(fp8_finish_kernel, dim3((unsigned)(wgs < 16384 ? wgs : 16384)), dim3(256),
-                       0, stream, p);
+    const dim3 grid((unsigned)(wgs < 16384 ? wgs : 16384));
+    if (p.c_bf16) hipLaunchKernelGGL(fp8_finish_kernel<true>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(fp8_finish_kernel<false>, grid, dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
