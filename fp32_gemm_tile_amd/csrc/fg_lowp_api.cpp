@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/fp32gemm_fp8.h"
 #include "../../include/fp32gemm_moe.h"
@@ -61,24 +62,36 @@ struct Plan {
     int64_t splits;
 };
 
+// The cheapest by estimate: rounds of one workgroup per CU, each taking the
+// blocks of K one after the other, or the stream of both operands; slices of K
+// (at most 16) cost another kernel and their partial sums' way to memory and
+// back.
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
-    constexpr int64_t kCUs = 256;
-    Plan p;
-    if (bf16 && cdiv(M, 256) * cdiv(N, 256) >= kCUs) p.shape = 2;
-    else if (!bf16 && cdiv(M, 256) * cdiv(N, 128) >= kCUs) p.shape = 3;
-    else p.shape = cdiv(M, 128) * cdiv(N, 128) >= kCUs / 2 ? 1 : 0;
-    const fg::Fp8Shape s = fg::fp8_shape(p.shape);
-    const int64_t tiles = cdiv(M, s.bm) * cdiv(N, s.bn), kb = cdiv(K, fg::kScaleBlock);
-    int64_t want = tiles >= kCUs ? 1 : std::min<int64_t>({cdiv(2 * kCUs, tiles), kb, 32});
-    const int64_t slice = M * N * 4;
-    want = std::min<int64_t>(want, slice > 0 ? (int64_t)(ws_bytes / (size_t)slice) : 1);
-    if (want <= 1) {
-        p.splits = 1;
-    } else {
-        const int64_t per = cdiv(kb, want);
-        p.splits = cdiv(kb, per);
+    constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
+    constexpr double kFinish = 3.2;
+    const int64_t kb = cdiv(K, fg::kScaleBlock);
+    const double stream = ((double)M * K + (double)N * K) / kStream;
+    const double slice = (double)M * N * 4;
+    Plan best{-1, 1};
+    double best_us = 0;
+    for (int s = 0; s < fg::fp8_num_shapes(); ++s) {
+        const fg::Fp8Shape sh = fg::fp8_shape(s);
+        const double per_block = bf16 ? sh.bf16_us : sh.f32_us;
+        if (per_block == 0) continue;
+        const double tiles = (double)cdiv(M, sh.bm) * (double)cdiv(N, sh.bn);
+        for (int64_t n = 1; n <= 16; n *= 2) {
+            const int64_t per = cdiv(kb, n), used = cdiv(kb, per);
+            if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
+            const double rounds = std::ceil(tiles * (double)n / kCUs);
+            double us = sh.fixed_us + std::max(rounds * (double)per * per_block, stream);
+            if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
+            if (best.shape < 0 || us < best_us) {
+                best = Plan{s, n};
+                best_us = us;
+            }
+        }
     }
-    return p;
+    return best;
 }
 
 }  // namespace

@@ -51,7 +51,9 @@ struct Fp8Params {
 // Tile kernels' shapes: index into the table of gemm_fp8.hip.
 struct Fp8Shape {
     int bm, bn;      // rows of A and of B per workgroup
-    int threads;
+    float fixed_us;  // start and end
+    float bf16_us, f32_us;  // per block of K and round of 256 workgroups, by C's
+                            // type (0: not built)
 };
 int fp8_num_shapes();
 Fp8Shape fp8_shape(int shape);

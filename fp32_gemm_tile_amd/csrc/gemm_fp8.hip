@@ -106,15 +106,16 @@ __device__ __forceinline__ i4v keep_bytes(i4v v, int left) {
 }
 
 // The lane's 32 codes of row r of a tile in LDS: chunks g and g + 4.
-template <bool TAIL>
-__device__ __forceinline__ i8v read_frag(const uint8_t* tile, int r, int g, int k_left) {
+__device__ __forceinline__ i8v read_frag(const uint8_t* tile, int r, int g) {
     const uint8_t* row = tile + r * 128;
-    i4v lo = *reinterpret_cast<const i4v*>(row + ((g ^ (r & 7)) << 4));
-    i4v hi = *reinterpret_cast<const i4v*>(row + (((g + 4) ^ (r & 7)) << 4));
-    if constexpr (TAIL) {
-        lo = keep_bytes(lo, k_left - 16 * g);
-        hi = keep_bytes(hi, k_left - 64 - 16 * g);
-    }
+    const i4v lo = *reinterpret_cast<const i4v*>(row + ((g ^ (r & 7)) << 4));
+    const i4v hi = *reinterpret_cast<const i4v*>(row + (((g + 4) ^ (r & 7)) << 4));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// Those of them that are inside K (k_left: columns of the block that are).
+__device__ __forceinline__ i8v keep_codes(i8v c, int g, int k_left) {
+    const i4v lo = keep_bytes(__builtin_shufflevector(c, c, 0, 1, 2, 3), k_left - 16 * g);
+    const i4v hi = keep_bytes(__builtin_shufflevector(c, c, 4, 5, 6, 7), k_left - 64 - 16 * g);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -221,17 +222,25 @@ struct Flag {
     static constexpr bool value = V;
 };
 
-template <int BM, int BN, int WM, int WN, int NS, bool B_TILE, bool FP8>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp8Params p) {
-    constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
+// KG groups of waves take the blocks of K in turn, each with its own ring of NS
+// stages and its own sums, which are added in group order at the end: small
+// results get enough waves per SIMD to hide one block's chain of latencies.
+template <int BM, int BN, int WM, int WN, int NS, int KG, bool B_TILE, bool FP8>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kernel(Fp8Params p) {
+    constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;  // waves of one group
     constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int kStage = (BM + BN) * 128;
-    constexpr int kScales = BM + (B_TILE ? 0 : BN);
-    __shared__ __attribute__((aligned(128))) uint8_t lds[NS * kStage];
-    __shared__ __attribute__((aligned(16))) float scales[NS * kScales];
+    // (scales come 64 at a time)
+    constexpr int kScalesA = BM < 64 ? 64 : BM, kScalesB = BN < 64 ? 64 : BN;
+    constexpr int kScales = kScalesA + (B_TILE ? 0 : kScalesB);
+    __shared__ __attribute__((aligned(128))) uint8_t all_lds[KG * NS * kStage];
+    __shared__ __attribute__((aligned(16))) float all_scales[KG * NS * kScales];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = wave_id / NW, wave = wave_id % NW;
+    uint8_t* const lds = all_lds + group * NS * kStage;
+    float* const scales = all_scales + group * NS * kScales;
     const int n16 = lane & 15, g = lane >> 4;
     const int wi = (wave % NWM) * WM, wj = (wave / NWM) * WN;
     int tm, tn;
@@ -252,44 +261,37 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
     const uint32_t va = (uint32_t)((lane >> 3) * p.lda) + chunk;
     const uint32_t vb = (uint32_t)((lane >> 3) * p.ldb) + chunk;
 
-    static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && BM / 64 <= NW && BN / 64 <= NW, "");
-    // Part q of block kb's loads of this wave: 1024 bytes of A or B, or scales.
+    static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "whole loads per wave");
     constexpr int kPartsA = BM / 8 / NW, kParts = kPartsA + BN / 8 / NW;
+    constexpr int kLoads = kParts + (B_TILE ? 1 : 2);  // of one wave for one block
+    static_assert((NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
     const uint32_t lds0 = lds_address(lds), scales0 = lds_address(scales);
-    auto fetch_part = [&](int kb, int stage, int q) {
-        // (past the last block: buffers without a byte, zeros nobody reads)
-        const uint32_t s = lds0 + stage * kStage;
+    // Block kb into a stage. Past the last block: buffers without a byte, zeros.
+    // Every wave loads 64 scales of each operand, some of them twice, so that
+    // all have the same number of loads in flight.
+    auto fetch = [&](int kb, int stage) {
         const bool more = kb < kb1;
-        i4v ra = a_words, rb = b_words;
-        if (!more) ra[2] = rb[2] = 0;
-        if (q < kPartsA) {
-            const int c = wave + NW * q;
-            dma16(ra, s + c * 1024, va + (uint32_t)(c * 8 * p.lda + (int64_t)kb * 128));
-        } else {
-            const int c = wave + NW * (q - kPartsA);
-            dma16(rb, s + BM * 128 + c * 1024,
-                  vb + (uint32_t)(c * 8 * p.ldb + (int64_t)kb * 128));
-        }
-    };
-    // (every wave loads 64 scales of each operand, some of them twice, so that
-    // all have the same number of loads in flight)
-    auto fetch_scales = [&](int kb, int stage) {
-        const uint32_t sc = scales0 + stage * kScales * 4;
-        const bool more = kb < kb1;
-        const int ca = wave % (BM / 64), cb = wave % (BN / 64);
+        const uint32_t s = lds0 + stage * kStage, sc = scales0 + stage * kScales * 4;
+        const int ca = wave % (kScalesA / 64), cb = wave % (kScalesB / 64);
         dma4(buffer_words(p.SA + kb * p.ldsa + m0, more ? (int64_t)rows_a * 4 : 0), sc + ca * 256,
              (uint32_t)(ca * 64 + lane) * 4u);
         if constexpr (!B_TILE)
             dma4(buffer_words(p.SB + kb * p.ldsb + n0, more ? (int64_t)rows_b * 4 : 0),
-                 sc + (BM + cb * 64) * 4, (uint32_t)(cb * 64 + lane) * 4u);
-    };
-    auto fetch = [&](int kb, int stage) {
-        fetch_scales(kb, stage);
+                 sc + (kScalesA + cb * 64) * 4, (uint32_t)(cb * 64 + lane) * 4u);
+        i4v ra = a_words, rb = b_words;
+        if (!more) ra[2] = rb[2] = 0;
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) fetch_part(kb, stage, q);
+        for (int q = 0; q < kParts; ++q) {
+            if (q < kPartsA) {
+                const int c = wave + NW * q;
+                dma16(ra, s + c * 1024, va + (uint32_t)(c * 8 * p.lda + (int64_t)kb * 128));
+            } else {
+                const int c = wave + NW * (q - kPartsA);
+                dma16(rb, s + BM * 128 + c * 1024,
+                      vb + (uint32_t)(c * 8 * p.ldb + (int64_t)kb * 128));
+            }
+        }
     };
-    constexpr int kLoads = kParts + (B_TILE ? 1 : 2);  // of one wave for one block
-    static_assert((NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
 
     f4 acc[TI][TJ];
 #pragma unroll
@@ -297,39 +299,43 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
-    // The block in stage `stage`; block kb + NS - 1 is fetched into the stage of
-    // the block before.
+    // The block in stage `stage`: one matrix instruction after the other, column
+    // tile by column tile; the sum of the one kAhead before is taken over while
+    // it runs, and the codes of the next column tile are read. (The scheduler is
+    // kept to this order: left to itself it lines up all reads first and runs
+    // out of registers.) The group's block NS - 1 further on is fetched into the
+    // stage of the block before.
     auto use = [&](int kb, int stage, auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
         const int k_left = p.K - kb * 128;
         const uint8_t* const sa = lds + stage * kStage + wi * 128;
         const uint8_t* const sb = lds + stage * kStage + (BM + wj) * 128;
         const float* const sc = scales + stage * kScales;
+        auto codes = [&](const uint8_t* tile, int r) {
+            const i8v c = read_frag(tile, r + n16, g);
+            return Operand<FP8>(TAIL ? keep_codes(c, g, k_left) : c);
+        };
         // B_TILE: the wave's columns lie in WN / 128 blocks of columns, at least one
         constexpr int NB = B_TILE ? (WN + 127) / 128 : 1;
         float s[TI][NB];
-        Operand<FP8> a[TI];
+        Operand<FP8> a[TI], b[2];
+        b[0] = codes(sb, 0);
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-            a[i] = Operand<FP8>(read_frag<TAIL>(sa, 16 * i + n16, g, k_left));
+            a[i] = codes(sa, 16 * i);
             const float si = sc[wi + 16 * i + n16];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                s[i][b] = si;
+            for (int c = 0; c < NB; ++c) {
+                s[i][c] = si;
                 if constexpr (B_TILE) {
-                    const int64_t jb = ((n0 + wj) >> 7) + b;
-                    s[i][b] = si * scale_at(p.SB, kb * p.ldsb + (jb < (p.N + 127) >> 7 ? jb : 0));
+                    const int64_t jb = ((n0 + wj) >> 7) + c;
+                    s[i][c] = si * scale_at(p.SB, (kb < kb1 ? kb : kb1 - 1) * p.ldsb +
+                                                      (jb < (p.N + 127) >> 7 ? jb : 0));
                 }
             }
         }
-        // One matrix instruction after the other, column tile by column tile; the
-        // sum of the one kAhead before is taken over while it runs, and the codes
-        // of the next column tile are read. (The scheduler is kept to this order:
-        // left to itself it lines up all reads first and runs out of registers.)
         constexpr int kAhead = 2, kRing = kAhead + 1, kAll = TI * TJ;
         f4 t[kRing], sj[2];
-        Operand<FP8> b[2];
-        b[0] = Operand<FP8>(read_frag<TAIL>(sb, n16, g, k_left));
         auto add = [&](int n) {
             const int i = n % TI, j = n / TI;
 #pragma unroll
@@ -344,15 +350,12 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
             t[n % kRing] = b[j & 1].times(a[i]);
             __builtin_amdgcn_sched_barrier(0);
             if (n >= kAhead) add(n - kAhead);
-            if (i == (TI > kAhead ? kAhead : TI - 1)) {
-                if (j + 1 < TJ)
-                    b[(j + 1) & 1] =
-                        Operand<FP8>(read_frag<TAIL>(sb, 16 * (j + 1) + n16, g, k_left));
-            }
+            if (i == (TI > kAhead ? kAhead : TI - 1) && j + 1 < TJ)
+                b[(j + 1) & 1] = codes(sb, 16 * (j + 1));
             if (i == 0) {
                 if constexpr (!B_TILE)
-                    sj[j & 1] = *reinterpret_cast<const f4*>(sc + BM + wj + 16 * j + 4 * g);
-                if (j == 0) fetch(kb + NS - 1, stage == 0 ? NS - 1 : stage - 1);
+                    sj[j & 1] = *reinterpret_cast<const f4*>(sc + kScalesA + wj + 16 * j + 4 * g);
+                if (j == 0) fetch(kb + KG * (NS - 1), stage == 0 ? NS - 1 : stage - 1);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -360,70 +363,93 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) fp8_tile_kernel(Fp
         for (int n = kAll - kAhead; n < kAll; ++n) add(n);
     };
 
-    // Block kb is in LDS for everyone (NS - 2 later ones may still be on their
-    // way), and everyone has read the block before. Only the last block of K can
-    // be partial; it is outside the loop.
-    auto step = [&] {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
-                     : "memory");
+    // The next block is in LDS for everyone (later ones may still be on their
+    // way), and everyone has read the block before.
+    // (A wave that is a group by itself has nobody to meet.)
+    auto meet = [] {
+        if constexpr (NW == 1)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * kLoads) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
+                         : "memory");
     };
-    const int full = p.K / 128 < kb1 ? p.K / 128 : kb1;
+    // Only the last block of K can be partial: the last round of the groups takes
+    // it, outside the loop (the other groups' masks keep everything).
+    const int rounds = (kb1 - kb0 + KG - 1) / KG;
+    const int whole = kb1 * 128 > p.K ? rounds - 1 : rounds;
+    int kb = kb0 + group, stage = 0;
 #pragma unroll
-    for (int d = 0; d < NS - 1; ++d) fetch(kb0 + d, d);
-    int stage = 0;
-    for (int kb = kb0; kb < full; ++kb) {
-        step();
+    for (int d = 0; d < NS - 1; ++d) fetch(kb + KG * d, d);
+    for (int r = 0; r < whole; ++r) {
+        meet();
         use(kb, stage, Flag<false>{});
         stage = stage + 1 == NS ? 0 : stage + 1;
+        kb += KG;
     }
-    if (full < kb1) {
-        step();
-        use(full, stage, Flag<true>{});
+    if (whole < rounds) {
+        meet();
+        use(kb, stage, Flag<true>{});
     }
 
-    // 16 rows at a time through the wave's own part of the LDS, so that a store
-    // covers consecutive elements of a row (a lane holds four of each of 16
-    // rows), and so that this code, run once, is short.
+    // 16 rows at a time through the waves' own parts of the LDS: the groups' sums
+    // are added in order, each group taking some of the rows, and a store covers
+    // consecutive elements of a row (a lane holds four of each of 16 rows).
     constexpr int kPitch = WN + 4, kLanes = WN / 4, kRows = 64 / kLanes;
-    static_assert(NW * 16 * kPitch * 4 <= NS * kStage, "the stages hold the waves' rows");
-    float* const own = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+    constexpr int kPart = NW * 16 * kPitch;  // floats of one group
+    static_assert(KG * kPart * 4 <= KG * NS * kStage, "the stages hold the waves' rows");
+    static_assert(16 % KG == 0, "rows per group");
+    float* const own = reinterpret_cast<float*>(all_lds) + wave * 16 * kPitch;
     const bool plain = p.vec_c && p.beta == 0.f && p.splits == 1 && n0 + wj + WN <= p.N;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto sync = [] {
+        if constexpr (KG > 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
-            *reinterpret_cast<f4*>(own + n16 * kPitch + 16 * j + 4 * g) = acc[i][j];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        const int r0 = lane / kLanes;
+            *reinterpret_cast<f4*>(own + group * kPart + n16 * kPitch + 16 * j + 4 * g) = acc[i][j];
+        sync();
+        constexpr int kMine = 16 / KG, kTurns = (kMine + kRows - 1) / kRows;
+        const int r0 = group * kMine + lane / kLanes;
         const int64_t cj = n0 + wj + (lane % kLanes) * 4;
         const float* const from = own + r0 * kPitch + (lane % kLanes) * 4;
+        auto sum_at = [&](int r) {
+            f4 v = *reinterpret_cast<const f4*>(from + r * kPitch);
+#pragma unroll
+            for (int k = 1; k < KG; ++k)
+                v = v + *reinterpret_cast<const f4*>(from + k * kPart + r * kPitch);
+            return v;
+        };
+        const bool busy = kRows <= kMine || lane / kLanes < kMine;
         if (plain && m0 + wi + 16 * i + 16 <= p.M) {
-            f4 v[16 / kRows];
+            f4 v[kTurns];
 #pragma unroll
-            for (int r = 0; r < 16 / kRows; ++r)
-                v[r] = *reinterpret_cast<const f4*>(from + r * kRows * kPitch);
+            for (int r = 0; r < kTurns; ++r) v[r] = sum_at(r * kRows);
             const int64_t at = (m0 + wi + 16 * i + r0) * p.ldc + cj;
+            if (busy) {
 #pragma unroll
-            for (int r = 0; r < 16 / kRows; ++r) {
-                const f4 o = v[r] * p.alpha;
-                if constexpr (FP8)
-                    *reinterpret_cast<b4*>(static_cast<__bf16*>(p.C) + at + r * kRows * p.ldc) =
-                        __builtin_convertvector(o, b4);
-                else
-                    *reinterpret_cast<f4*>(static_cast<float*>(p.C) + at + r * kRows * p.ldc) = o;
+                for (int r = 0; r < kTurns; ++r) {
+                    const f4 o = v[r] * p.alpha;
+                    if constexpr (FP8)
+                        *reinterpret_cast<b4*>(static_cast<__bf16*>(p.C) + at +
+                                               r * kRows * p.ldc) = __builtin_convertvector(o, b4);
+                    else
+                        *reinterpret_cast<f4*>(static_cast<float*>(p.C) + at + r * kRows * p.ldc) = o;
+                }
             }
         } else {
 #pragma unroll 1
-            for (int r = 0; r < 16; r += kRows) {
+            for (int r = 0; r < kTurns * kRows; r += kRows) {
                 const int64_t ci = m0 + wi + 16 * i + r + r0;
-                const f4 v = *reinterpret_cast<const f4*>(from + r * kPitch);
-                if (ci >= p.M || cj >= p.N) continue;
+                const f4 v = sum_at(r);
+                if (!busy || ci >= p.M || cj >= p.N) continue;
                 if (p.splits > 1) store_ws(p, split, ci, cj, v);
                 else store_c<FP8>(p, ci, cj, v);
             }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        sync();
     }
 }
 
@@ -448,14 +474,14 @@ __global__ void __launch_bounds__(256) fp8_finish_kernel(Fp8Params p) {
     }
 }
 
-template <int BM, int BN, int WM, int WN, int NS, bool BF16_ONLY = false>
+template <int BM, int BN, int WM, int WN, int NS, int KG, bool BF16_ONLY = false>
 hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
-    constexpr int threads = 64 * (BM / WM) * (BN / WN);
+    constexpr int threads = 64 * (BM / WM) * (BN / WN) * KG;
     const dim3 grid((unsigned)(((p.M + BM - 1) / BM) * (int64_t)((p.N + BN - 1) / BN)),
                     (unsigned)p.splits);
     const bool fp8 = p.c_bf16;
 #define FG_LAUNCH(BT, F)                                                                       \
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, NS, BT, F>), grid, dim3(threads), 0, stream, p)
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, NS, KG, BT, F>), grid, dim3(threads), 0, stream, p)
     if (b_tile && fp8) FG_LAUNCH(true, true);
     else if (fp8) FG_LAUNCH(false, true);
     else if constexpr (!BF16_ONLY) {
@@ -468,12 +494,20 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// The tile shapes, with what one costs (fp8_estimate): microseconds for a start
+// and end, and per block of K while 256 workgroups run, for bfloat16 and for
+// binary32 C. Measured on one MI355X (slopes over K at full grids);
+// rows of small results: many groups of K, so that the whole of a CU's LDS is in
+// flight (1 x 8192 x 8192 11.4 us = 5.9 TB/s, 32 x 8192 x 8192 13.1 us; with
+// the 64 x 64 tile and four slices of K 17.4 and 18.4).
 constexpr Fp8Shape kShapes[] = {
-    {64, 64, 256},
-    {128, 128, 256},
-    {256, 256, 512},  // bfloat16 C only
-    {256, 128, 512},
-    {128, 128, 512},
+    {16, 32, 4.5f, 0.07f, 0.08f},
+    {32, 32, 4.5f, 0.18f, 0.21f},
+    {64, 32, 4.5f, 0.20f, 0.26f},
+    {64, 64, 4.7f, 0.25f, 0.34f},
+    {128, 128, 5.7f, 0.66f, 1.15f},
+    {256, 128, 7.5f, 1.08f, 2.1f},
+    {256, 256, 10.f, 1.7f, 0.f},  // bfloat16 C only
 };
 
 }  // namespace
@@ -483,11 +517,13 @@ Fp8Shape fp8_shape(int shape) { return kShapes[shape]; }
 
 hipError_t launch_gemm_fp8(int shape, bool b_tile, const Fp8Params& p, hipStream_t stream) {
     switch (shape) {
-        case 0: return launch_tile<64, 64, 32, 32, 4>(b_tile, p, stream);
-        case 1: return launch_tile<128, 128, 64, 64, 2>(b_tile, p, stream);
-        case 2: return launch_tile<256, 256, 64, 128, 2, true>(b_tile, p, stream);
-        case 3: return launch_tile<256, 128, 64, 64, 3>(b_tile, p, stream);
-        case 4: return launch_tile<128, 128, 64, 32, 4>(b_tile, p, stream);
+        case 0: return launch_tile<16, 32, 16, 32, 3, 8>(b_tile, p, stream);
+        case 1: return launch_tile<32, 32, 32, 32, 2, 8>(b_tile, p, stream);
+        case 2: return launch_tile<64, 32, 64, 32, 3, 4>(b_tile, p, stream);
+        case 3: return launch_tile<64, 64, 32, 32, 2, 2>(b_tile, p, stream);
+        case 4: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
+        case 5: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
+        case 6: return launch_tile<256, 256, 64, 128, 2, 1, true>(b_tile, p, stream);
         default: return hipErrorInvalidValue;
     }
 }
