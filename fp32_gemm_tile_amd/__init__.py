@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp32gemm.so")
@@ -197,6 +198,8 @@ def load_library(path: str = LIB_PATH):
     lib.fg_gemm_fp8.restype = i32
     lib.fg_gemm_fp8_workspace_size.argtypes = [i64, i64, i64]
     lib.fg_gemm_fp8_workspace_size.restype = ctypes.c_size_t
+    if _MOE_RECORD.size != ctypes.sizeof(fg_moe_layer):
+        raise ImportError("fg_moe_layer: the packed record does not match the structure")
     lib.fg_moe.argtypes = [ctypes.POINTER(fg_moe_layer), vp, ctypes.c_size_t, vp]
     lib.fg_moe.restype = i32
     lib.fg_moe_workspace_size.argtypes = [i32, i32, i32, i32, i32]
@@ -570,67 +573,85 @@ def sgemm(A, B, C, alpha=1.0, beta=0.0, transA="N", transB="N", config=-1, strea
 
 
 # ---- 8-bit matrices and mixture of experts: torch convenience --------------
+# (Short calls on purpose: a decode step's kernels take a few microseconds, and
+# so does the marshalling.)
 
-def _type(t, name):
+_codes_of = {}   # torch dtype -> fg_type, filled on first use
+
+
+def _torch_types():
     import torch
-    if t.dtype == torch.float32:
-        return FG_TYPE_F32
-    if t.dtype == torch.bfloat16:
-        return FG_TYPE_BF16
-    raise TypeError(f"{name} must be float32 or bfloat16")
+    if not _codes_of:
+        _codes_of.update({torch.float32: FG_TYPE_F32, torch.bfloat16: FG_TYPE_BF16,
+                          torch.float8_e4m3fn: FG_TYPE_E4M3, torch.uint8: FG_TYPE_E4M3})
+    return torch, _codes_of
 
 
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+def _wrong(name, what):
+    raise ValueError(f"{name} must {what}")
+
+
+def _value_type(types, t, name):
+    ty = types.get(t.dtype)
+    if ty != FG_TYPE_F32 and ty != FG_TYPE_BF16:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return ty
 
 
 def _gpu(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be on the GPU")
-    return t.device
+    return dev
 
 
-def _call_on(device, stream, fn):
-    """fn(hipStream_t) with `device` current; stream: a torch stream, an int or
-    None (torch's current stream of that device)."""
-    import torch
+def _run_on(torch, dev, stream, fn, args):
+    """fn(*args, hipStream_t) with device `dev` current; stream: a torch stream,
+    a raw handle or None (torch's current stream of that device)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if torch.cuda.current_device() == device.index:
-        _raise_if(fn(s))
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream or None)
     else:
-        with torch.cuda.device(device):
-            _raise_if(fn(s))
+        with torch.cuda.device(dev):
+            st = fn(*args, stream or None)
+    if st != FG_OK:
+        _raise_if(st)
 
 
-def _codes(t, name):
-    """Leading dimension of a 2-D tensor of codes."""
-    import torch
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+def _codes(types, t, name, dev, rows, cols):
+    """Leading dimension of a rows x cols tensor of codes."""
+    if types.get(t.dtype) != FG_TYPE_E4M3:
         raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes)")
-    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit stride along its rows")
+    if t.shape != (rows, cols) or t.get_device() != dev:
+        _wrong(name, f"be {rows} x {cols} on device {dev}, is {tuple(t.shape)} on {t.device}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        _wrong(name, "have unit stride along its rows")
     # (one row: its stride is free, and codes need a multiple of 16)
-    return t.stride(0) if t.size(0) > 1 else -(-max(1, t.size(1)) // 16) * 16
+    return ld if rows > 1 else (max(1, cols) + 15) // 16 * 16
 
 
-def _scales(t, name, blocks, outer):
+def _scales(torch, t, name, dev, blocks, outer):
     """Leading dimension of a [column blocks, rows or row blocks] tensor."""
-    import torch
     if t is None or t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32")
-    if t.dim() != 2 or t.shape[0] != blocks or t.shape[1] != outer:
-        raise ValueError(f"{name} must be {blocks} x {outer}, is {tuple(t.shape)}")
-    if outer > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    return max(t.stride(0), outer, 1) if blocks > 1 else max(outer, 1)
+    if t.shape != (blocks, outer) or t.get_device() != dev:
+        _wrong(name, f"be {blocks} x {outer} on device {dev}, is {tuple(t.shape)} on {t.device}")
+    ld, inner = t.stride()
+    if outer > 1 and inner != 1:
+        _wrong(name, "have unit stride along its rows")
+    return max(ld, outer, 1) if blocks > 1 else max(outer, 1)
 
 
-def _cdiv(a, b):
-    return -(-a // b)
+def _workspace(t, dev):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.get_device() != dev:
+        _wrong("workspace", f"be contiguous on device {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def empty_fp8(rows, cols, block="row", device="cuda"):
@@ -639,10 +660,10 @@ def empty_fp8(rows, cols, block="row", device="cuda"):
     [ceil(cols / 128), rows] ("row") or [ceil(cols / 128), ceil(rows / 128)]
     ("tile")."""
     import torch
-    wide = _cdiv(max(1, cols), 16) * 16
+    wide = (max(1, cols) + 15) // 16 * 16
     q = torch.empty(rows, wide, dtype=torch.float8_e4m3fn, device=device)[:, :cols]
-    outer = rows if _BLOCKS[block] == FG_BLOCK_ROW else _cdiv(rows, 128)
-    return q, torch.empty(_cdiv(cols, 128), outer, dtype=torch.float32, device=device)
+    outer = rows if _BLOCKS[block] == FG_BLOCK_ROW else (rows + 127) // 128
+    return q, torch.empty((cols + 127) // 128, outer, dtype=torch.float32, device=device)
 
 
 def quantize_fp8(X, Q=None, S=None, QT=None, ST=None, block="row", stream=None):
@@ -651,21 +672,25 @@ def quantize_fp8(X, Q=None, S=None, QT=None, ST=None, block="row", stream=None):
     128 x 128 block ("tile"): X's own order into Q and S, its transpose into QT
     and ST (either pair may be None; empty_fp8 makes them). X is read once.
     Enqueued on ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
     dev = _gpu(X, "X")
-    _on(dev, Q=Q, S=S, QT=QT, ST=ST)
-    ty, kind, ldx = _type(X, "X"), _BLOCKS[block], _ld(X, "X")
+    kind, ldx = _BLOCKS[block], _ld(X, "X")
     M, N = X.shape
-    args = []
-    for name, q, s, r, c in (("Q", Q, S, M, N), ("QT", QT, ST, N, M)):
-        if q is None:
-            args += [0, 0, 0, 0]
-            continue
-        if tuple(q.shape) != (r, c):
-            raise ValueError(f"{name} must be {r} x {c}, is {tuple(q.shape)}")
-        outer = r if kind == FG_BLOCK_ROW else _cdiv(r, 128)
-        args += [q.data_ptr(), _codes(q, name), s.data_ptr() if s is not None else 0,
-                 _scales(s, "S" if q is Q else "ST", _cdiv(c, 128), outer)]
-    _call_on(dev, stream, lambda st: fg_quantize_fp8(ty, kind, M, N, X.data_ptr(), ldx, *args, st))
+    q = s = qt = st = None
+    ldq = lds = ldqt = ldst = 0
+    if Q is not None:
+        ldq = _codes(types, Q, "Q", dev, M, N)
+        lds = _scales(torch, S, "S", dev, (N + 127) // 128, (M + 127) // 128 if kind else M)
+        q, s = Q.data_ptr() or None, S.data_ptr() or None
+    if QT is not None:
+        ldqt = _codes(types, QT, "QT", dev, N, M)
+        ldst = _scales(torch, ST, "ST", dev, (M + 127) // 128, (N + 127) // 128 if kind else N)
+        qt, st = QT.data_ptr() or None, ST.data_ptr() or None
+    if M == 0 or N == 0:
+        return
+    _run_on(torch, dev, stream, load_library().fg_quantize_fp8,
+            (_value_type(types, X, "X"), kind, M, N, X.data_ptr(), ldx, q, ldq, s, lds, qt, ldqt,
+             st, ldst))
 
 
 def gemm_fp8(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
@@ -675,49 +700,54 @@ def gemm_fp8(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
     contiguous GPU tensor that no call running at the same time uses
     (fg_gemm_fp8_workspace_size bytes are useful), or None. Returns C.
     Enqueued on ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
     dev = _gpu(C, "C")
-    _on(dev, A=A, SA=SA, B=B, SB=SB, workspace=workspace)
     M, N = C.shape
     K = A.shape[1]
-    if A.shape[0] != M or B.shape[0] != N or B.shape[1] != K:
-        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not give C {tuple(C.shape)}")
-    lda, ldb, ldc, tc = _codes(A, "A"), _codes(B, "B"), _ld(C, "C"), _type(C, "C")
-    kb = _cdiv(K, 128)
-    ldsa = _scales(SA, "SA", kb, M)
+    kb = (K + 127) // 128
     tile = SB.dim() == 2 and SB.shape[1] != N
-    ldsb = _scales(SB, "SB", kb, _cdiv(N, 128) if tile else N)
-    ws, ws_bytes = 0, 0
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call_on(dev, stream, lambda st: fg_gemm_fp8(
-        M, N, K, alpha, A.data_ptr(), lda, SA.data_ptr(), ldsa, B.data_ptr(), ldb, SB.data_ptr(),
-        ldsb, FG_BLOCK_TILE if tile else FG_BLOCK_ROW, beta, C.data_ptr(), ldc, tc, ws, ws_bytes,
-        st))
+    lda, ldb = _codes(types, A, "A", dev, M, K), _codes(types, B, "B", dev, N, K)
+    ldsa = _scales(torch, SA, "SA", dev, kb, M)
+    ldsb = _scales(torch, SB, "SB", dev, kb, (N + 127) // 128 if tile else N)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run_on(torch, dev, stream, load_library().fg_gemm_fp8,
+            (M, N, K, alpha, A.data_ptr() or None, lda, SA.data_ptr() or None, ldsa,
+             B.data_ptr() or None, ldb, SB.data_ptr() or None, ldsb, 1 if tile else 0, beta,
+             C.data_ptr() or None, _ld(C, "C"), _value_type(types, C, "C"), ws, ws_bytes))
     return C
 
 
-def _experts(w, scales, name, E, rows, cols):
-    """fg_experts and fg_type of an [E, rows, cols] tensor."""
-    import torch
-    if tuple(w.shape) != (E, rows, cols):
-        raise ValueError(f"{name} must be {E} x {rows} x {cols}, is {tuple(w.shape)}")
-    if cols > 1 and w.stride(2) != 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    per = 16 // w.element_size()
-    ld = w.stride(1) if rows > 1 else _cdiv(cols, per) * per
-    stride = w.stride(0) if E > 1 else 0
-    if w.dtype in (torch.float8_e4m3fn, torch.uint8):
-        if scales is None or scales.dtype != torch.float32:
-            raise TypeError(f"{name} needs float32 scales")
-        kb, rb = _cdiv(cols, 128), _cdiv(rows, 128)
-        if tuple(scales.shape) != (E, kb, rb) or (rb > 1 and scales.stride(2) != 1):
-            raise ValueError(f"scales of {name} must be {E} x {kb} x {rb} with unit inner stride")
-        return FG_TYPE_E4M3, fg_experts(w.data_ptr(), ld, stride, scales.data_ptr(),
-                                        scales.stride(1) if kb > 1 else rb,
-                                        scales.stride(0) if E > 1 else 0)
-    return _type(w, name), fg_experts(w.data_ptr(), ld, stride, None, 0, 0)
+# fg_moe_layer as one packed record (quicker than a ctypes constructor)
+_MOE_RECORD = struct.Struct("@9iPq" + 3 * "PqqPqq" + "PqiPPPq")
+
+
+def _experts(torch, types, w, s, name, dev, E, R, C):
+    """fg_type and the values of fg_experts of an [E, R, C] tensor."""
+    if w.shape != (E, R, C) or w.get_device() != dev:
+        _wrong(name, f"be {E} x {R} x {C} on device {dev}, is {tuple(w.shape)} on {w.device}")
+    ty = types.get(w.dtype)
+    if ty is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or e4m3 codes")
+    stride, ld, inner = w.stride()
+    if C > 1 and inner != 1:
+        _wrong(name, "have unit stride along its rows")
+    if R == 1:
+        per = 16 // w.element_size()
+        ld = (C + per - 1) // per * per
+    if E == 1:
+        stride = 0
+    if ty != FG_TYPE_E4M3:
+        return ty, (w.data_ptr(), ld, stride, 0, 0, 0)
+    if s is None or s.dtype != torch.float32:
+        raise TypeError(f"{name} needs float32 scales")
+    kb, rb = (C + 127) // 128, (R + 127) // 128
+    if s.shape != (E, kb, rb) or s.get_device() != dev:
+        _wrong(f"scales of {name}", f"be {E} x {kb} x {rb} on device {dev}")
+    sstride, lds, inner = s.stride()
+    if rb > 1 and inner != 1:
+        _wrong(f"scales of {name}", "have unit inner stride")
+    return ty, (w.data_ptr(), ld, stride, s.data_ptr(), lds if kb > 1 else rb,
+                sstride if E > 1 else 0)
 
 
 def moe(x, gate, up, down, ids, weights, out, router=None, renormalize=True, scales=None,
@@ -733,44 +763,40 @@ def moe(x, gate, up, down, ids, weights, out, router=None, renormalize=True, sca
     at least fg_moe_workspace_size(T, k, E, H, I) bytes that no call running at
     the same time uses; None allocates one with torch. Returns out. Enqueued on
     ``stream`` (default: torch's current stream)."""
-    import torch
+    torch, types = _torch_types()
     dev = _gpu(x, "x")
     T, H = x.shape
     E, I = gate.shape[0], gate.shape[1]
     sg, su, sd = scales if scales is not None else (None, None, None)
-    _on(dev, gate=gate, up=up, down=down, ids=ids, weights=weights, out=out, router=router,
-        workspace=workspace, **{"scales[0]": sg, "scales[1]": su, "scales[2]": sd})
-    wt, g = _experts(gate, sg, "gate", E, I, H)
-    ut, u = _experts(up, su, "up", E, I, H)
-    dt, d = _experts(down, sd, "down", E, H, I)
+    wt, g = _experts(torch, types, gate, sg, "gate", dev, E, I, H)
+    ut, u = _experts(torch, types, up, su, "up", dev, E, I, H)
+    dt, d = _experts(torch, types, down, sd, "down", dev, E, H, I)
     if not wt == ut == dt:
         raise TypeError("gate, up and down must have one type")
-    if tuple(out.shape) != (T, H) or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and type")
-    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous():
-        raise ValueError("ids must be a contiguous int32 tensor of T rows")
+    if out.shape != (T, H) or out.dtype != x.dtype or out.get_device() != dev:
+        _wrong("out", "have x's shape, type and device")
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 \
+            or not ids.is_contiguous() or ids.get_device() != dev:
+        _wrong("ids", "be a contiguous int32 tensor of T rows on x's device")
     k = ids.shape[1]
-    if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32 \
-            or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 tensor of ids' shape")
-    if router is not None and tuple(router.shape) != (E, H):
-        raise ValueError(f"router must be {E} x {H}")
-    layer = fg_moe_layer(T, E, k, H, I, _type(x, "x"), wt, activation_code(activation),
-                         int(bool(renormalize)), x.data_ptr() or None, _ld(x, "x"), g, u, d,
-                         router.data_ptr() if router is not None else None,
-                         _ld(router, "router") if router is not None else 0,
-                         _type(router, "router") if router is not None else 0,
-                         ids.data_ptr() or None, weights.data_ptr() or None,
-                         out.data_ptr() or None, _ld(out, "out"))
+    if weights.shape != (T, k) or weights.dtype != torch.float32 \
+            or not weights.is_contiguous() or weights.get_device() != dev:
+        _wrong("weights", "be a contiguous float32 tensor of ids' shape on x's device")
+    rt = rp = ldr = 0
+    if router is not None:
+        if router.shape != (E, H) or router.get_device() != dev:
+            _wrong("router", f"be {E} x {H} on x's device")
+        rt, rp, ldr = _value_type(types, router, "router"), router.data_ptr(), _ld(router, "router")
     if workspace is None:
         if stream is not None and not hasattr(stream, "cuda_stream"):
             raise ValueError("a raw stream handle needs a workspace")
         need = fg_moe_workspace_size(T, k, E, H, I)
-        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
-                               else torch.cuda.current_stream(dev)):
-            workspace = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _call_on(dev, stream, lambda st: fg_moe(layer, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), st))
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            workspace = torch.empty(max(16, need), dtype=torch.uint8, device=x.device)
+    ws, ws_bytes = _workspace(workspace, dev)
+    layer = fg_moe_layer.from_buffer_copy(_MOE_RECORD.pack(
+        T, E, k, H, I, _value_type(types, x, "x"), wt, activation_code(activation),
+        1 if renormalize else 0, x.data_ptr(), _ld(x, "x"), *g, *u, *d, rp, ldr, rt,
+        ids.data_ptr(), weights.data_ptr(), out.data_ptr(), _ld(out, "out")))
+    _run_on(torch, dev, stream, load_library().fg_moe, (layer, ws, ws_bytes))
     return out
