@@ -146,7 +146,6 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
     p.ldst = ldst;
     p.bf16 = type == FG_TYPE_BF16;
     p.tile = tile;
-    p.vec = ldx % 4 == 0 && aligned(X, 4 * (uintptr_t)type_size(type));
     return launched(fg::launch_quantize_fp8(p, stream), "quantisation kernel");
 }
 

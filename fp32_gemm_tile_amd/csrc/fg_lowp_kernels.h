@@ -27,7 +27,6 @@ struct QuantParams {
     int64_t ldst;
     int32_t bf16;   // X is bfloat16
     int32_t tile;   // 128 x 128 blocks
-    int32_t vec;    // rows of X start aligned to 4 elements
 };
 hipError_t launch_quantize_fp8(const QuantParams& p, hipStream_t stream);
 

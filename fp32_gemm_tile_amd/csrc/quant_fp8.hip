@@ -4,15 +4,20 @@
 //   s = max(fl32(max|x| / 448), 2^-126),  code = e4m3 nearest to x / s
 //
 // Bound by HBM: 4 or 2 bytes read and 1 written per element and order, so X is
-// read once for both orders. The code is the one nearest to the exact
-// quotient, which costs a handful of instructions per element:
-// with s = 2^e s', s' in [1, 2), x' = x 2^-e (exact) and r = fl(1 / s'), the
-// quotient q = x' r is corrected once with its exact remainder, q1 = q +
-// (x' - q s') r, the binary32 value nearest to x'/s' (A. Markstein, "IA-64 and
-// Elementary Functions", theorem on correctly rounded quotients). Rounding q1
-// to e4m3 equals rounding x'/s' unless q1 is the middle of two codes, which
-// ends in 19 zero bits; there the sign of the remainder moves q1 by one unit
-// in the last place to the side the exact quotient is on.
+// read once for both orders; next by the vector ALU, hence the few instructions
+// per element. Measured: 8192 x 8192 binary32 in both orders 76 us, 5.3 TB/s, the
+// vector ALU 62 % busy (148 us with an exact division per element); a row of 4096
+// bfloat16 3.6 us, a launch's own time; 3001 x 2047 bfloat16 both ways 18.5 us, a
+// single round of tiles, whose chain of load, two folds, division and LDS exchange
+// nothing covers. The code is the one nearest to the exact quotient: with s = 2^e
+// s', s' in [1, 2), and r = fl(1 / s'), q = fl(x (2^-e r)) is within two units in
+// the last place of x / s. The middle of two codes ends in 19 zero bits, so q
+// rounds to the code that x / s does unless it is within two units of such a
+// number; only there the quotient is settled: q1 = fl(q + (x' - q s') r) with
+// x' = 2^-e x, one correction step with the exact remainder, is the binary32
+// value nearest to x'/s' up to a 2^-23rd of a unit, and if q1 is the middle
+// itself, the sign of its remainder moves it to the side the exact quotient is
+// on (a quotient that is not the middle is at least a 32nd of a unit off it).
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
 
@@ -21,102 +26,113 @@ namespace {
 
 constexpr float kTop = 448.f;
 
-// A block's scale and what dividing by it needs.
-struct Divisor {
-    float f;   // 2^-e
-    float s1;  // s * 2^-e, in [1, 2)
-    float r;   // fl(1 / s1)
-};
-
-__device__ __forceinline__ float scale_of(float amax) {
-    return fmaxf(amax / kTop, 1.17549435e-38f);
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+    return fmaxf(__builtin_bit_cast(float, amax) / kTop, 1.17549435e-38f);
 }
 
+// What dividing by a scale needs: 2^-e r, 2^-e, s' and r.
+typedef f4 Divisor;
 __device__ __forceinline__ Divisor divisor_of(float s) {
     const uint32_t u = __builtin_bit_cast(uint32_t, s);  // normal, positive, < 2^121
-    Divisor d;
-    d.f = __builtin_bit_cast(float, (254u << 23) - (u & 0x7F800000u));
-    d.s1 = __builtin_bit_cast(float, (u & 0x007FFFFFu) | 0x3F800000u);
-    d.r = 1.f / d.s1;
-    return d;
+    const float f = __builtin_bit_cast(float, (254u << 23) - (u & 0x7F800000u));
+    const float s1 = __builtin_bit_cast(float, (u & 0x007FFFFFu) | 0x3F800000u);
+    const float r = 1.f / s1;
+    return Divisor{f * r, f, s1, r};
 }
 
-__device__ __forceinline__ float quotient(float xf, const Divisor& d) {
-    const float q = xf * d.r;
-    return fmaf(fmaf(-q, d.s1, xf), d.r, q);
-}
-
-// q1 moved off the middle of two codes when the exact quotient is not there;
-// a zero with x's sign, which the correction lost.
-__device__ __forceinline__ float settle(float q, float xf, const Divisor& d) {
-    const float rem = fmaf(-q, d.s1, xf);
+// The quotient x / s as described above (a zero with x's sign).
+__device__ __forceinline__ float settle(float x, const Divisor& d) {
+    const float xf = x * d[1];
+    float q = xf * d[3];
+    q = fmaf(fmaf(-q, d[2], xf), d[3], q);
+    const float rem = fmaf(-q, d[2], xf);
     uint32_t u = __builtin_bit_cast(uint32_t, q);
     if ((u & 0x7FFFFu) == 0 && rem != 0.f)  // (a NaN's bits are not all 0)
         u += ((rem > 0.f) == (q > 0.f)) ? 1u : 0xFFFFFFFFu;
-    return q == 0.f ? copysignf(0.f, xf) : __builtin_bit_cast(float, u);
+    return q == 0.f ? copysignf(0.f, x) : __builtin_bit_cast(float, u);
 }
 
-// Codes of four elements, in one dword. d[i] divides x[i].
-__device__ __forceinline__ uint32_t codes4(const f4& x, const Divisor& d0, const Divisor& d1,
-                                           const Divisor& d2, const Divisor& d3) {
-    const float x0 = x[0] * d0.f, x1 = x[1] * d1.f, x2 = x[2] * d2.f, x3 = x[3] * d3.f;
-    float q0 = quotient(x0, d0), q1 = quotient(x1, d1), q2 = quotient(x2, d2),
-          q3 = quotient(x3, d3);
-    const uint32_t m0 = __builtin_bit_cast(uint32_t, q0) & 0x7FFFFu,
-                   m1 = __builtin_bit_cast(uint32_t, q1) & 0x7FFFFu,
-                   m2 = __builtin_bit_cast(uint32_t, q2) & 0x7FFFFu,
-                   m3 = __builtin_bit_cast(uint32_t, q3) & 0x7FFFFu;
-    const uint32_t a = m0 < m1 ? m0 : m1, b = m2 < m3 ? m2 : m3;
-    if ((a < b ? a : b) == 0) {
-        q0 = settle(q0, x0, d0);
-        q1 = settle(q1, x1, d1);
-        q2 = settle(q2, x2, d2);
-        q3 = settle(q3, x3, d3);
+// At most 4 when q is within two units in the last place of a number that ends
+// in 19 zero bits. Below 2^-10 (zeros among them) and above 432 (the block's
+// largest element among them, at 448) there is no middle: magnitudes are clamped
+// to numbers of those ranges that do not end so.
+__device__ __forceinline__ uint32_t near_middle(float q) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, q) & 0x7FFFFFFFu;
+    constexpr uint32_t kLow = 0x3A040000u, kHigh = 0x43DC0000u;  // 1.03 * 2^-11, 440
+    return (min(max(u, kLow), kHigh) + 2u) & 0x7FFFFu;
+}
+
+// The same for q whose codes have four bits (2^-6 and more), where those numbers
+// are the codes themselves, which need no care, and the middles between them.
+__device__ __forceinline__ bool not_near_code(float q) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, q) & 0x7FFFFFFFu;
+    return u < 0x3C800000u || ((u + 2u) & 0x80000u) != 0;
+}
+
+// Codes of four elements, in one dword; r(i) is the divisor's 2^-e r for x[i] and
+// d(i) the whole of it, fetched only to settle.
+template <typename R, typename D>
+__device__ __forceinline__ uint32_t codes4(const f4& x, R r, D d) {
+    float q[4];
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = x[i] * r(i);
+        m[i] = near_middle(q[i]);
     }
-    int c = __builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q2, q3, c, true);
+    if (min(min(m[0], m[1]), min(m[2], m[3])) <= 4u) {
+        // (elements and largest elements of few bits have many quotients that
+        // are codes: 3001 x 2047 bfloat16 spent half its instructions on them)
+        bool need = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) need |= m[i] <= 4u && not_near_code(q[i]);
+        if (need) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = settle(x[i], d(i));
+        }
+    }
+    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], c, true);
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a < __builtin_inff() ? a : 0.f;  // NaN and infinities: 0
+// Magnitudes as bits, whose order is that of the values (NaN and infinities at
+// the top): an integer maximum needs no care for NaN.
+constexpr uint32_t kInf = 0x7F800000u;
+__device__ __forceinline__ uint32_t magnitude(float x) {
+    return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+    const uint32_t m = magnitude(x);
+    return m < kInf ? m : 0u;
 }
 
-// Largest finite magnitude of four elements and m. fmaxf drops NaN by itself;
-// an infinity takes the slow way.
-__device__ __forceinline__ float amax4(float m, const f4& x) {
-    const float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    if (a == __builtin_inff())
-        return fmaxf(m, fmaxf(fmaxf(finite_abs(x[0]), finite_abs(x[1])),
-                              fmaxf(finite_abs(x[2]), finite_abs(x[3]))));
-    return fmaxf(m, a);
-}
-
-// Elements (row, col .. col + 3); past the matrix they read as 0.
+// Elements (row, col .. col + 3); past the matrix they read as 0. Rows may begin
+// at any element: the loads are wide but ask for no more than its alignment.
 template <bool BF16>
 __device__ __forceinline__ f4 load4(const QuantParams& p, int64_t row, int col) {
     f4 v = {0.f, 0.f, 0.f, 0.f};
     if (row >= p.M || col >= p.N) return v;
     if constexpr (BF16) {
         const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ldx + col;
-        if (p.vec && col + 4 <= p.N) {
-            const uint2 u = *reinterpret_cast<const uint2*>(x);
+        if (col + 4 <= p.N) {
+            uint2 u;
+            __builtin_memcpy(&u, x, sizeof(u));
             v[0] = __builtin_bit_cast(float, u.x << 16);
             v[1] = __builtin_bit_cast(float, u.x & 0xFFFF0000u);
             v[2] = __builtin_bit_cast(float, u.y << 16);
             v[3] = __builtin_bit_cast(float, u.y & 0xFFFF0000u);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 if (col + i < p.N) v[i] = __builtin_bit_cast(float, (uint32_t)x[i] << 16);
         }
     } else {
         const float* x = static_cast<const float*>(p.x) + row * p.ldx + col;
-        if (p.vec && col + 4 <= p.N) {
-            v = *reinterpret_cast<const f4*>(x);
+        if (col + 4 <= p.N) {
+            __builtin_memcpy(&v, x, sizeof(v));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 if (col + i < p.N) v[i] = x[i];
         }
     }
@@ -132,145 +148,170 @@ __device__ __forceinline__ void store_codes4(uint8_t* q, uint32_t c, int left) {
 }
 
 // 1 x 128 blocks, own order only: half a wave per block, 4 elements per lane,
-// 32 rows by 128 columns per workgroup and step.
+// 32 rows by 128 columns per workgroup.
 template <bool BF16>
-__global__ void __launch_bounds__(256) quant_rows_kernel(QuantParams p) {
+__global__ void __launch_bounds__(256) quant_rows_kernel(QuantParams p, int64_t first) {
     const int l = threadIdx.x & 31, hw = threadIdx.x >> 5;
     const int nb = (p.N + kScaleBlock - 1) / kScaleBlock;
-    const int64_t tiles = (int64_t)((p.M + 31) / 32) * nb;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t row0 = t / nb * 32 + hw;
-        const int b = (int)(t % nb);
-        const int col = b * kScaleBlock + 4 * l;
-        f4 v[4];
+    const int64_t t = first + blockIdx.x;
+    const int64_t row0 = t / nb * 32 + hw;
+    const int b = (int)(t % nb);
+    const int col = b * kScaleBlock + 4 * l;
+    f4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = load4<BF16>(p, row0 + 8 * i, col);
-        float m[4];
+    for (int i = 0; i < 4; ++i) v[i] = load4<BF16>(p, row0 + 8 * i, col);
+    uint32_t m[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = amax4(0.f, v[i]);
+    for (int i = 0; i < 4; ++i) {
+        m[i] = max(max(magnitude(v[i][0]), magnitude(v[i][1])),
+                   max(magnitude(v[i][2]), magnitude(v[i][3])));
+        if (m[i] >= kInf)
+            m[i] = max(max(finite_magnitude(v[i][0]), finite_magnitude(v[i][1])),
+                       max(finite_magnitude(v[i][2]), finite_magnitude(v[i][3])));
+    }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __shfl_xor(m[i], o, 64));
+        for (int i = 0; i < 4; ++i) m[i] = max(m[i], (uint32_t)__shfl_xor((int)m[i], o, 64));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = row0 + 8 * i;
-            const float s = scale_of(m[i]);
-            const Divisor d = divisor_of(s);
-            const uint32_t c = codes4(v[i], d, d, d, d);
-            if (row < p.M) {
-                if (col < p.N) store_codes4(p.q + row * p.ldq + col, c, p.N - col);
-                if (l == 0) p.s[b * p.lds + row] = s;
-            }
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + 8 * i;
+        const float s = scale_of(m[i]);
+        const Divisor d = divisor_of(s);
+        const uint32_t c = codes4(v[i], [&](int) { return d[0]; }, [&](int) { return d; });
+        if (row < p.M) {
+            if (col < p.N) store_codes4(p.q + row * p.ldq + col, c, p.N - col);
+            if (l == 0) p.s[b * p.lds + row] = s;
         }
     }
 }
 
-// A 128 x 128 tile per workgroup: half wave hw holds rows 16 hw .. 16 hw + 15,
-// lane l columns 4 l .. 4 l + 3, so that a lane owns 16 consecutive bytes of
-// four rows of the transposed codes; those go through LDS and leave as whole
-// 128-byte rows.
+// A 128 x 128 tile per workgroup of 16 waves: half wave hw holds rows 4 hw ..
+// 4 hw + 3, lane l columns 4 l .. 4 l + 3, so that a lane owns a dword of four
+// rows of the codes and of four rows of the transposed codes; the latter go
+// through LDS and leave as whole 128-byte rows. (With 4 waves and 64 elements
+// per lane the unrolled code was 20 KB, and fetching it took most of the time:
+// 3001 x 2047 28 us.) No loop over tiles: what it kept in registers cost a second
+// workgroup on the CU (104 us at 8192 x 8192).
+constexpr int kTileThreads = 1024;
 template <bool BF16, bool TILE>
-__global__ void __launch_bounds__(256) quant_tile_kernel(QuantParams p) {
+__global__ void __launch_bounds__(kTileThreads) quant_tile_kernel(QuantParams p, int64_t first) {
+    // Transposed codes: row c (a column of the tile) at c * kPitch, its 16-byte
+    // chunk k at position k ^ ((c >> 4) & 7), which spreads the lanes' dwords
+    // over the banks.
     constexpr int kPitch = 128 + 16;
     __shared__ __attribute__((aligned(16))) uint8_t codes_t[128 * kPitch];
-    __shared__ float row_part[128];
-    __shared__ __attribute__((aligned(16))) float col_part[8][128];
-    __shared__ float row_s[128], col_s[128];
-    const int tid = threadIdx.x;
+    __shared__ uint32_t row_part[128];
+    __shared__ __attribute__((aligned(16))) uint32_t col_part[16][128];
+    __shared__ Divisor row_d[128], col_d[128];
+    __shared__ __attribute__((aligned(16))) float row_r[128], col_r[128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l = tid & 31, hw = tid >> 5;
-    const int nb = (p.N + 127) / 128, mb = (p.M + 127) / 128;
-    const int64_t tiles = (int64_t)nb * mb;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int bm = (int)(t / nb), bn = (int)(t % nb);
-        const int64_t row0 = (int64_t)bm * 128 + 16 * hw;
-        const int col0 = bn * 128, col = col0 + 4 * l;
-        f4 v[16];
+    const int nb = (p.N + 127) / 128;
+    const int64_t t = first + blockIdx.x;
+    const int bm = (int)(t / nb), bn = (int)(t % nb);
+    const int64_t row0 = (int64_t)bm * 128 + 4 * hw;
+    const int col0 = bn * 128, col = col0 + 4 * l;
+    f4 v[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = load4<BF16>(p, row0 + i, col);
-        f4 cm = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 4; ++i) v[i] = load4<BF16>(p, row0 + i, col);
+    uint32_t rm[4], cm[4];
+    auto maxima = [&](auto of) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float m = amax4(0.f, v[i]);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-            if (l == 0) row_part[16 * hw + i] = m;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cm[j] = fmaxf(cm[j], finite_abs(v[i][j]));
+        for (int i = 0; i < 4; ++i) {
+            rm[i] = max(max(of(v[i][0]), of(v[i][1])), max(of(v[i][2]), of(v[i][3])));
+            cm[i] = max(max(of(v[0][i]), of(v[1][i])), max(of(v[2][i]), of(v[3][i])));
         }
-        *reinterpret_cast<f4*>(&col_part[hw][4 * l]) = cm;
+    };
+    maxima([](float x) { return magnitude(x); });
+    if (max(max(rm[0], rm[1]), max(rm[2], rm[3])) >= kInf)
+        maxima([](float x) { return finite_magnitude(x); });
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rm[i] = max(rm[i], (uint32_t)__shfl_xor((int)rm[i], o, 64));
+    if (l == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row_part[4 * hw + i] = rm[i];
+    }
+    if constexpr (!TILE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32, 64));
+        if (lane < 32)
+            *reinterpret_cast<uint4*>(&col_part[wave][4 * l]) =
+                make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    }
+    __syncthreads();
+    if constexpr (TILE) {
+        // every wave folds the 128 row maxima
+        uint32_t m = max(row_part[lane], row_part[64 + lane]);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        const float s = scale_of(m);
+        if (tid < 128) {
+            const Divisor d = divisor_of(s);
+            row_d[tid] = col_d[tid] = d;
+            row_r[tid] = col_r[tid] = d[0];
+        }
+        if (tid == 0) {
+            if (p.q) p.s[bn * p.lds + bm] = s;
+            if (p.qt) p.st[bm * p.ldst + bn] = s;
+        }
+    } else if (tid < 256) {
+        // waves 0 and 1: the rows' scales, 2 and 3: the columns'
+        const bool rows = tid < 128;
+        const int c = tid & 127;
+        uint32_t m = rows ? row_part[c] : 0u;
+        if (!rows) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = max(m, col_part[i][c]);
+        }
+        const float s = scale_of(m);
+        const Divisor d = divisor_of(s);
+        (rows ? row_d : col_d)[c] = d;
+        (rows ? row_r : col_r)[c] = d[0];
+        const int64_t row = (int64_t)bm * 128 + c;
+        if (rows && p.q && row < p.M) p.s[bn * p.lds + row] = s;
+        if (!rows && p.qt && col0 + c < p.N) p.st[bm * p.ldst + col0 + c] = s;
+    }
+    __syncthreads();
+    if (p.q) {
+        const f4 r = *reinterpret_cast<const f4*>(&row_r[4 * hw]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = codes4(v[i], [&](int) { return r[i]; },
+                                      [&](int) { return row_d[4 * hw + i]; });
+            if (row0 + i < p.M && col < p.N)
+                store_codes4(p.q + (row0 + i) * p.ldq + col, c, p.N - col);
+        }
+    }
+    if (p.qt) {
+        const f4 r = *reinterpret_cast<const f4*>(&col_r[4 * l]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f4 x = {v[0][j], v[1][j], v[2][j], v[3][j]};
+            const int at = (4 * l + j) * kPitch + (((hw >> 2) ^ ((l >> 2) & 7)) << 4) + 4 * (hw & 3);
+            *reinterpret_cast<uint32_t*>(&codes_t[at]) =
+                codes4(x, [&](int) { return r[j]; }, [&](int) { return col_d[4 * l + j]; });
+        }
         __syncthreads();
-        if constexpr (TILE) {
-            // every thread folds the 128 row maxima (LDS broadcasts)
-            float m = fmaxf(row_part[tid & 63], row_part[64 + (tid & 63)]);
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-            const float s = scale_of(m);
-            if (tid < 128) {
-                row_s[tid] = s;
-                col_s[tid] = s;
-            }
-            if (tid == 0) {
-                if (p.q) p.s[bn * p.lds + bm] = s;
-                if (p.qt) p.st[bm * p.ldst + bn] = s;
-            }
-        } else if (tid < 128) {
-            const float s = scale_of(row_part[tid]);
-            row_s[tid] = s;
-            const int64_t row = (int64_t)bm * 128 + tid;
-            if (p.q && row < p.M) p.s[bn * p.lds + row] = s;
-        } else {
-            const int c = tid - 128;
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, col_part[i][c]);
-            const float s = scale_of(m);
-            col_s[c] = s;
-            if (p.qt && col0 + c < p.N) p.st[bm * p.ldst + col0 + c] = s;
-        }
-        __syncthreads();
-        if (p.q) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const Divisor d = divisor_of(row_s[16 * hw + i]);
-                const uint32_t c = codes4(v[i], d, d, d, d);
-                if (row0 + i < p.M && col < p.N)
-                    store_codes4(p.q + (row0 + i) * p.ldq + col, c, p.N - col);
-            }
-        }
-        if (p.qt) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Divisor d = divisor_of(col_s[4 * l + j]);
-                uint32_t c[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f4 x = {v[4 * i][j], v[4 * i + 1][j], v[4 * i + 2][j], v[4 * i + 3][j]};
-                    c[i] = codes4(x, d, d, d, d);
-                }
-                *reinterpret_cast<uint4*>(&codes_t[(4 * l + j) * kPitch + 16 * hw]) =
-                    make_uint4(c[0], c[1], c[2], c[3]);
-            }
-            __syncthreads();
-            const int rows_left = p.M - bm * 128;  // codes of a transposed row that exist
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = tid + 256 * i, c = u >> 3, k = (u & 7) * 16;
-                const uint4 w = *reinterpret_cast<const uint4*>(&codes_t[c * kPitch + k]);
-                if (col0 + c < p.N && k < rows_left) {
-                    uint8_t* q = p.qt + (int64_t)(col0 + c) * p.ldqt + (int64_t)bm * 128 + k;
-                    if (k + 16 <= rows_left) {
-                        *reinterpret_cast<uint4*>(q) = w;
-                    } else {
-                        const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (k + e < rows_left) q[e] = (uint8_t)(d[e >> 2] >> (8 * (e & 3)));
-                    }
+        const int rows_left = p.M - bm * 128;  // codes of a transposed row that exist
+        const int c = tid >> 3, k = (tid & 7) * 16;
+        const uint4 w = *reinterpret_cast<const uint4*>(
+            &codes_t[c * kPitch + (((tid & 7) ^ ((c >> 4) & 7)) << 4)]);
+        if (col0 + c < p.N && k < rows_left) {
+            uint8_t* q = p.qt + (int64_t)(col0 + c) * p.ldqt + (int64_t)bm * 128 + k;
+            if (k + 16 <= rows_left) {
+                *reinterpret_cast<uint4*>(q) = w;
+            } else {
+                const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t b = e == 0 ? d[0] : (e == 1 ? d[1] : (e == 2 ? d[2] : d[3]));
+                    store_codes4(q + 4 * e, b, rows_left - k - 4 * e);
                 }
             }
         }
-        __syncthreads();  // the next tile reuses the LDS arrays
     }
 }
 
@@ -278,23 +319,16 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(QuantParams p) {
 
 hipError_t launch_quantize_fp8(const QuantParams& p, hipStream_t stream) {
     const int64_t nb = ((int64_t)p.N + 127) / 128;
-    constexpr int64_t kMaxGrid = 1 << 20;  // the kernels stride over the rest
-    if (!p.qt && !p.tile) {
-        const int64_t tiles = ((int64_t)p.M + 31) / 32 * nb;
-        const dim3 g((unsigned)(tiles < kMaxGrid ? tiles : kMaxGrid));
-        if (p.bf16) hipLaunchKernelGGL(quant_rows_kernel<true>, g, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL(quant_rows_kernel<false>, g, dim3(256), 0, stream, p);
-    } else {
-        const int64_t tiles = ((int64_t)p.M + 127) / 128 * nb;
-        const dim3 g((unsigned)(tiles < kMaxGrid ? tiles : kMaxGrid));
-        if (p.bf16 && p.tile)
-            hipLaunchKernelGGL((quant_tile_kernel<true, true>), g, dim3(256), 0, stream, p);
-        else if (p.bf16)
-            hipLaunchKernelGGL((quant_tile_kernel<true, false>), g, dim3(256), 0, stream, p);
-        else if (p.tile)
-            hipLaunchKernelGGL((quant_tile_kernel<false, true>), g, dim3(256), 0, stream, p);
-        else
-            hipLaunchKernelGGL((quant_tile_kernel<false, false>), g, dim3(256), 0, stream, p);
+    constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of one launch
+    const bool rows = !p.qt && !p.tile;
+    const int rows_per_wg = rows ? 32 : 128, threads = rows ? 256 : kTileThreads;
+    auto kernel = p.bf16 ? quant_rows_kernel<true> : quant_rows_kernel<false>;
+    if (!rows && p.tile) kernel = p.bf16 ? quant_tile_kernel<true, true> : quant_tile_kernel<false, true>;
+    else if (!rows) kernel = p.bf16 ? quant_tile_kernel<true, false> : quant_tile_kernel<false, false>;
+    const int64_t tiles = ((int64_t)p.M + rows_per_wg - 1) / rows_per_wg * nb;
+    for (int64_t first = 0; first < tiles; first += kMaxGrid) {
+        const int64_t n = tiles - first < kMaxGrid ? tiles - first : kMaxGrid;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(threads), 0, stream, p, first);
     }
     return hipGetLastError();
 }
