@@ -65,10 +65,13 @@ struct Plan {
 // The cheapest by estimate: rounds of one workgroup per CU, each taking the
 // blocks of K one after the other, or the stream of both operands; slices of K
 // (at most 16) cost another kernel and their partial sums' way to memory and
-// back.
+// back. Slices pay for small results of long sums (bfloat16 C, the best tile each:
+// 256 x 256 x 65536 33.9 us in one slice, 21.8 in four; 1024 x 1024 x 65536 348
+// and 91 in sixteen), and cost where a sum is short (512 x 512 x 16384 16.8 us in
+// one, 22.0 in two).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
-    constexpr double kFinish = 3.2;
+    constexpr double kFinish = 7;
     const int64_t kb = cdiv(K, fg::kScaleBlock);
     const double stream = ((double)M * K + (double)N * K) / kStream;
     const double slice = (double)M * N * 4;
@@ -83,7 +86,8 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
             const int64_t per = cdiv(kb, n), used = cdiv(kb, per);
             if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
             const double rounds = std::ceil(tiles * (double)n / kCUs);
-            double us = sh.fixed_us + std::max(rounds * (double)per * per_block, stream);
+            const double share = sh.stream * std::min(1.0, tiles * (double)n / kCUs);
+            double us = sh.fixed_us + std::max(rounds * (double)per * per_block, stream / share);
             if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
             if (best.shape < 0 || us < best_us) {
                 best = Plan{s, n};

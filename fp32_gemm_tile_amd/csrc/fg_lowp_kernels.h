@@ -53,6 +53,7 @@ struct Fp8Shape {
     float fixed_us;  // start and end
     float bf16_us, f32_us;  // per block of K and round of 256 workgroups, by C's
                             // type (0: not built)
+    float stream;           // share of the memory's rate that 256 workgroups draw
 };
 int fp8_num_shapes();
 Fp8Shape fp8_shape(int shape);

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int kStage = (BM + BN) * 128;
     // (scales come 64 at a time)
-    constexpr int kScalesA = BM < 64 ? 64 : BM, kScalesB = BN < 64 ? 64 : BN;
+    constexpr int kScalesA = (BM + 63) / 64 * 64, kScalesB = (BN + 63) / 64 * 64;
     constexpr int kScales = kScalesA + (B_TILE ? 0 : kScalesB);
     __shared__ __attribute__((aligned(128))) uint8_t all_lds[KG * NS * kStage];
     __shared__ __attribute__((aligned(16))) float all_scales[KG * NS * kScales];
@@ -494,20 +494,29 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The tile shapes, with what one costs (fp8_estimate): microseconds for a start
-// and end, and per block of K while 256 workgroups run, for bfloat16 and for
-// binary32 C. Measured on one MI355X (slopes over K at full grids);
-// rows of small results: many groups of K, so that the whole of a CU's LDS is in
-// flight (1 x 8192 x 8192 11.4 us = 5.9 TB/s, 32 x 8192 x 8192 13.1 us; with
-// the 64 x 64 tile and four slices of K 17.4 and 18.4).
+// The tile shapes, with what one costs by estimate: microseconds for a start and
+// end, and per block of K and round of 256 workgroups, for bfloat16 and for
+// binary32 C, and the share of the memory's rate that its loads in flight draw
+// (fits to 16 .. 1024 x 4096 x 2048 and 1 .. 1024 x 8192 x 8192 on one MI355X).
+//   The tiles of up to 64 x 32 are for few rows: many groups of K, so that the
+// whole of a CU's LDS is in flight (bfloat16, 1 x 8192 x 8192 11.5 us = 5.8 TB/s;
+// 32 rows 13.1 us, 64 rows 14.8, with the 64 x 64 tile 32).
+//   The tiles between 64 x 64 and 128 x 128 save results that a smaller tile
+// takes in two rounds and a larger one in less than one (binary32 C):
+// 517 x 2047 x 3001 80 x 64 15.6 us, 64 x 64 19.7, 128 x 128 29.4;
+// 2048 x 1024 x 1024 128 x 64 9.3 us, 64 x 64 9.9, 128 x 128 12.1;
+// 600 x 4096 x 4096 160 x 64 26.8 us, 64 x 64 36.2, 128 x 128 34.5.
 constexpr Fp8Shape kShapes[] = {
-    {16, 32, 4.5f, 0.07f, 0.08f},
-    {32, 32, 4.5f, 0.18f, 0.21f},
-    {64, 32, 4.5f, 0.20f, 0.26f},
-    {64, 64, 4.7f, 0.25f, 0.34f},
-    {128, 128, 5.7f, 0.66f, 1.15f},
-    {256, 128, 7.5f, 1.08f, 2.1f},
-    {256, 256, 10.f, 1.7f, 0.f},  // bfloat16 C only
+    {16, 32, 3.0f, 0.088f, 0.093f, 1.f},
+    {32, 32, 3.0f, 0.11f, 0.127f, 1.f},
+    {64, 32, 3.2f, 0.155f, 0.24f, 1.f},
+    {64, 64, 3.5f, 0.26f, 0.37f, 0.38f},
+    {80, 64, 3.5f, 0.33f, 0.42f, 1.f},
+    {128, 64, 3.7f, 0.52f, 0.61f, 1.f},
+    {160, 64, 3.8f, 0.58f, 0.71f, 1.f},
+    {128, 128, 4.5f, 0.64f, 0.95f, 1.f},
+    {256, 128, 6.0f, 1.0f, 1.87f, 1.f},
+    {256, 256, 10.f, 1.7f, 0.f, 1.f},  // bfloat16 C only
 };
 
 }  // namespace
@@ -521,9 +530,12 @@ hipError_t launch_gemm_fp8(int shape, bool b_tile, const Fp8Params& p, hipStream
         case 1: return launch_tile<32, 32, 32, 32, 2, 8>(b_tile, p, stream);
         case 2: return launch_tile<64, 32, 64, 32, 3, 4>(b_tile, p, stream);
         case 3: return launch_tile<64, 64, 32, 32, 2, 2>(b_tile, p, stream);
-        case 4: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
-        case 5: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
-        case 6: return launch_tile<256, 256, 64, 128, 2, 1, true>(b_tile, p, stream);
+        case 4: return launch_tile<80, 64, 80, 32, 2, 4>(b_tile, p, stream);
+        case 5: return launch_tile<128, 64, 64, 32, 2, 2>(b_tile, p, stream);
+        case 6: return launch_tile<160, 64, 80, 32, 2, 2>(b_tile, p, stream);
+        case 7: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
+        case 8: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
+        case 9: return launch_tile<256, 256, 64, 128, 2, 1, true>(b_tile, p, stream);
         default: return hipErrorInvalidValue;
     }
 }
