@@ -598,7 +598,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t expert_rows(const ExpertMatrix
 // the steps of K in turn. A wave keeps the operands of its next D - 1 steps in
 // flight while it uses the present ones.
 template <int WT, bool XBF16, int RT, int NW, int D>
-__global__ void __launch_bounds__(64 * NW, 2) gate_up_kernel(MoeParams p) {
+__global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoeParams p) {
     static_assert(NW >= 4, "the joining of the waves' sums takes 256 threads");
     using W = Weight<WT>;
     using N = Terms<WT, XBF16>;
@@ -894,11 +894,15 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_kernel(MoeParams p, i
 
 template <int WT, bool XBF16>
 hipError_t launch_experts(const MoeParams& p, hipStream_t stream) {
-    // Two workgroups of 4 waves on a CU, so that one streams while the other
-    // starts; 8 waves while that leaves CUs idle. Steps in flight: what the
-    // registers hold.
-    constexpr int RT = WT == TYPE_F32 ? 1 : 2;
-    constexpr int D = WT == TYPE_E4M3 ? 3 : 2;
+    // Workgroups of 4 waves, so that some stream while others start or join; 8
+    // waves while that leaves CUs idle. What covers the memory's latency is best
+    // kept in other workgroups (four on a CU, one step per wave) for 8- and 16-bit
+    // weights (82 experts of 4096 x 1536 e4m3 180 us against 189 with two
+    // workgroups and two steps in flight, 34 of 2048 x 1408 bfloat16 81 against
+    // 90); a step of binary32 weights takes too many registers for that (98 us for
+    // 16 of 2048 x 2000, two workgroups, two steps; 100).
+    constexpr int RT = WT == TYPE_E4M3 ? 2 : 1;
+    constexpr int D = WT == TYPE_F32 ? 2 : 1;
     const int tiles = (p.I + 16 * RT - 1) / (16 * RT);
     if ((int64_t)tiles * p.most_x >= 512)
         hipLaunchKernelGGL((gate_up_kernel<WT, XBF16, RT, 4, D>), dim3(tiles, p.most_x), dim3(256),
