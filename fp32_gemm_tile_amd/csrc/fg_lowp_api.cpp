@@ -437,6 +437,7 @@ fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_by
     p.most_x = (int32_t)most_groups(T, l.top_k, E, p.gx);
     p.most_h = (int32_t)most_groups(T, l.top_k, E, p.gh);
     p.groups_x = reinterpret_cast<fg::MoeGroup*>(ws + space.groups_x);
+    if (T == 1) p.gh = p.gx;  // (one token to a group whatever its size)
     p.groups_h =
         p.gh == p.gx ? p.groups_x : reinterpret_cast<fg::MoeGroup*>(ws + space.groups_h);
     p.down_wgs = fg::moe_down_workgroups(p.wtype, p.H, p.I, p.most_h);

@@ -413,44 +413,56 @@ __device__ __forceinline__ bool last_to_arrive(int32_t* counter, int all, int* s
     return *s_last;
 }
 
+static_assert(kPlanThreads == 2 * kMaxE, "a thread per expert and list");
 struct PlanLds {
     int ids[kMaxT * kMaxK];
     float w[kMaxT * kMaxK];
-    unsigned long long chose[kMaxE];  // the tokens that chose the expert
-    int base[kMaxE];                  // its first group
-    int wave_sum[kMaxE / 64];
+    unsigned long long chose[kMaxE];   // the tokens that chose the expert
+    int base[2][kMaxE];                // its first group, in the list for x and for h
+    int wave_sum[kPlanThreads / 64];
 };
 
-// One list from l.ids and l.chose (kPlanThreads threads).
-__device__ __forceinline__ void write_groups(const MoeParams& p, PlanLds& l, int G, int* total,
-                                             MoeGroup* out) {
-    const int tid = threadIdx.x;
-    int own = 0, sum = 0;
-    if (tid < kMaxE) {
-        sum = own = (unsigned)(__popcll(l.chose[tid]) + G - 1) / (unsigned)G;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(sum, o, 64);
-            if ((tid & 63) >= o) sum += v;
-        }
-        if ((tid & 63) == 63) l.wave_sum[tid >> 6] = sum;
+// The plan, from l.ids and l.w (kPlanThreads threads, half of them for each list);
+// the tickets of the down kernel are set to 0.
+__device__ __forceinline__ void write_plan(const MoeParams& p, PlanLds& l) {
+    const int tid = threadIdx.x, list = tid / kMaxE, e0 = tid % kMaxE;
+    if (!list) l.chose[e0] = 0;
+    for (int i = tid; i < (p.H + 15) / 16; i += kPlanThreads) p.tickets[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < p.T * p.k; i += kPlanThreads) {
+        const int e = l.ids[i];
+        if (e >= 0 && e < p.E) atomicOr(&l.chose[e], 1ull << ((unsigned)i / (unsigned)p.k));
     }
     __syncthreads();
-    if (tid < kMaxE) {
+    const bool wanted = !list || p.groups_h != p.groups_x;
+    const int G = list ? p.gh : p.gx;
+    MoeGroup* const out = list ? p.groups_h : p.groups_x;
+    const int own = (unsigned)(__popcll(l.chose[e0]) + G - 1) / (unsigned)G;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sum, o, 64);
+        if ((tid & 63) >= o) sum += v;
+    }
+    if ((tid & 63) == 63) l.wave_sum[tid >> 6] = sum;
+    __syncthreads();
 #pragma unroll 1
-        for (int w = 0; w < (tid >> 6); ++w) sum += l.wave_sum[w];
-        l.base[tid] = sum - own;
-        if (tid == kMaxE - 1) *total = sum;
+    for (int w = list * (kMaxE / 64); w < (tid >> 6); ++w) sum += l.wave_sum[w];
+    l.base[list][e0] = sum - own;
+    if (wanted) {
+        if (e0 == kMaxE - 1) *(list ? &p.plan->total_h : &p.plan->total_x) = sum;
 #pragma unroll 1
         for (int c = 0; c < own; ++c) {
             MoeGroup& m = out[sum - own + c];
-            m.expert = tid;
-            const int left = __popcll(l.chose[tid]) - c * G;
+            m.expert = e0;
+            const int left = __popcll(l.chose[e0]) - c * G;
             m.count = left < G ? left : G;
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.T * p.k; i += kPlanThreads) {
+    if (!wanted) return;
+#pragma unroll 1
+    for (int i = e0; i < p.T * p.k; i += kMaxE) {
         const int e = l.ids[i], t = (unsigned)i / (unsigned)p.k;
         if (e < 0 || e >= p.E) continue;
         float w = 0.f;
@@ -464,31 +476,10 @@ __device__ __forceinline__ void write_groups(const MoeParams& p, PlanLds& l, int
         if (!first) continue;
         const int rank = __popcll(l.chose[e] & ((1ull << t) - 1ull));
         const int c = (unsigned)rank / (unsigned)G;
-        MoeGroup& m = out[l.base[e] + c];
+        MoeGroup& m = out[l.base[list][e] + c];
         m.pair[rank - c * G] = (int16_t)i;
         m.weight[rank - c * G] = w;
     }
-    __syncthreads();
-}
-
-// The plan, from l.ids and l.w; the tickets of the down kernel are set to 0.
-__device__ __forceinline__ void write_plan(const MoeParams& p, PlanLds& l) {
-    const int tid = threadIdx.x;
-    if (tid < kMaxE) l.chose[tid] = 0;
-    for (int i = tid; i < (p.H + 15) / 16; i += kPlanThreads) p.tickets[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < p.T * p.k; i += kPlanThreads) {
-        const int e = l.ids[i];
-        if (e >= 0 && e < p.E) atomicOr(&l.chose[e], 1ull << ((unsigned)i / (unsigned)p.k));
-    }
-    __syncthreads();
-    // (one copy of the code: these kernels run each instruction about once, and
-    // fetching them is most of their time)
-    const int lists = p.groups_h != p.groups_x ? 2 : 1;
-#pragma unroll 1
-    for (int i = 0; i < lists; ++i)
-        write_groups(p, l, i ? p.gh : p.gx, i ? &p.plan->total_h : &p.plan->total_x,
-                     i ? p.groups_h : p.groups_x);
 }
 
 __device__ __forceinline__ void read_choice(const MoeParams& p, PlanLds& l) {
@@ -517,14 +508,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(MoeParams p) {
 // logit, then lower number; NaN as -inf), counted by `parts` threads against a
 // part of them each: threads = tokens * width * parts, width = the power of two
 // at or above E. A NaN logit's weight is NaN. Then the plan: one workgroup for
-// all tokens writes it from LDS, of one per token the last to finish does.
+// all tokens writes it from LDS, of one per token the last to finish does. For a
+// single token its slots are the groups, and few threads do (5.7 -> 2.7 us of 8
+// experts): LONE.
+template <bool LONE>
 __global__ void __launch_bounds__(kPlanThreads) topk_kernel(MoeParams p, int width, int tokens) {
     __shared__ PlanLds l;
     __shared__ double key[kPlanThreads], raw[kPlanThreads];  // [tokens][width]
     __shared__ int rank[kPlanThreads];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int parts = kPlanThreads / (tokens * width);
+    const int threads = LONE ? blockDim.x : kPlanThreads;
+    const int parts = threads / (tokens * width);
     const int e = tid % width, part = tid / width % parts, lt = tid / (width * parts);
     const int t0 = gridDim.x == 1 ? 0 : (int)blockIdx.x;
     const int t1 = gridDim.x == 1 ? p.T : t0 + 1;
@@ -552,7 +547,7 @@ __global__ void __launch_bounds__(kPlanThreads) topk_kernel(MoeParams p, int wid
         if (mine && part == 0 && rank[lt * width + e] < p.k)
             l.ids[t * p.k + rank[lt * width + e]] = e;
         __syncthreads();
-        for (int q = wave; q < tokens && tb + q < t1; q += kPlanThreads / 64) {  // a wave per token
+        for (int q = wave; q < tokens && tb + q < t1; q += threads / 64) {  // a wave per token
             const double* const r = raw + q * width;
             const int* const chosen = l.ids + (tb + q) * p.k;
             const double top = r[chosen[0]];
@@ -570,7 +565,19 @@ __global__ void __launch_bounds__(kPlanThreads) topk_kernel(MoeParams p, int wid
                 l.w[at] = mine_w / sum;
                 leave(p.ids + at, (int32_t)chosen[lane]);
                 leave(p.weights + at, mine_w / sum);
+                if constexpr (LONE) {
+                    MoeGroup& m = p.groups_x[lane];
+                    m.expert = chosen[lane];
+                    m.count = 1;
+                    m.pair[0] = (int16_t)lane;
+                    m.weight[0] = mine_w / sum;
+                    if (lane == 0) p.plan->total_x = p.k;
+                }
             }
+        }
+        if constexpr (LONE) {
+            for (int i = tid; i < (p.H + 15) / 16; i += threads) p.tickets[i] = 0;
+            return;
         }
         __syncthreads();
     }
@@ -943,18 +950,27 @@ void launch_logits(const MoeParams& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_moe_route(const MoeParams& p, hipStream_t stream) {
+    // One token per workgroup while all of them run at once (16 tokens of 128
+    // experts 7.6 us, four tokens per workgroup 8.2; 8 of 64 6.0 and 8.3).
     if (p.T == 1) launch_logits<1, 8>(p, stream);
+    else if ((p.E + 3) / 4 * p.T <= 512) launch_logits<1, 16>(p, stream);
     else launch_logits<4, 16>(p, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // One workgroup while its comparisons (T E^2) take less time than the
-    // arrivals of several (3 us): up to 2^17.
     int width = 8, tokens = 1;
     while (width < p.E) width *= 2;
-    const bool one = p.T == 1 || (int64_t)p.T * width * width <= 1 << 17;
+    if (p.T == 1) {
+        const int threads = std::min(kPlanThreads, std::max(64, 8 * width));
+        hipLaunchKernelGGL(topk_kernel<true>, dim3(1), dim3(threads), 0, stream, p, width, 1);
+        return hipGetLastError();
+    }
+    // One workgroup while its comparisons (T E^2) take less time than the
+    // arrivals of several: 8 tokens of 32 experts 6.2 us against 7.0, 8 of 64
+    // 7.7 both, 16 of 64 9.9 against 7.4.
+    const bool one = (int64_t)p.T * width * width < 1 << 15;
     while (one && tokens < p.T && tokens * width < kPlanThreads) tokens *= 2;
-    hipLaunchKernelGGL(topk_kernel, dim3(one ? 1 : p.T), dim3(kPlanThreads), 0, stream, p, width,
-                       tokens);
+    hipLaunchKernelGGL(topk_kernel<false>, dim3(one ? 1 : p.T), dim3(kPlanThreads), 0, stream, p,
+                       width, tokens);
     return hipGetLastError();
 }
 
