@@ -272,8 +272,11 @@ struct MoeSpace {
         groups_x = take(groups * (int64_t)sizeof(fg::MoeGroup));
         groups_h = take(groups * (int64_t)sizeof(fg::MoeGroup));
         tickets = take(cdiv(H, 16) * 4);
-        pieces = take(round_up(H, 32) * 4 * T *
-                      fg::moe_down_workgroups(fg::TYPE_E4M3, (int)H, (int)I, (int)groups));
+        int pieces_of_rows = 0;
+        for (int type : {fg::TYPE_F32, fg::TYPE_BF16, fg::TYPE_E4M3})
+            pieces_of_rows = std::max(
+                pieces_of_rows, fg::moe_down_workgroups(type, (int)H, (int)I, (int)groups));
+        pieces = take(round_up(H, 32) * 4 * T * pieces_of_rows);
         h = take(T * k * moe_h_ld(I) * 6);
         xs = take(T * moe_xs_ld(H) * 6);
         end = at;

@@ -734,14 +734,19 @@ __global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoePar
 // keeps the weights and h of its next D units in flight, over the border of two
 // groups too, and adds each group's weighted results to its own tokens x rows
 // piece in LDS. (One CU draws about 25 GB/s whatever it keeps in flight, so
-// fewer than 256 row tiles are split among several workgroups.)
-constexpr int kDownWaves = 8;
+// fewer than 256 row tiles are split among several workgroups; one on a CU is
+// best, since each has a start and a piece to join: 47, 64 and 97 us with two,
+// 41, 53 and 92 with one for 34 experts of 2048 x 1408 bfloat16, 16 of 2048 x 2000
+// binary32 and 82 of 4096 x 1536 e4m3.)
 // Output rows of a workgroup: 32 share the reads of h (e4m3: 125 -> 102 us for
-// 82 experts of 4096 x 1536), 16 for binary32 weights (66 -> 60 us).
+// 82 experts of 4096 x 1536), 16 for binary32 weights (61 -> 53 us).
 constexpr int down_rows(int wtype) { return wtype == TYPE_F32 ? 16 : 32; }
+// Its waves: 4, 8 for e4m3, whose units are small (111 -> 92 us).
+constexpr int down_waves(int wtype) { return wtype == TYPE_E4M3 ? 8 : 4; }
 
 template <int WT, bool XBF16, int RT, int D>
-__global__ void __launch_bounds__(64 * kDownWaves, 4) down_kernel(MoeParams p, int most) {
+__global__ void __launch_bounds__(64 * down_waves(WT), 2) down_kernel(MoeParams p, int most) {
+    constexpr int kDownWaves = down_waves(WT);
     constexpr int kRows = 16 * RT;
     using W = Weight<WT>;
     using N = Terms<WT, XBF16>;
@@ -919,10 +924,10 @@ hipError_t launch_experts(const MoeParams& p, hipStream_t stream) {
                            dim3(512), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr int kRows = down_rows(WT), DD = WT == TYPE_E4M3 ? 2 : 1;
-    const size_t lds = p.most_h * sizeof(MoeGroup) + (size_t)kDownWaves * p.T * kRows * 4;
-    hipLaunchKernelGGL((down_kernel<WT, XBF16, kRows / 16, DD>),
-                       dim3((p.H + kRows - 1) / kRows, p.down_wgs), dim3(64 * kDownWaves),
+    constexpr int kRows = down_rows(WT), kWaves = down_waves(WT);
+    const size_t lds = p.most_h * sizeof(MoeGroup) + (size_t)kWaves * p.T * kRows * 4;
+    hipLaunchKernelGGL((down_kernel<WT, XBF16, kRows / 16, 2>),
+                       dim3((p.H + kRows - 1) / kRows, p.down_wgs), dim3(64 * kWaves),
                        lds, stream, p, p.most_h);
     return hipGetLastError();
 }
@@ -984,10 +989,18 @@ hipError_t launch_moe_plan(const MoeParams& p, hipStream_t stream) {
 int moe_group_size(int terms) { return 16 / terms; }
 
 int moe_down_workgroups(int wtype, int H, int I, int most_groups) {
-    // Two workgroups for every CU, each wave with at least two units.
+    // As many as n workgroups on every CU take, for the n with the most even share,
+    // with 2 % for every piece to join; each wave with at least two units.
     const int tiles = (H + down_rows(wtype) - 1) / down_rows(wtype);
+    int best = 1;
+    float best_cost = 0.f;
+    for (int n = (tiles + 255) / 256, all = n + 4; n < all; ++n) {
+        const int y = n * 256 / tiles;
+        const float cost = (float)n / (float)y + 0.02f * (float)n;
+        if (best_cost == 0.f || cost < best_cost) best = y, best_cost = cost;
+    }
     const int units = most_groups * ((I + 127) / 128);
-    return std::max(1, std::min((512 + tiles - 1) / tiles, units / (2 * kDownWaves)));
+    return std::max(1, std::min(best, units / (2 * down_waves(wtype))));
 }
 
 hipError_t launch_moe_experts(const MoeParams& p, hipStream_t stream) {
