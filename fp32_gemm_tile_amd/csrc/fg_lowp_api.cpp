@@ -72,6 +72,7 @@ struct Plan {
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
     constexpr double kFinish = 7;
+    constexpr double kMaxTiles = 1 << 23;  // of 512 threads: a grid has fewer than 2^32
     const int64_t kb = cdiv(K, fg::kScaleBlock);
     const double stream = ((double)M * K + (double)N * K) / kStream;
     const double slice = (double)M * N * 4;
@@ -80,8 +81,8 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     for (int s = 0; s < fg::fp8_num_shapes(); ++s) {
         const fg::Fp8Shape sh = fg::fp8_shape(s);
         const double per_block = bf16 ? sh.bf16_us : sh.f32_us;
-        if (per_block == 0) continue;
         const double tiles = (double)cdiv(M, sh.bm) * (double)cdiv(N, sh.bn);
+        if (per_block == 0 || tiles >= kMaxTiles) continue;
         for (int64_t n = 1; n <= 16; n *= 2) {
             const int64_t per = cdiv(kb, n), used = cdiv(kb, per);
             if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
@@ -224,9 +225,7 @@ fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_
         return launched(fg::launch_fp8_finish(p, stream), "scaling kernel");
     }
     const Plan plan = plan_gemm(M, N, K, p.c_bf16, workspace ? workspace_bytes : 0);
-    const fg::Fp8Shape s = fg::fp8_shape(plan.shape);
-    if (cdiv(M, s.bm) * cdiv(N, s.bn) > 0x7FFFFFFFll)
-        return fail(FG_ERR_UNSUPPORTED, 0, "more than 2^31 - 1 output tiles");
+    if (plan.shape < 0) return fail(FG_ERR_UNSUPPORTED, 0, "2^23 or more output tiles");
     if ((st = check_device()) != FG_OK) return st;
     p.kb = (int32_t)cdiv(K, fg::kScaleBlock);
     p.splits = (int32_t)plan.splits;

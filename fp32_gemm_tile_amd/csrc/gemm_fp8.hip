@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(256) fp8_finish_kernel(Fp8Params p) {
 template <int BM, int BN, int WM, int WN, int NS, int KG, bool BF16_ONLY = false>
 hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN) * KG;
+    static_assert(threads <= 512, "the host bounds the number of tiles by it");
     const dim3 grid((unsigned)(((p.M + BM - 1) / BM) * (int64_t)((p.N + BN - 1) / BN)),
                     (unsigned)p.splits);
     const bool fp8 = p.c_bf16;

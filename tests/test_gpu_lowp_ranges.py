@@ -96,6 +96,23 @@ def test_rows_beyond_32_bits():
     assert torch.equal(C, want[M // 2:])
 
 
+def test_more_rows_than_small_tiles_reach():
+    """So many rows that a grid of the smallest tiles would have 2^32 threads."""
+    import torch
+    M, N, K = (1 << 27) + 5, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    A, SA, B, SB, b = (torch.empty(M, K, dtype=torch.float8_e4m3fn, device="cuda"),
+                       torch.ones(1, M, device="cuda")) + integers(g, N, K, 1)
+    some = torch.randint(-8, 9, (4096, K), generator=g, device="cuda").float()
+    A.view(torch.uint8)[:] = some[0].to(torch.float8_e4m3fn).view(torch.uint8)
+    A[-4096:] = some.to(torch.float8_e4m3fn)
+    C = fg.gemm_fp8(A, SA, B, SB, torch.empty(M, N, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(C[-4096:], (some.double() @ b.t()).float())
+    first = (some[0].double() @ b.t()).float()
+    assert (C[:-4096] == first).all()
+
+
 class Experts:
     """Random experts of small integers / 8 (exact in every type)."""
 
