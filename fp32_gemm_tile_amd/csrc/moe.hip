@@ -69,21 +69,26 @@ __device__ __forceinline__ bf8 codes_to_bf16(int lo, int hi) {
     return v;
 }
 
-// x = sum of NS bfloat16 terms, each the nearest to what the others leave (a
-// term holds 8 bits, and the remainders are exact). An infinity keeps its
-// first term only (the remainder would be NaN).
+// Takes a bfloat16 term off `left`, exactly (a term holds 8 bits). All but the
+// last are cut off towards zero, so that sums of the first terms of values up to
+// the largest binary32 do not pass it; the last is the nearest. An infinity or
+// NaN keeps its first term only (the remainder would be NaN).
+__device__ __forceinline__ __bf16 next_term(float& left, bool last) {
+    const bool finite = fabsf(left) < __builtin_inff();
+    const float cut = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, left) & 0xFFFF0000u);
+    const __bf16 h = (__bf16)(last || !finite ? left : cut);
+    left = finite ? left - (float)h : 0.f;
+    return h;
+}
+
+// x = sum of NS bfloat16 terms.
 template <int NS>
 __device__ __forceinline__ void split_bf16(const float (&x)[8], bf8 (&t)[NS]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         float left = x[e];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const __bf16 h = (__bf16)left;
-            t[s][e] = h;
-            left -= (float)h;
-            if (s == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
-        }
+        for (int s = 0; s < NS; ++s) t[s][e] = next_term(left, s == NS - 1);
     }
 }
 
@@ -717,10 +722,8 @@ __global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoePar
                     float left = h;
 #pragma unroll
                     for (int t = 0; t < N::kH; ++t) {
-                        const __bf16 b = (__bf16)left;
+                        const __bf16 b = next_term(left, t == N::kH - 1);
                         p.h[t * p.h_plane + to] = __builtin_bit_cast(uint16_t, b);
-                        left -= (float)b;
-                        if (t == 0 && !(fabsf(left) < __builtin_inff())) left = 0.f;
                     }
                 }
             }

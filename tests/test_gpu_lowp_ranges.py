@@ -175,6 +175,35 @@ def test_largest_layers(wt, xt):
         check(L, x, ids, w, out)
 
 
+@pytest.mark.parametrize("wt", ["bfloat16", "float32"])
+def test_largest_and_infinite_values(wt):
+    """binary32 x and h between the largest bfloat16 and infinity stay finite;
+    infinities and NaN reach their own token only."""
+    import torch
+    top, tiny = float(np.finfo(np.float32).max), 2.0 ** -120
+    H, I, dt = 20, 18, getattr(torch, wt)
+    gate, up, down = (torch.zeros(1, I, 32, dtype=dt, device="cuda")[:, :, :H],
+                      torch.zeros(1, I, 32, dtype=dt, device="cuda")[:, :, :H],
+                      torch.zeros(1, H, 32, dtype=dt, device="cuda")[:, :, :I])
+    gate[0, 0, 0], gate[0, 1, 1] = tiny, 1.0
+    up[0, 0, 0], up[0, 1, 2] = tiny, 1.0
+    down[0, 0, 0], down[0, 1, 1], down[0, 2, 0] = 1.0, tiny, -1.0
+    x = torch.zeros(4, H, device="cuda")
+    x[0, 0] = -top                       # h[0] = (top tiny)^2
+    x[1, 1], x[1, 2] = 1.0, top          # h[1] = top
+    x[2, 0] = float("inf")
+    x[3, 5] = float("nan")
+    ids, w = torch.zeros(4, 1, dtype=torch.int32, device="cuda"), torch.ones(4, 1, device="cuda")
+    out = fg.moe(x, gate, up, down, ids, w, torch.empty(4, H, device="cuda"), activation="none")
+    out = out.double().cpu().numpy()
+    a, b = (top * tiny) ** 2, top * tiny
+    # (roundings of g, u, g * u and the sums: a few of 2^-24 each)
+    np.testing.assert_allclose(out[0, :3], [a, 0.0, -a], rtol=2.0 ** -20)
+    np.testing.assert_allclose(out[1, :3], [0.0, b, 0.0], rtol=2.0 ** -20)
+    assert (out[:2, 3:] == 0).all() and np.isnan(out[3]).all()
+    assert not np.isfinite(out[2, 0])
+
+
 def test_experts_beyond_32_bits():
     """Experts further apart than 2^32 bytes."""
     import torch
