@@ -71,7 +71,7 @@ struct Plan {
 // one, 22.0 in two).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
-    constexpr double kFinish = 7;
+    constexpr double kLaunch = 1.6, kFirst = 1.5, kFinish = 7, kNear = 2.5;  // us
     constexpr double kMaxTiles = 1 << 23;  // of 512 threads: a grid has fewer than 2^32
     const int64_t kb = cdiv(K, fg::kScaleBlock);
     const double stream = ((double)M * K + (double)N * K) / kStream;
@@ -80,15 +80,18 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     double best_us = 0;
     for (int s = 0; s < fg::fp8_num_shapes(); ++s) {
         const fg::Fp8Shape sh = fg::fp8_shape(s);
-        const double per_block = bf16 ? sh.bf16_us : sh.f32_us;
+        const double near_us = bf16 ? sh.bf16_us : sh.f32_us;
         const double tiles = (double)cdiv(M, sh.bm) * (double)cdiv(N, sh.bn);
-        if (per_block == 0 || tiles >= kMaxTiles) continue;
+        if (near_us == 0 || tiles >= kMaxTiles) continue;
         for (int64_t n = 1; n <= 16; n *= 2) {
             const int64_t per = cdiv(kb, n), used = cdiv(kb, per);
             if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
             const double rounds = std::ceil(tiles * (double)n / kCUs);
-            const double share = sh.stream * std::min(1.0, tiles * (double)n / kCUs);
-            double us = sh.fixed_us + std::max(rounds * (double)per * per_block, stream / share);
+            const double per_block = stream > kNear && tiles * (double)n <= kCUs
+                                         ? std::max(near_us, (double)sh.far_us) : near_us;
+            const double share = std::min(1.0, 4 * tiles * (double)n / kCUs);
+            double us = kLaunch + std::max(rounds * (sh.start_us + (double)per * per_block),
+                                           kFirst + stream / share);
             if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
             if (best.shape < 0 || us < best_us) {
                 best = Plan{s, n};
@@ -218,7 +221,6 @@ fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_
     p.alpha = alpha;
     p.beta = beta;
     p.c_bf16 = type_c == FG_TYPE_BF16;
-    p.vec_c = ldc % 4 == 0 && aligned(C, 4 * (uintptr_t)type_size(type_c));
     if (!product) {
         if ((st = check_device()) != FG_OK) return st;
         p.alpha = 0.f;

@@ -44,16 +44,14 @@ struct Fp8Params {
     int32_t splits;
     float alpha, beta;
     int32_t c_bf16;
-    int32_t vec_c;         // C rows start aligned to 4 elements
     float* ws;             // partial sums (splits > 1): slice s at s * M * N
 };
 // Tile kernels' shapes: index into the table of gemm_fp8.hip.
 struct Fp8Shape {
-    int bm, bn;      // rows of A and of B per workgroup
-    float fixed_us;  // start and end
-    float bf16_us, f32_us;  // per block of K and round of 256 workgroups, by C's
-                            // type (0: not built)
-    float stream;           // share of the memory's rate that 256 workgroups draw
+    int bm, bn;             // rows of A and of B per workgroup
+    float start_us;         // of a round of 256 workgroups
+    float bf16_us, f32_us;  // of a block of K in it, by C's type (0: not built)
+    float far_us;           // at least, from beyond the L2s and one workgroup per CU
 };
 int fp8_num_shapes();
 Fp8Shape fp8_shape(int shape);

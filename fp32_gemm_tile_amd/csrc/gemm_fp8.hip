@@ -123,7 +123,10 @@ __device__ __forceinline__ i8v keep_codes(i8v c, int g, int k_left) {
 // instructions, because the compiler makes every LDS read wait for all such
 // loads it knows of, also those into the stage that is not being read; the loop
 // below waits for them itself. They have no result registers, and offsets past
-// the buffer's end read zeros. M0 holds the LDS address (one wait state).
+// the buffer's end read zeros. M0 holds the LDS address (one wait state); the
+// compiler warns that it does not preserve M0 over the statement, and need not: it
+// writes M0 before each use of its own.
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
@@ -153,31 +156,53 @@ __device__ __forceinline__ void dma4(i4v r, uint32_t lds, uint32_t off) {
 #endif
 }
 
+// Four consecutive elements of C as they are in memory; rows may begin at any
+// element, so the accesses are wide but ask for no more than its alignment.
 template <bool BF16>
-__device__ __forceinline__ void store_c(const Fp8Params& p, int64_t i, int64_t j, f4 acc) {
-    const int n = p.N - j < 4 ? (int)(p.N - j) : 4;
-    if constexpr (BF16) {
-        uint16_t* c = static_cast<uint16_t*>(p.C) + i * p.ldc + j;
-        f4 o = acc * p.alpha;
-        if (p.beta != 0.f)
-            for (int e = 0; e < n; ++e)
-                o[e] += p.beta * __builtin_bit_cast(float, (uint32_t)c[e] << 16);
-        if (n == 4 && p.vec_c) {
-            uint2 u;
-            u.x = bf16_code(o[0]) | bf16_code(o[1]) << 16;
-            u.y = bf16_code(o[2]) | bf16_code(o[3]) << 16;
-            *reinterpret_cast<uint2*>(c) = u;
-        } else {
-            for (int e = 0; e < n; ++e) c[e] = (uint16_t)bf16_code(o[e]);
+struct Quad {
+    uint32_t u[BF16 ? 2 : 4];
+
+    static __device__ __forceinline__ uint8_t* at(const Fp8Params& p, int64_t i, int64_t j) {
+        return static_cast<uint8_t*>(p.C) + (i * p.ldc + j) * (BF16 ? 2 : 4);
+    }
+    __device__ __forceinline__ void load(const uint8_t* c) { __builtin_memcpy(u, c, sizeof u); }
+    // alpha * sum + beta * this, stored
+    __device__ __forceinline__ void store(uint8_t* c, f4 sum, float alpha, float beta) {
+        f4 o = sum * alpha;
+        if (beta != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] += beta * __builtin_bit_cast(
+                                   float, !BF16 ? u[e % (BF16 ? 2 : 4)]
+                                                : (e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16));
         }
-    } else {
-        float* c = static_cast<float*>(p.C) + i * p.ldc + j;
-        f4 o = acc * p.alpha;
-        if (n == 4 && p.vec_c) {
-            if (p.beta != 0.f) o = o + p.beta * *reinterpret_cast<const f4*>(c);
-            *reinterpret_cast<f4*>(c) = o;
+        if constexpr (BF16) {
+            const b4 r = __builtin_convertvector(o, b4);
+            __builtin_memcpy(c, &r, sizeof r);
         } else {
-            for (int e = 0; e < n; ++e) c[e] = p.beta != 0.f ? o[e] + p.beta * c[e] : o[e];
+            __builtin_memcpy(c, &o, sizeof o);
+        }
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store_c(const Fp8Params& p, int64_t i, int64_t j, f4 sum) {
+    uint8_t* const at = Quad<BF16>::at(p, i, j);
+    Quad<BF16> q{};
+    if (j + 4 <= p.N) {
+        if (p.beta != 0.f) q.load(at);
+        q.store(at, sum, p.alpha, p.beta);
+        return;
+    }
+    for (int e = 0; e < 3 && j + e < p.N; ++e) {
+        if constexpr (BF16) {
+            uint16_t* const c = reinterpret_cast<uint16_t*>(at) + e;
+            float o = sum[e] * p.alpha;
+            if (p.beta != 0.f) o += p.beta * __builtin_bit_cast(float, (uint32_t)*c << 16);
+            *c = (uint16_t)bf16_code(o);
+        } else {
+            float* const c = reinterpret_cast<float*>(at) + e;
+            *c = p.beta != 0.f ? sum[e] * p.alpha + p.beta * *c : sum[e] * p.alpha;
         }
     }
 }
@@ -399,7 +424,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     static_assert(KG * kPart * 4 <= KG * NS * kStage, "the stages hold the waves' rows");
     static_assert(16 % KG == 0, "rows per group");
     float* const own = reinterpret_cast<float*>(all_lds) + wave * 16 * kPitch;
-    const bool plain = p.vec_c && p.beta == 0.f && p.splits == 1 && n0 + wj + WN <= p.N;
+    const bool plain = p.splits == 1 && n0 + wj + WN <= p.N;
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     auto sync = [] {
         if constexpr (KG > 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -407,13 +432,23 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     };
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
+        constexpr int kMine = 16 / KG, kTurns = (kMine + kRows - 1) / kRows;
+        const int r0 = group * kMine + lane / kLanes;
+        const int64_t cj = n0 + wj + (lane % kLanes) * 4;
+        const bool busy = kRows <= kMine || lane / kLanes < kMine;
+        const bool whole_rows = plain && m0 + wi + 16 * i + 16 <= p.M;
+        // (C's old elements on their way during the exchange)
+        Quad<FP8> old[kTurns] = {};
+        uint8_t* const at = Quad<FP8>::at(p, m0 + wi + 16 * i + r0, cj);
+        constexpr int64_t kTurn = kRows * (FP8 ? 2 : 4);
+        if (whole_rows && busy && p.beta != 0.f) {
+#pragma unroll
+            for (int r = 0; r < kTurns; ++r) old[r].load(at + r * kTurn * p.ldc);
+        }
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
             *reinterpret_cast<f4*>(own + group * kPart + n16 * kPitch + 16 * j + 4 * g) = acc[i][j];
         sync();
-        constexpr int kMine = 16 / KG, kTurns = (kMine + kRows - 1) / kRows;
-        const int r0 = group * kMine + lane / kLanes;
-        const int64_t cj = n0 + wj + (lane % kLanes) * 4;
         const float* const from = own + r0 * kPitch + (lane % kLanes) * 4;
         auto sum_at = [&](int r) {
             f4 v = *reinterpret_cast<const f4*>(from + r * kPitch);
@@ -422,22 +457,14 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
                 v = v + *reinterpret_cast<const f4*>(from + k * kPart + r * kPitch);
             return v;
         };
-        const bool busy = kRows <= kMine || lane / kLanes < kMine;
-        if (plain && m0 + wi + 16 * i + 16 <= p.M) {
+        if (whole_rows) {
             f4 v[kTurns];
 #pragma unroll
             for (int r = 0; r < kTurns; ++r) v[r] = sum_at(r * kRows);
-            const int64_t at = (m0 + wi + 16 * i + r0) * p.ldc + cj;
             if (busy) {
 #pragma unroll
-                for (int r = 0; r < kTurns; ++r) {
-                    const f4 o = v[r] * p.alpha;
-                    if constexpr (FP8)
-                        *reinterpret_cast<b4*>(static_cast<__bf16*>(p.C) + at +
-                                               r * kRows * p.ldc) = __builtin_convertvector(o, b4);
-                    else
-                        *reinterpret_cast<f4*>(static_cast<float*>(p.C) + at + r * kRows * p.ldc) = o;
-                }
+                for (int r = 0; r < kTurns; ++r)
+                    old[r].store(at + r * kTurn * p.ldc, v[r], p.alpha, p.beta);
             }
         } else {
 #pragma unroll 1
@@ -495,29 +522,30 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The tile shapes, with what one costs by estimate: microseconds for a start and
-// end, and per block of K and round of 256 workgroups, for bfloat16 and for
-// binary32 C, and the share of the memory's rate that its loads in flight draw
-// (fits to 16 .. 1024 x 4096 x 2048 and 1 .. 1024 x 8192 x 8192 on one MI355X).
+// The tile shapes, with what one costs by estimate: microseconds for the start and
+// end of a round of 256 workgroups, and for a block of K in it, for bfloat16 and
+// for binary32 C, and for a block that comes from beyond the L2s where that is
+// more (the latency over the loads in flight, with one workgroup on a CU) (fits to 16 .. 2048 x 1024 .. 8192 x 1024 .. 8192 on one MI355X, one to twelve
+// rounds; mostly within 15 %).
 //   The tiles of up to 64 x 32 are for few rows: many groups of K, so that the
 // whole of a CU's LDS is in flight (bfloat16, 1 x 8192 x 8192 11.5 us = 5.8 TB/s;
 // 32 rows 13.1 us, 64 rows 14.8, with the 64 x 64 tile 32).
 //   The tiles between 64 x 64 and 128 x 128 save results that a smaller tile
 // takes in two rounds and a larger one in less than one (binary32 C):
-// 517 x 2047 x 3001 80 x 64 15.6 us, 64 x 64 19.7, 128 x 128 29.4;
+// 517 x 2047 x 3001 80 x 64 15.6 us, 64 x 64 19.9, 128 x 128 29.4;
 // 2048 x 1024 x 1024 128 x 64 9.3 us, 64 x 64 9.9, 128 x 128 12.1;
 // 600 x 4096 x 4096 160 x 64 26.8 us, 64 x 64 36.2, 128 x 128 34.5.
 constexpr Fp8Shape kShapes[] = {
-    {16, 32, 3.0f, 0.088f, 0.093f, 1.f},
-    {32, 32, 3.0f, 0.11f, 0.127f, 1.f},
-    {64, 32, 3.2f, 0.155f, 0.24f, 1.f},
-    {64, 64, 3.5f, 0.26f, 0.37f, 0.38f},
-    {80, 64, 3.5f, 0.33f, 0.42f, 1.f},
-    {128, 64, 3.7f, 0.52f, 0.61f, 1.f},
-    {160, 64, 3.8f, 0.58f, 0.71f, 1.f},
-    {128, 128, 4.5f, 0.64f, 0.95f, 1.f},
-    {256, 128, 6.0f, 1.0f, 1.87f, 1.f},
-    {256, 256, 10.f, 1.7f, 0.f, 1.f},  // bfloat16 C only
+    {16, 32, 1.5f, 0.070f, 0.074f, 0.f},
+    {32, 32, 2.5f, 0.073f, 0.086f, 0.f},
+    {64, 32, 3.0f, 0.117f, 0.185f, 0.f},
+    {64, 64, 1.5f, 0.22f, 0.31f, 0.45f},
+    {80, 64, 3.4f, 0.27f, 0.33f, 0.f},
+    {128, 64, 3.5f, 0.48f, 0.55f, 0.f},
+    {160, 64, 3.5f, 0.52f, 0.65f, 0.f},
+    {128, 128, 2.5f, 0.59f, 0.94f, 0.f},
+    {256, 128, 4.0f, 1.0f, 1.87f, 0.f},
+    {256, 256, 5.0f, 1.7f, 0.f, 0.f},  // bfloat16 C only
 };
 
 }  // namespace

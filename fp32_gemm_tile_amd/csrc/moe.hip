@@ -901,8 +901,16 @@ __global__ void __launch_bounds__(64 * down_waves(WT), 2) down_kernel(MoeParams 
     if (!last_to_arrive(p.tickets + blockIdx.x, gridDim.y, &s_last)) return;
     for (int i = threadIdx.x; i < piece; i += blockDim.x) {
         float s = 0.f;
-        for (int y = 0; y < (int)gridDim.y; ++y)
-            s += fetch_left(pieces + y * piece + i);
+        for (int y = 0; y < (int)gridDim.y; y += 8) {  // (eight loads in flight)
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int from = y + q < (int)gridDim.y ? y + q : 0;
+                v[q] = fetch_left(pieces + from * piece + i);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s += y + q < (int)gridDim.y ? v[q] : 0.f;
+        }
         store(i, s);
     }
 }
