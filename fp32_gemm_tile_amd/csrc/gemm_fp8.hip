@@ -525,8 +525,9 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
 // The tile shapes, with what one costs by estimate: microseconds for the start and
 // end of a round of 256 workgroups, and for a block of K in it, for bfloat16 and
 // for binary32 C, and for a block that comes from beyond the L2s where that is
-// more (the latency over the loads in flight, with one workgroup on a CU) (fits to 16 .. 2048 x 1024 .. 8192 x 1024 .. 8192 on one MI355X, one to twelve
-// rounds; mostly within 15 %).
+// more (the latency over the loads in flight, with one workgroup on a CU). Fits to
+// 16 .. 2048 x 1024 .. 8192 x 1024 .. 8192 on one MI355X, one to twelve rounds;
+// mostly within 15 %.
 //   The tiles of up to 64 x 32 are for few rows: many groups of K, so that the
 // whole of a CU's LDS is in flight (bfloat16, 1 x 8192 x 8192 11.5 us = 5.8 TB/s;
 // 32 rows 13.1 us, 64 rows 14.8, with the 64 x 64 tile 32).
