@@ -111,7 +111,7 @@ struct MoeParams {
     MoePlan* plan;
     MoeGroup *groups_x, *groups_h;
     int32_t gx, gh, most_x, most_h;
-    // down: workgroups per 16 output rows, which ones have finished, their pieces
+    // down: workgroups per tile of output rows, how many have finished, their pieces
     int32_t down_wgs;
     int32_t* tickets;
     float* pieces;

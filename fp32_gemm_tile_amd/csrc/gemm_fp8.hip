@@ -17,12 +17,20 @@
 //     off by about 3e-5 of its size on normal data, far below the 2^-9 of the
 //     rounding to bfloat16; the sums over the blocks are binary32.
 //
-// Tiles of both operands go from memory straight to LDS (two stages, the next
-// block in flight while this one is used). A 128-byte row of a tile is eight
+// Tiles of both operands go from memory straight to LDS (two or three stages, the
+// next blocks in flight while this one is used). A 128-byte row of a tile is eight
 // 16-byte chunks, chunk c of row r at position c ^ (r & 7), so the 16 rows
 // that a wave's 128-bit LDS reads touch together fall on different banks.
 // Rows past the matrix read as zero through the buffer's bound; the bytes of
 // the last block past K are cleared when they are read from LDS.
+//
+// Bound by the matrix cores for large results, by HBM for few rows, by the
+// latency of a block (load, LDS, one instruction after the other) in between.
+// Measured on one MI355X: 4096^3, bfloat16 C 61 us (2250 TFLOP/s; the library's
+// product with one scale per matrix 50); 8192^3, binary32 C, beta = 0.5 1067 us
+// (1030 TFLOP/s; the library's binary16 product reaches 1149, and the sums of
+// blocks take a v_fma per element and block beside it); 32 x 8192 x 8192 13.2 us
+// (5.2 TB/s); 517 x 2047 x 3001, binary32 C 15.6 us.
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
 

@@ -8,11 +8,19 @@
 //            plan alone);
 //   gate/up  one workgroup per 16 or 32 inner rows of one group: waves take
 //            the steps of K in turn, sums joined in wave order, h = act(g) * u;
-//   down     16 output rows and all groups per workgroup: waves take the
+//   down     16 or 32 output rows and all groups per workgroup: waves take the
 //            (group, step) units in turn, each adds its weighted results to a
-//            private tokens x 16 piece in LDS, and the pieces are joined in
+//            private tokens x rows piece in LDS, and the pieces are joined in
 //            wave order, those of several workgroups by the last to finish. No
 //            atomics on values: repeated calls are identical.
+//
+// Measured (one MI355X; the experts' types e4m3, bfloat16, e4m3 and binary32):
+// 1 token, 2 of 8 experts of 1024 x 512: route 3.0 us, top-k 2.8, gate/up 6.5,
+// down 5.1; 8 tokens, 6 of 64 of 2048 x 1408: 5.3, 8.4, 81, 42; 16 tokens, 8 of
+// 128 of 4096 x 1536: 7.8, 8.4, 180 (5.7 TB/s of the weights), 98 (5.3 TB/s);
+// 64 routed tokens, 2 of 16 of 2048 x 2000: plan 5, 98 (5.3 TB/s), 51 (5.1 TB/s).
+// Route, top-k and plan are chains of latencies. A read of that many bytes
+// alone runs at 5.8 to 6.3 TB/s.
 //
 // The products run on v_mfma_f32_16x16x32_bf16 with the 16 weight rows as the
 // instruction's rows and the group's tokens as its columns. e4m3 and bfloat16

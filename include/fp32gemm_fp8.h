@@ -85,7 +85,7 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
  * For binary32 C, products are exact and sums binary32. For bfloat16 C the
  * sum of a block may be taken by the fp8 matrix cores, which drop what lies
  * more than 2^-14 below the block's largest product; the sum over the blocks
- * is binary32. A's scales are FG_BLOCK_ROW, B's either kind. A linear
+ * is binary32. SA * SB of a block is rounded to binary32 first. A's scales are FG_BLOCK_ROW, B's either kind. A linear
  * layer's three products are all of this form: Y = X W^T (X by rows, W by
  * tiles), dX = dY W (W's transposed codes), dW = dY^T X (both transposed
  * codes, by rows; beta = 1 adds to what is there).
@@ -108,7 +108,8 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
  *                       is split among fewer workgroups, or not at all)
  *   20 stream
  * Quick returns and the treatment of alpha == 0, K == 0 and beta == 0 are
- * those of fg_sgemm. Repeated calls with the same arguments and workspace
+ * those of fg_sgemm; M and N are at most 2^30, and C has fewer than 2^23 tiles
+ * of 256 x 128 (else FG_ERR_UNSUPPORTED). Repeated calls with the same arguments and workspace
  * size give identical bits. Leading dimensions up to FG_MAX_LD.
  */
 fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_t* A,
