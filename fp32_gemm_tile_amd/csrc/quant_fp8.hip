@@ -6,18 +6,15 @@
 // Bound by HBM: 4 or 2 bytes read and 1 written per element and order, so X is
 // read once for both orders; next by the vector ALU, hence the few instructions
 // per element. Measured: 8192 x 8192 binary32 in both orders 76 us, 5.3 TB/s, the
-// vector ALU 62 % busy (148 us with an exact division per element); a row of 4096
-// bfloat16 3.6 us, a launch's own time; 3001 x 2047 bfloat16 both ways 18.5 us, a
-// single round of tiles, whose chain of load, two folds, division and LDS exchange
-// nothing covers. The code is the one nearest to the exact quotient: with s = 2^e
+// vector ALU 61 % busy (148 us with an exact division per element); a row of 4096
+// bfloat16 3.6 us, a launch's own time; 3001 x 2047 bfloat16 in 128 x 128 blocks both
+// ways 13 us, a single round of tiles, whose chain of load, fold, division and LDS
+// exchange nothing covers. The code is the one nearest to the exact quotient: with s = 2^e
 // s', s' in [1, 2), and r = fl(1 / s'), q = fl(x (2^-e r)) is within two units in
 // the last place of x / s. The middle of two codes ends in 19 zero bits, so q
 // rounds to the code that x / s does unless it is within two units of such a
-// number; only there the quotient is settled: q1 = fl(q + (x' - q s') r) with
-// x' = 2^-e x, one correction step with the exact remainder, is the binary32
-// value nearest to x'/s' up to a 2^-23rd of a unit, and if q1 is the middle
-// itself, the sign of its remainder moves it to the side the exact quotient is
-// on (a quotient that is not the middle is at least a 32nd of a unit off it).
+// number m; only there it is settled: the sign of the remainder 2^-e x - m s',
+// one fma and so exact in its sign, says on which side of m the quotient is.
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
 
@@ -30,26 +27,24 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
     return fmaxf(__builtin_bit_cast(float, amax) / kTop, 1.17549435e-38f);
 }
 
-// What dividing by a scale needs: 2^-e r, 2^-e, s' and r.
+// What dividing by a scale needs: 2^-e r, 2^-e, s'.
 typedef f4 Divisor;
 __device__ __forceinline__ Divisor divisor_of(float s) {
     const uint32_t u = __builtin_bit_cast(uint32_t, s);  // normal, positive, < 2^121
     const float f = __builtin_bit_cast(float, (254u << 23) - (u & 0x7F800000u));
     const float s1 = __builtin_bit_cast(float, (u & 0x007FFFFFu) | 0x3F800000u);
-    const float r = 1.f / s1;
-    return Divisor{f * r, f, s1, r};
+    return Divisor{f * (1.f / s1), f, s1, 0.f};
 }
 
-// The quotient x / s as described above (a zero with x's sign).
-__device__ __forceinline__ float settle(float x, const Divisor& d) {
-    const float xf = x * d[1];
-    float q = xf * d[3];
-    q = fmaf(fmaf(-q, d[2], xf), d[3], q);
-    const float rem = fmaf(-q, d[2], xf);
-    uint32_t u = __builtin_bit_cast(uint32_t, q);
-    if ((u & 0x7FFFFu) == 0 && rem != 0.f)  // (a NaN's bits are not all 0)
-        u += ((rem > 0.f) == (q > 0.f)) ? 1u : 0xFFFFFFFFu;
-    return q == 0.f ? copysignf(0.f, x) : __builtin_bit_cast(float, u);
+// q, which is within two units of a number m that ends in 19 zero bits, as m or
+// the next number on the side of it that x / s is on.
+__device__ __forceinline__ float settle(float x, float q, const Divisor& d) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, q);
+    const uint32_t m = (u + 2u) & 0xFFF80000u;  // (the sign stays: q is far from 0)
+    const float rem = fmaf(-__builtin_bit_cast(float, m), d[2], x * d[1]);
+    const uint32_t away = m + 1u, back = m - 1u;
+    const uint32_t side = (rem > 0.f) == (q > 0.f) ? away : back;
+    return __builtin_bit_cast(float, rem == 0.f ? m : side);
 }
 
 // At most 4 when q is within two units in the last place of a number that ends
@@ -60,13 +55,6 @@ __device__ __forceinline__ uint32_t near_middle(float q) {
     const uint32_t u = __builtin_bit_cast(uint32_t, q) & 0x7FFFFFFFu;
     constexpr uint32_t kLow = 0x3A040000u, kHigh = 0x43DC0000u;  // 1.03 * 2^-11, 440
     return (min(max(u, kLow), kHigh) + 2u) & 0x7FFFFu;
-}
-
-// The same for q whose codes have four bits (2^-6 and more), where those numbers
-// are the codes themselves, which need no care, and the middles between them.
-__device__ __forceinline__ bool not_near_code(float q) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, q) & 0x7FFFFFFFu;
-    return u < 0x3C800000u || ((u + 2u) & 0x80000u) != 0;
 }
 
 // Codes of four elements, in one dword; r(i) is the divisor's 2^-e r for x[i] and
@@ -81,18 +69,25 @@ __device__ __forceinline__ uint32_t codes4(const f4& x, R r, D d) {
         m[i] = near_middle(q[i]);
     }
     if (min(min(m[0], m[1]), min(m[2], m[3])) <= 4u) {
-        // (elements and largest elements of few bits have many quotients that
-        // are codes: 3001 x 2047 bfloat16 spent half its instructions on them)
-        bool need = false;
+        // (not rare in bfloat16: elements and largest elements of few bits have
+        // many quotients that are codes or middles)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) need |= m[i] <= 4u && not_near_code(q[i]);
-        if (need) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = settle(x[i], d(i));
-        }
+        for (int i = 0; i < 4; ++i) q[i] = m[i] <= 4u ? settle(x[i], q[i], d(i)) : q[i];
     }
     const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], c, true);
+}
+
+// Bytes of a 4 x 4 block, rows to columns.
+__device__ __forceinline__ void transpose4(const uint32_t (&r)[4], uint32_t (&c)[4]) {
+    const uint32_t lo01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u);
+    const uint32_t hi01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+    const uint32_t lo23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+    const uint32_t hi23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+    c[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+    c[1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+    c[2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+    c[3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
 }
 
 // Magnitudes as bits, whose order is that of the values (NaN and infinities at
@@ -189,7 +184,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(QuantParams p, int64_t 
 // A 128 x 128 tile per workgroup of 16 waves: half wave hw holds rows 4 hw ..
 // 4 hw + 3, lane l columns 4 l .. 4 l + 3, so that a lane owns a dword of four
 // rows of the codes and of four rows of the transposed codes; the latter go
-// through LDS and leave as whole 128-byte rows. (With 4 waves and 64 elements
+// through LDS and leave as whole 128-byte rows. (128 x 128 blocks have the same
+// codes both ways, which are transposed in registers.) (With 4 waves and 64 elements
 // per lane the unrolled code was 20 KB, and fetching it took most of the time:
 // 3001 x 2047 28 us.) No loop over tiles: what it kept in registers cost a second
 // workgroup on the CU (104 us at 8192 x 8192).
@@ -201,7 +197,7 @@ __global__ void __launch_bounds__(kTileThreads) quant_tile_kernel(QuantParams p,
     // over the banks.
     constexpr int kPitch = 128 + 16;
     __shared__ __attribute__((aligned(16))) uint8_t codes_t[128 * kPitch];
-    __shared__ uint32_t row_part[128];
+    __shared__ __attribute__((aligned(16))) uint32_t row_part[128];
     __shared__ __attribute__((aligned(16))) uint32_t col_part[16][128];
     __shared__ Divisor row_d[128], col_d[128];
     __shared__ __attribute__((aligned(16))) float row_r[128], col_r[128];
@@ -226,15 +222,18 @@ __global__ void __launch_bounds__(kTileThreads) quant_tile_kernel(QuantParams p,
     maxima([](float x) { return magnitude(x); });
     if (max(max(rm[0], rm[1]), max(rm[2], rm[3])) >= kInf)
         maxima([](float x) { return finite_magnitude(x); });
+    if constexpr (TILE) {
+        uint32_t m = max(max(rm[0], rm[1]), max(rm[2], rm[3]));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
+        for (int o = 1; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        if (lane == 0) row_part[wave] = m;
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rm[i] = max(rm[i], (uint32_t)__shfl_xor((int)rm[i], o, 64));
-    if (l == 0) {
+        for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) row_part[4 * hw + i] = rm[i];
-    }
-    if constexpr (!TILE) {
+            for (int i = 0; i < 4; ++i)
+                rm[i] = max(rm[i], (uint32_t)__shfl_xor((int)rm[i], o, 64));
+        if (l == 0) *reinterpret_cast<uint4*>(&row_part[4 * hw]) = make_uint4(rm[0], rm[1], rm[2], rm[3]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) cm[j] = max(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32, 64));
         if (lane < 32)
@@ -242,17 +241,16 @@ __global__ void __launch_bounds__(kTileThreads) quant_tile_kernel(QuantParams p,
                 make_uint4(cm[0], cm[1], cm[2], cm[3]);
     }
     __syncthreads();
+    Divisor tile_d;
     if constexpr (TILE) {
-        // every wave folds the 128 row maxima
-        uint32_t m = max(row_part[lane], row_part[64 + lane]);
+        uint32_t m = 0;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-        const float s = scale_of(m);
-        if (tid < 128) {
-            const Divisor d = divisor_of(s);
-            row_d[tid] = col_d[tid] = d;
-            row_r[tid] = col_r[tid] = d[0];
+        for (int w = 0; w < 16; w += 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(&row_part[w]);
+            m = max(max(m, max(u.x, u.y)), max(u.z, u.w));
         }
+        const float s = scale_of(m);
+        tile_d = divisor_of(s);
         if (tid == 0) {
             if (p.q) p.s[bn * p.lds + bm] = s;
             if (p.qt) p.st[bm * p.ldst + bn] = s;
@@ -274,25 +272,35 @@ __global__ void __launch_bounds__(kTileThreads) quant_tile_kernel(QuantParams p,
         if (rows && p.q && row < p.M) p.s[bn * p.lds + row] = s;
         if (!rows && p.qt && col0 + c < p.N) p.st[bm * p.ldst + col0 + c] = s;
     }
-    __syncthreads();
-    if (p.q) {
-        const f4 r = *reinterpret_cast<const f4*>(&row_r[4 * hw]);
+    if constexpr (!TILE) __syncthreads();
+    uint32_t cq[4];  // codes of row i
+    if (TILE || p.q) {
+        f4 r;
+        if constexpr (!TILE) r = *reinterpret_cast<const f4*>(&row_r[4 * hw]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t c = codes4(v[i], [&](int) { return r[i]; },
-                                      [&](int) { return row_d[4 * hw + i]; });
-            if (row0 + i < p.M && col < p.N)
-                store_codes4(p.q + (row0 + i) * p.ldq + col, c, p.N - col);
+            cq[i] = codes4(v[i], [&](int) { return TILE ? tile_d[0] : r[i]; },
+                           [&](int) { return TILE ? tile_d : row_d[4 * hw + i]; });
+            if (p.q && row0 + i < p.M && col < p.N)
+                store_codes4(p.q + (row0 + i) * p.ldq + col, cq[i], p.N - col);
         }
     }
     if (p.qt) {
-        const f4 r = *reinterpret_cast<const f4*>(&col_r[4 * l]);
+        uint32_t ct[4];  // codes of column j
+        if constexpr (TILE) {
+            transpose4(cq, ct);  // (the same scale, the same codes)
+        } else {
+            const f4 r = *reinterpret_cast<const f4*>(&col_r[4 * l]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 x = {v[0][j], v[1][j], v[2][j], v[3][j]};
+                ct[j] = codes4(x, [&](int) { return r[j]; }, [&](int) { return col_d[4 * l + j]; });
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f4 x = {v[0][j], v[1][j], v[2][j], v[3][j]};
             const int at = (4 * l + j) * kPitch + (((hw >> 2) ^ ((l >> 2) & 7)) << 4) + 4 * (hw & 3);
-            *reinterpret_cast<uint32_t*>(&codes_t[at]) =
-                codes4(x, [&](int) { return r[j]; }, [&](int) { return col_d[4 * l + j]; });
+            *reinterpret_cast<uint32_t*>(&codes_t[at]) = ct[j];
         }
         __syncthreads();
         const int rows_left = p.M - bm * 128;  // codes of a transposed row that exist
