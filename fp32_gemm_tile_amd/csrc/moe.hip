@@ -3,9 +3,8 @@
 //
 //   route    logits = x R^T summed in binary64 (float products are exact
 //            there), so that experts with near logits are not exchanged;
-//   top-k    one workgroup per token; the last one writes the plan: the groups
-//            of tokens that share an expert (a call without a router runs the
-//            plan alone);
+//   top-k    a wave per token; then the plan: the groups of tokens that share
+//            an expert (a call without a router runs the plan alone);
 //   gate/up  one workgroup per 16 or 32 inner rows of one group: waves take
 //            the steps of K in turn, sums joined in wave order, h = act(g) * u;
 //   down     16 or 32 output rows and all groups per workgroup: waves take the
@@ -15,9 +14,9 @@
 //            atomics on values: repeated calls are identical.
 //
 // Measured (one MI355X; the experts' types e4m3, bfloat16, e4m3 and binary32):
-// 1 token, 2 of 8 experts of 1024 x 512: route 3.0 us, top-k 2.8, gate/up 6.5,
-// down 5.1; 8 tokens, 6 of 64 of 2048 x 1408: 5.3, 8.4, 81, 42; 16 tokens, 8 of
-// 128 of 4096 x 1536: 7.8, 8.4, 180 (5.7 TB/s of the weights), 98 (5.3 TB/s);
+// 1 token, 2 of 8 experts of 1024 x 512: route 3.0 us, top-k 2.4, gate/up 6.6,
+// down 5.1; 8 tokens, 6 of 64 of 2048 x 1408: 5.5, 6.9, 79, 40; 16 tokens, 8 of
+// 128 of 4096 x 1536: 7.6, 8.0, 178 (5.8 TB/s of the weights), 96 (5.4 TB/s);
 // 64 routed tokens, 2 of 16 of 2048 x 2000: plan 5, 98 (5.3 TB/s), 51 (5.1 TB/s).
 // Route, top-k and plan are chains of latencies. A read of that many bytes
 // alone runs at 5.8 to 6.3 TB/s.
@@ -495,14 +494,6 @@ __device__ __forceinline__ void write_plan(const MoeParams& p, PlanLds& l) {
     }
 }
 
-__device__ __forceinline__ void read_choice(const MoeParams& p, PlanLds& l) {
-    for (int i = threadIdx.x; i < p.T * p.k; i += kPlanThreads) {
-        l.ids[i] = fetch_left(p.ids + i);
-        l.w[i] = fetch_left(p.weights + i);
-    }
-    __syncthreads();
-}
-
 // Workgroup 0 writes the plan; the others prepare x.
 template <bool XBF16>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(MoeParams p) {
@@ -512,94 +503,145 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(MoeParams p) {
                               (int64_t)(gridDim.x - 1) * kPlanThreads);
         return;
     }
-    read_choice(p, l);
+    for (int i = threadIdx.x; i < p.T * p.k; i += kPlanThreads) {
+        l.ids[i] = p.ids[i];
+        l.w[i] = p.weights[i];
+    }
+    __syncthreads();
     write_plan(p, l);
 }
 
-// Top-k of `tokens` tokens at a time from the first one of the workgroup on.
-// An expert's rank is the number of experts before it in the order (larger
-// logit, then lower number; NaN as -inf), counted by `parts` threads against a
-// part of them each: threads = tokens * width * parts, width = the power of two
-// at or above E. A NaN logit's weight is NaN. Then the plan: one workgroup for
-// all tokens writes it from LDS, of one per token the last to finish does. For a
-// single token its slots are the groups, and few threads do (5.7 -> 2.7 us of 8
-// experts): LONE.
-template <bool LONE>
-__global__ void __launch_bounds__(kPlanThreads) topk_kernel(MoeParams p, int width, int tokens) {
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#define FG_ROR(n) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 15, 15, true))
+    FG_ROR(8);  // rotations within rows of 16
+    FG_ROR(4);
+    FG_ROR(2);
+    FG_ROR(1);
+#undef FG_ROR
+#endif
+    const uint32_t a = __builtin_amdgcn_readlane((int)v, 0), b = __builtin_amdgcn_readlane((int)v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane((int)v, 32), d = __builtin_amdgcn_readlane((int)v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+// Top-k, a wave per token, and the plan: one workgroup writes it from LDS, of
+// several (of `per` tokens each) the last to finish does. A lane holds experts
+// lane, lane + 64, ... as integers in the logits' order (NaN as -inf, -0 as 0); k
+// times the largest is taken out: the larger upper half, of several the larger
+// lower half, of several the lowest expert. A NaN logit's weight is NaN. (Counting
+// every expert's rank against all others took 23 us for 64 tokens of 512 experts
+// against 16, and 7.7 for 8 of 64 against 5.6.) The code is short for few experts,
+// J = 1 and 2: it runs about once, and fetching it is most of the time (J = 8 for
+// all: 9.6 us for 8 tokens of 64). A lone token's slots are the groups: LONE, one
+// wave.
+template <bool LONE, int J>
+__global__ void __launch_bounds__(LONE ? 64 : kPlanThreads) topk_kernel(MoeParams p, int per) {
     __shared__ PlanLds l;
-    __shared__ double key[kPlanThreads], raw[kPlanThreads];  // [tokens][width]
-    __shared__ int rank[kPlanThreads];
     __shared__ int s_last;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int threads = LONE ? blockDim.x : kPlanThreads;
-    const int parts = threads / (tokens * width);
-    const int e = tid % width, part = tid / width % parts, lt = tid / (width * parts);
-    const int t0 = gridDim.x == 1 ? 0 : (int)blockIdx.x;
-    const int t1 = gridDim.x == 1 ? p.T : t0 + 1;
-    for (int tb = t0; tb < t1; tb += tokens) {
-        const int t = tb + lt;
-        const bool mine = t < t1 && e < p.E;
-        double* const k = key + lt * width;
-        if (mine && part == 0) {
-            const double v = p.logits[t * p.E + e];
-            raw[lt * width + e] = v;
-            k[e] = v == v ? v : -__builtin_inf();
-            rank[lt * width + e] = 0;
-        }
-        __syncthreads();
-        if (mine) {
-            const int per = (p.E + parts - 1) / parts, f0 = part * per;
-            const int f1 = f0 + per < p.E ? f0 + per : p.E;
-            const double v = k[e];
-            int n = 0;
-#pragma unroll 4
-            for (int f = f0; f < f1; ++f) n += k[f] > v || (k[f] == v && f < e);
-            if (n) atomicAdd(&rank[lt * width + e], n);
-        }
-        __syncthreads();
-        if (mine && part == 0 && rank[lt * width + e] < p.k)
-            l.ids[t * p.k + rank[lt * width + e]] = e;
-        __syncthreads();
-        for (int q = wave; q < tokens && tb + q < t1; q += threads / 64) {  // a wave per token
-            const double* const r = raw + q * width;
-            const int* const chosen = l.ids + (tb + q) * p.k;
-            const double top = r[chosen[0]];
-            const float mine_w = lane < p.k ? expf((float)(r[chosen[lane]] - top)) : 0.f;
-            float sum = mine_w;
-            if (!p.renorm) {
-                sum = 0.f;
-#pragma unroll 1
-                for (int f = lane; f < p.E; f += 64) sum += expf((float)(r[f] - top));
-            }
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t0 = blockIdx.x * per, t1 = t0 + per < p.T ? t0 + per : p.T;
+    for (int t = t0 + wave; t < t1; t += (LONE ? 1 : kPlanThreads / 64)) {
+        double raw[J];
+        uint64_t key[J];
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-            if (lane < p.k) {
-                const int at = (tb + q) * p.k + lane;
-                l.w[at] = mine_w / sum;
-                leave(p.ids + at, (int32_t)chosen[lane]);
-                leave(p.weights + at, mine_w / sum);
-                if constexpr (LONE) {
-                    MoeGroup& m = p.groups_x[lane];
-                    m.expert = chosen[lane];
-                    m.count = 1;
-                    m.pair[0] = (int16_t)lane;
-                    m.weight[0] = mine_w / sum;
-                    if (lane == 0) p.plan->total_x = p.k;
+        for (int j = 0; j < J; ++j) {
+            const int e = 64 * j + lane;
+            raw[j] = e < p.E ? p.logits[t * p.E + e] : 0.0;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const double v = raw[j] == raw[j] ? raw[j] + 0.0 : -__builtin_inf();
+            const uint64_t b = __builtin_bit_cast(uint64_t, v);
+            const uint64_t order = b >> 63 ? ~b : b | 1ull << 63;  // not 0
+            key[j] = 64 * j + lane < p.E ? order : 0;
+        }
+        int chosen = 0;  // of slot `lane`
+        double value = 0.0;
+#pragma unroll 1
+        for (int s = 0; s < p.k; ++s) {
+            uint64_t best = key[0];
+            int at = 0;
+#pragma unroll
+            for (int j = 1; j < J; ++j)
+                if (64 * j < p.E && key[j] > best) best = key[j], at = j;
+            const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+            // (wave_max is called by all lanes, never behind && or ?:, since it reads
+            // the other lanes' registers)
+            const uint32_t max_hi = wave_max(hi);
+            bool in = hi == max_hi;
+            uint64_t who = __ballot(in);
+            if (who & (who - 1)) {
+                const uint32_t max_lo = wave_max(in ? lo : 0u);
+                in = in && lo == max_lo;
+                who = __ballot(in);
+                if (who & (who - 1)) {
+                    const uint32_t low = in ? ~(uint32_t)(64 * at + lane) : 0u;
+                    const uint32_t max_low = wave_max(low);
+                    who = __ballot(low == max_low);
                 }
             }
+            const int winner = __builtin_amdgcn_readfirstlane(__builtin_ctzll(who));
+            const int slot = __builtin_amdgcn_readlane(at, winner);
+            double v = raw[0];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (slot != j) continue;
+                v = raw[j];
+                if (lane == winner) key[j] = 0;
+            }
+            const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+            const uint32_t v_lo = __builtin_amdgcn_readlane((int)(uint32_t)bits, winner);
+            const uint32_t v_hi = __builtin_amdgcn_readlane((int)(uint32_t)(bits >> 32), winner);
+            if (lane == s) {
+                chosen = 64 * slot + winner;
+                value = __builtin_bit_cast(double, (uint64_t)v_hi << 32 | v_lo);
+            }
         }
-        if constexpr (LONE) {
-            for (int i = tid; i < (p.H + 15) / 16; i += threads) p.tickets[i] = 0;
-            return;
+        const double top = __shfl(value, 0, 64);
+        const float mine = lane < p.k ? expf((float)(value - top)) : 0.f;
+        float sum = mine;
+        if (!p.renorm) {
+            sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (64 * j + lane < p.E) sum += expf((float)(raw[j] - top));
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+        if (lane < p.k) {
+            const float w = mine / sum;
+            leave(p.ids + t * p.k + lane, (int32_t)chosen);
+            leave(p.weights + t * p.k + lane, w);
+            if constexpr (LONE) {
+                MoeGroup& m = p.groups_x[lane];
+                m.expert = chosen;
+                m.count = 1;
+                m.pair[0] = (int16_t)lane;
+                m.weight[0] = w;
+                if (lane == 0) p.plan->total_x = p.k;
+            } else {
+                l.ids[t * p.k + lane] = chosen;
+                l.w[t * p.k + lane] = w;
+            }
+        }
+    }
+    if constexpr (LONE) {
+        for (int i = lane; i < (p.H + 15) / 16; i += 64) p.tickets[i] = 0;
+    } else {
+        if (gridDim.x > 1) {
+            // (the counter was set to 0 by the router kernel)
+            if (!last_to_arrive(&p.plan->ticket, gridDim.x, &s_last)) return;
+            for (int i = threadIdx.x; i < p.T * p.k; i += kPlanThreads) {
+                l.ids[i] = fetch_left(p.ids + i);
+                l.w[i] = fetch_left(p.weights + i);
+            }
         }
         __syncthreads();
+        write_plan(p, l);
     }
-    if (gridDim.x > 1) {
-        // (the counter was set to 0 by the router kernel)
-        if (!last_to_arrive(&p.plan->ticket, gridDim.x, &s_last)) return;
-        read_choice(p, l);
-    }
-    write_plan(p, l);
 }
 
 // ---- experts ---------------------------------------------------------------
@@ -983,20 +1025,15 @@ hipError_t launch_moe_route(const MoeParams& p, hipStream_t stream) {
     else launch_logits<4, 16>(p, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    int width = 8, tokens = 1;
-    while (width < p.E) width *= 2;
-    if (p.T == 1) {
-        const int threads = std::min(kPlanThreads, std::max(64, 8 * width));
-        hipLaunchKernelGGL(topk_kernel<true>, dim3(1), dim3(threads), 0, stream, p, width, 1);
-        return hipGetLastError();
-    }
-    // One workgroup while its comparisons (T E^2) take less time than the
-    // arrivals of several: 8 tokens of 32 experts 6.2 us against 7.0, 8 of 64
-    // 7.7 both, 16 of 64 9.9 against 7.4.
-    const bool one = (int64_t)p.T * width * width < 1 << 15;
-    while (one && tokens < p.T && tokens * width < kPlanThreads) tokens *= 2;
-    hipLaunchKernelGGL(topk_kernel<false>, dim3(one ? 1 : p.T), dim3(kPlanThreads), 0, stream, p,
-                       width, tokens);
+    auto kernel = p.T == 1 ? topk_kernel<true, 8> : topk_kernel<false, 8>;
+    if (p.E <= 64) kernel = p.T == 1 ? topk_kernel<true, 1> : topk_kernel<false, 1>;
+    else if (p.E <= 128) kernel = p.T == 1 ? topk_kernel<true, 2> : topk_kernel<false, 2>;
+    // One workgroup for few tokens, four tokens each for more (us, one against four
+    // each: 16 of 64 experts 6.0, 7.1; 16 of 128 7.4, 8.1; 16 of 256 11.3, 9.3; 64 of
+    // 64, sixteen against four each 9.6, 8.5; 64 of 512 21.6, 16.3).
+    const int per = p.E <= 128 && p.T <= 16 ? 16 : 4;
+    hipLaunchKernelGGL(kernel, dim3((p.T + per - 1) / per), dim3(p.T == 1 ? 64 : kPlanThreads), 0,
+                       stream, p, per);
     return hipGetLastError();
 }
 

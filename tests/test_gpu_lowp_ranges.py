@@ -175,6 +175,44 @@ def test_largest_layers(wt, xt):
         check(L, x, ids, w, out)
 
 
+@pytest.mark.parametrize("E,k", [(3, 3), (40, 7), (64, 16), (100, 16), (128, 5), (300, 16), (512, 8)])
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 64])
+def test_router_order(E, k, T):
+    """Equal logits, logits equal in their upper 32 bits, infinite and NaN ones,
+    against a stable sort in binary64."""
+    import torch
+    rng = np.random.default_rng(E + T)
+    H = 8
+    L = Experts(rng, E, H, 8, torch.bfloat16)
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0], x[:, 1] = 1.0, 2.0 ** -40
+    if T > 1:
+        x[1::3, 0] = -1.0
+        x[T - 1] = 0.0                                   # all of its logits equal
+    router = torch.zeros(E, H, device="cuda")
+    router[:, 0] = torch.from_numpy(rng.integers(-2, 3, E).astype(np.float32))
+    router[:, 1] = torch.from_numpy(rng.integers(-1, 2, E).astype(np.float32))
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    out = torch.empty(T, H, device="cuda")
+    for special in (False, True):
+        if special:
+            router[E // 2, 0], router[E - 1, 0] = float("nan"), float("-inf")
+            x[T - 1, 0] = 1.0                            # (0 * inf is NaN)
+        fg.moe(x, *L.t, ids, w, out, router=router)
+        logits = x.double().cpu().numpy() @ router.double().cpu().numpy().T
+        order = np.where(np.isnan(logits), -np.inf, logits)
+        want = np.argsort(-order, axis=1, kind="stable")[:, :k]
+        np.testing.assert_array_equal(ids.cpu().numpy(), want)
+        chosen = np.take_along_axis(logits, want, 1)
+        top = chosen[:, :1]
+        with np.errstate(invalid="ignore"):
+            e = np.exp(chosen - top)
+            weights = e / e.sum(1, keepdims=True)
+        # (differences below 8, exp, a sum of at most 16 and a division)
+        np.testing.assert_allclose(w.cpu().numpy(), weights, rtol=40 * 2.0 ** -23, atol=0)
+
+
 @pytest.mark.parametrize("wt", ["bfloat16", "float32"])
 def test_largest_and_infinite_values(wt):
     """binary32 x and h between the largest bfloat16 and infinity stay finite;
