@@ -643,7 +643,7 @@ def _scales(torch, t, name, dev, blocks, outer):
     ld, inner = t.stride()
     if outer > 1 and inner != 1:
         _wrong(name, "have unit stride along its rows")
-    return max(ld, outer, 1) if blocks > 1 else max(outer, 1)
+    return ld if blocks > 1 else max(outer, 1)   # (the library refuses one below `outer`)
 
 
 def _workspace(t, dev):

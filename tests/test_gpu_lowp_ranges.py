@@ -354,6 +354,23 @@ def test_quantise_product_and_layer_in_one_graph():
         check(L, x, b["ids"], b["w"], b["out"])
 
 
+def test_overlapping_scales_are_refused():
+    """Scales of several blocks in one row of memory (a broadcast tensor)."""
+    import torch
+    X = torch.zeros(40, 300, device="cuda")
+    q, s = fg.empty_fp8(40, 300)
+    same = torch.ones(1, 40, device="cuda").expand(3, 40)
+    C = torch.zeros(40, 40, device="cuda")
+    with pytest.raises(fg.FgError):
+        fg.quantize_fp8(X, q, same)
+    fg.quantize_fp8(X, q, s)
+    for sa, sb in ((same, s), (s, same)):
+        with pytest.raises(fg.FgError):
+            fg.gemm_fp8(q, sa, q, sb, C)
+    fg.gemm_fp8(q, same.contiguous(), q, s, C)
+    torch.cuda.synchronize()
+
+
 def test_nothing_to_do():
     """Empty matrices and no tokens: accepted, nothing written."""
     import torch
