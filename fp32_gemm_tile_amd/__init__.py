@@ -577,14 +577,17 @@ def sgemm(A, B, C, alpha=1.0, beta=0.0, transA="N", transB="N", config=-1, strea
 # so does the marshalling.)
 
 _codes_of = {}   # torch dtype -> fg_type, filled on first use
+_torch = None
 
 
 def _torch_types():
-    import torch
-    if not _codes_of:
+    global _torch
+    if _torch is None:
+        import torch
         _codes_of.update({torch.float32: FG_TYPE_F32, torch.bfloat16: FG_TYPE_BF16,
                           torch.float8_e4m3fn: FG_TYPE_E4M3, torch.uint8: FG_TYPE_E4M3})
-    return torch, _codes_of
+        _torch = torch
+    return _torch, _codes_of
 
 
 def _wrong(name, what):
@@ -706,14 +709,26 @@ def gemm_fp8(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
     K = A.shape[1]
     kb = (K + 127) // 128
     tile = SB.dim() == 2 and SB.shape[1] != N
-    lda, ldb = _codes(types, A, "A", dev, M, K), _codes(types, B, "B", dev, N, K)
-    ldsa = _scales(torch, SA, "SA", dev, kb, M)
-    ldsb = _scales(torch, SB, "SB", dev, kb, (N + 127) // 128 if tile else N)
-    ws, ws_bytes = _workspace(workspace, dev)
-    _run_on(torch, dev, stream, load_library().fg_gemm_fp8,
+    outer = (N + 127) // 128 if tile else N
+    strides = A.stride() + SA.stride() + B.stride() + SB.stride() + C.stride()
+    if (N > 1 < kb and M > 0 and len(strides) == 10 and strides[1::2] == (1, 1, 1, 1, 1)
+            and A.shape == (M, K) and B.shape == (N, K) and SA.shape == (kb, M)
+            and SB.shape == (kb, outer) and SA.dtype is SB.dtype is torch.float32
+            and types.get(A.dtype) == FG_TYPE_E4M3 == types.get(B.dtype)
+            and A.get_device() == B.get_device() == SA.get_device() == SB.get_device() == dev):
+        lda, ldsa, ldb, ldsb, ldc = strides[::2]   # (nothing to look at one by one)
+        if M == 1:                                 # (one row: its stride is free)
+            lda, ldc = (K + 15) // 16 * 16, N
+    else:
+        lda, ldb = _codes(types, A, "A", dev, M, K), _codes(types, B, "B", dev, N, K)
+        ldsa = _scales(torch, SA, "SA", dev, kb, M)
+        ldsb = _scales(torch, SB, "SB", dev, kb, outer)
+        ldc = _ld(C, "C")
+    ws, ws_bytes = _workspace(workspace, dev) if workspace is not None else (None, 0)
+    _run_on(torch, dev, stream, (_lib or load_library()).fg_gemm_fp8,
             (M, N, K, alpha, A.data_ptr() or None, lda, SA.data_ptr() or None, ldsa,
              B.data_ptr() or None, ldb, SB.data_ptr() or None, ldsb, 1 if tile else 0, beta,
-             C.data_ptr() or None, _ld(C, "C"), _value_type(types, C, "C"), ws, ws_bytes))
+             C.data_ptr() or None, ldc, _value_type(types, C, "C"), ws, ws_bytes))
     return C
 
 
