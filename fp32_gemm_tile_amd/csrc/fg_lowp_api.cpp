@@ -69,7 +69,7 @@ struct Plan {
 // 256 x 256 x 65536 33.9 us in one slice, 21.8 in four; 1024 x 1024 x 65536 348
 // and 91 in sixteen), and cost where a sum is short (512 x 512 x 16384 16.8 us in
 // one, 22.0 in two).
-Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
+Plan plan_gemm(int64_t M, int64_t N, int64_t K, size_t ws_bytes) {
     constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
     constexpr double kLaunch = 1.6, kFirst = 1.5, kFinish = 7, kNear = 2.5;  // us
     constexpr double kMaxTiles = 1 << 23;  // of 512 threads: a grid has fewer than 2^32
@@ -80,9 +80,9 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws_bytes) {
     double best_us = 0;
     for (int s = 0; s < fg::fp8_num_shapes(); ++s) {
         const fg::Fp8Shape sh = fg::fp8_shape(s);
-        const double near_us = bf16 ? sh.bf16_us : sh.f32_us;
+        const double near_us = sh.block_us;
         const double tiles = (double)cdiv(M, sh.bm) * (double)cdiv(N, sh.bn);
-        if (near_us == 0 || tiles >= kMaxTiles) continue;
+        if (tiles >= kMaxTiles) continue;
         for (int64_t n = 1; n <= 16; n *= 2) {
             const int64_t per = cdiv(kb, n), used = cdiv(kb, per);
             if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
@@ -159,8 +159,7 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
 
 size_t fg_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
-    const int64_t splits = std::max(plan_gemm(M, N, K, false, (size_t)-1 / 2).splits,
-                                    plan_gemm(M, N, K, true, (size_t)-1 / 2).splits);
+    const int64_t splits = plan_gemm(M, N, K, (size_t)-1 / 2).splits;
     return splits > 1 ? (size_t)(splits * M * N) * 4 : 0;
 }
 
@@ -226,7 +225,7 @@ fg_status fg_gemm_fp8(int64_t M, int64_t N, int64_t K, float alpha, const uint8_
         p.alpha = 0.f;
         return launched(fg::launch_fp8_finish(p, stream), "scaling kernel");
     }
-    const Plan plan = plan_gemm(M, N, K, p.c_bf16, workspace ? workspace_bytes : 0);
+    const Plan plan = plan_gemm(M, N, K, workspace ? workspace_bytes : 0);
     if (plan.shape < 0) return fail(FG_ERR_UNSUPPORTED, 0, "2^23 or more output tiles");
     if ((st = check_device()) != FG_OK) return st;
     p.kb = (int32_t)cdiv(K, fg::kScaleBlock);

@@ -50,7 +50,7 @@ struct Fp8Params {
 struct Fp8Shape {
     int bm, bn;             // rows of A and of B per workgroup
     float start_us;         // of a round of 256 workgroups
-    float bf16_us, f32_us;  // of a block of K in it, by C's type (0: not built)
+    float block_us;         // of a block of K in it
     float far_us;           // at least, from beyond the L2s and one workgroup per CU
 };
 int fp8_num_shapes();

@@ -7,15 +7,12 @@
 // instruction's rows and A's its columns, so a lane holds one row of A (one SA
 // per block) and four consecutive columns of C, stored with one access.
 //
-// Two forms of the block's sum (FP8 below):
-//   * binary32 C: the codes are converted to binary16, which holds them
-//     exactly, and summed by v_mfma_f32_16x16x32_f16: products are exact and
-//     sums binary32.
-//   * bfloat16 C: v_mfma_f32_16x16x128_f8f6f4, twice the rate. It aligns the
-//     products of a block to the largest and drops what lies 2^-14 below it
-//     (measured: 448^2 + x keeps x = 8 and loses x = 4), so a block's sum is
-//     off by about 3e-5 of its size on normal data, far below the 2^-9 of the
-//     rounding to bfloat16; the sums over the blocks are binary32.
+// The codes are converted to binary16, which holds them exactly, and summed by
+// v_mfma_f32_16x16x32_f16: products are exact and sums binary32. (The fp8 matrix
+// instructions have twice the rate, but align the products of a group to the
+// largest and drop what lies 2^-14 below it: 448^2 + x keeps x = 8 and loses
+// x = 4, and where large products cancel the rest of a block's sum is lost, which
+// no rounding of C hides.)
 //
 // Tiles of both operands go from memory straight to LDS (two or three stages, the
 // next blocks in flight while this one is used). A 128-byte row of a tile is eight
@@ -26,10 +23,10 @@
 //
 // Bound by the matrix cores for large results, by HBM for few rows, by the
 // latency of a block (load, LDS, one instruction after the other) in between.
-// Measured on one MI355X: 4096^3, bfloat16 C 61 us (2250 TFLOP/s; the library's
-// product with one scale per matrix 50); 8192^3, binary32 C, beta = 0.5 1050 us
+// Measured on one MI355X: 4096^3, bfloat16 C 133 us (1034 TFLOP/s; 65 with the fp8
+// instruction); 8192^3, binary32 C, beta = 0.5 1050 us
 // (1047 TFLOP/s; the library's binary16 product reaches 1149, and the sums of
-// blocks take a v_fma per element and block beside it); 32 x 8192 x 8192 13.2 us
+// blocks take a v_fma per element and block beside it); 32 x 8192 x 8192 13.6 us
 // (5.2 TB/s); 517 x 2047 x 3001, binary32 C 15.6 us.
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
@@ -42,16 +39,6 @@ typedef int i4v __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f4 mfma_fp8(i8v a, i8v b) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    const f4 z = {0.f, 0.f, 0.f, 0.f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
-#else
-    (void)a, (void)b;
-    return f4{};
-#endif
-}
 
 // Eight codes as binary16, exactly.
 __device__ __forceinline__ h8 codes_to_f16(int lo, int hi) {
@@ -79,7 +66,6 @@ __device__ __forceinline__ f4 mfma_f16(h8 a, h8 b, f4 c) {
 }
 
 // A lane's 32 codes as the operand of a block's sum.
-template <bool FP8>
 struct Operand {
     h8 v[4];
     Operand() = default;
@@ -93,13 +79,6 @@ struct Operand {
         for (int j = 0; j < 4; ++j) t = mfma_f16(v[j], o.v[j], t);
         return t;
     }
-};
-template <>
-struct Operand<true> {
-    i8v v;
-    Operand() = default;
-    __device__ __forceinline__ explicit Operand(i8v c) : v(c) {}
-    __device__ __forceinline__ f4 times(const Operand& o) const { return mfma_fp8(v, o.v); }
 };
 
 // Bytes of a 16-byte chunk that are inside the matrix (left = how many).
@@ -258,7 +237,7 @@ struct Flag {
 // KG groups of waves take the blocks of K in turn, each with its own ring of NS
 // stages and its own sums, which are added in group order at the end: small
 // results get enough waves per SIMD to hide one block's chain of latencies.
-template <int BM, int BN, int WM, int WN, int NS, int KG, bool B_TILE, bool FP8>
+template <int BM, int BN, int WM, int WN, int NS, int KG, bool B_TILE, bool BF16>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kernel(Fp8Params p) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;  // waves of one group
     constexpr int TI = WM / 16, TJ = WN / 16;
@@ -346,12 +325,12 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
         const float* const sc = scales + stage * kScales;
         auto codes = [&](const uint8_t* tile, int r) {
             const i8v c = read_frag(tile, r + n16, g);
-            return Operand<FP8>(TAIL ? keep_codes(c, g, k_left) : c);
+            return Operand(TAIL ? keep_codes(c, g, k_left) : c);
         };
         // B_TILE: the wave's columns lie in WN / 128 blocks of columns, at least one
         constexpr int NB = B_TILE ? (WN + 127) / 128 : 1;
         float s[TI][NB];
-        Operand<FP8> a[TI], b[2];
+        Operand a[TI], b[2];
         b[0] = codes(sb, 0);
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
@@ -446,9 +425,9 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
         const bool busy = kRows <= kMine || lane / kLanes < kMine;
         const bool whole_rows = plain && m0 + wi + 16 * i + 16 <= p.M;
         // (C's old elements on their way during the exchange)
-        Quad<FP8> old[kTurns] = {};
-        uint8_t* const at = Quad<FP8>::at(p, m0 + wi + 16 * i + r0, cj);
-        constexpr int64_t kTurn = kRows * (FP8 ? 2 : 4);
+        Quad<BF16> old[kTurns] = {};
+        uint8_t* const at = Quad<BF16>::at(p, m0 + wi + 16 * i + r0, cj);
+        constexpr int64_t kTurn = kRows * (BF16 ? 2 : 4);
         if (whole_rows && busy && p.beta != 0.f) {
 #pragma unroll
             for (int r = 0; r < kTurns; ++r) old[r].load(at + r * kTurn * p.ldc);
@@ -481,7 +460,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
                 const f4 v = sum_at(r);
                 if (!busy || ci >= p.M || cj >= p.N) continue;
                 if (p.splits > 1) store_ws(p, split, ci, cj, v);
-                else store_c<FP8>(p, ci, cj, v);
+                else store_c<BF16>(p, ci, cj, v);
             }
         }
         sync();
@@ -509,30 +488,25 @@ __global__ void __launch_bounds__(256) fp8_finish_kernel(Fp8Params p) {
     }
 }
 
-template <int BM, int BN, int WM, int WN, int NS, int KG, bool BF16_ONLY = false>
+template <int BM, int BN, int WM, int WN, int NS, int KG>
 hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN) * KG;
     static_assert(threads <= 512, "the host bounds the number of tiles by it");
     const dim3 grid((unsigned)(((p.M + BM - 1) / BM) * (int64_t)((p.N + BN - 1) / BN)),
                     (unsigned)p.splits);
-    const bool fp8 = p.c_bf16;
-#define FG_LAUNCH(BT, F)                                                                       \
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, NS, KG, BT, F>), grid, dim3(threads), 0, stream, p)
-    if (b_tile && fp8) FG_LAUNCH(true, true);
-    else if (fp8) FG_LAUNCH(false, true);
-    else if constexpr (!BF16_ONLY) {
-        if (b_tile) FG_LAUNCH(true, false);
-        else FG_LAUNCH(false, false);
-    } else {
-        return hipErrorInvalidValue;
-    }
+#define FG_LAUNCH(BT, BF)                                                                      \
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WM, WN, NS, KG, BT, BF>), grid, dim3(threads), 0, stream, p)
+    if (b_tile && p.c_bf16) FG_LAUNCH(true, true);
+    else if (p.c_bf16) FG_LAUNCH(false, true);
+    else if (b_tile) FG_LAUNCH(true, false);
+    else FG_LAUNCH(false, false);
 #undef FG_LAUNCH
     return hipGetLastError();
 }
 
 // The tile shapes, with what one costs by estimate: microseconds for the start and
-// end of a round of 256 workgroups, and for a block of K in it, for bfloat16 and
-// for binary32 C, and for a block that comes from beyond the L2s where that is
+// end of a round of 256 workgroups, and for a block of K in it, and for a block
+// that comes from beyond the L2s where that is
 // more (the latency over the loads in flight, with one workgroup on a CU). Fits to
 // 16 .. 2048 x 1024 .. 8192 x 1024 .. 8192 on one MI355X, one to twelve rounds;
 // mostly within 15 %.
@@ -550,17 +524,16 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
 // operands from beyond the L2s (4800 x 112 x 7125 27.6 -> 19.3 us, but
 // 256 x 8192 x 8192, two rounds, 34.5 -> 38.9).
 constexpr Fp8Shape kShapes[] = {
-    {16, 32, 1.5f, 0.070f, 0.074f, 0.f},
-    {32, 32, 2.5f, 0.073f, 0.086f, 0.f},
-    {64, 32, 3.0f, 0.117f, 0.185f, 0.f},
-    {64, 64, 1.5f, 0.22f, 0.31f, 0.45f},
-    {64, 64, 1.5f, 0.30f, 0.45f, 0.f},  // three stages, one workgroup on a CU
-    {80, 64, 3.4f, 0.27f, 0.33f, 0.f},
-    {128, 64, 2.0f, 0.41f, 0.62f, 0.f},
-    {160, 64, 3.5f, 0.52f, 0.65f, 0.f},
-    {128, 128, 3.0f, 0.59f, 0.94f, 0.f},
-    {256, 128, 4.0f, 1.0f, 1.87f, 0.f},
-    {256, 256, 5.0f, 1.7f, 0.f, 0.f},  // bfloat16 C only
+    {16, 32, 1.5f, 0.074f, 0.f},
+    {32, 32, 2.5f, 0.086f, 0.f},
+    {64, 32, 3.0f, 0.185f, 0.f},
+    {64, 64, 1.5f, 0.31f, 0.45f},
+    {64, 64, 1.5f, 0.45f, 0.f},  // three stages, one workgroup on a CU
+    {80, 64, 3.4f, 0.33f, 0.f},
+    {128, 64, 2.0f, 0.62f, 0.f},
+    {160, 64, 3.5f, 0.65f, 0.f},
+    {128, 128, 3.0f, 0.94f, 0.f},
+    {256, 128, 4.0f, 1.87f, 0.f},
 };
 
 }  // namespace
@@ -580,7 +553,6 @@ hipError_t launch_gemm_fp8(int shape, bool b_tile, const Fp8Params& p, hipStream
         case 7: return launch_tile<160, 64, 80, 32, 2, 2>(b_tile, p, stream);
         case 8: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
         case 9: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
-        case 10: return launch_tile<256, 256, 64, 128, 2, 1, true>(b_tile, p, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -82,10 +82,8 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
  *   C(i,j) = alpha * sum_b SA[b*ldsa + i] * SB(b,j) *
  *                    sum_{k in block b} A(i,k) * B(j,k)  +  beta * C(i,j)
  *
- * For binary32 C, products are exact and sums binary32. For bfloat16 C the
- * sum of a block may be taken by the fp8 matrix cores, which drop what lies
- * more than 2^-14 below the block's largest product; the sum over the blocks
- * is binary32. SA * SB of a block is rounded to binary32 first. A's scales are FG_BLOCK_ROW, B's either kind. A linear
+ * Products are exact and sums binary32, whatever C's type. SA * SB of a block
+ * is rounded to binary32 first. A's scales are FG_BLOCK_ROW, B's either kind. A linear
  * layer's three products are all of this form: Y = X W^T (X by rows, W by
  * tiles), dX = dY W (W's transposed codes), dW = dY^T X (both transposed
  * codes, by rows; beta = 1 adds to what is there).

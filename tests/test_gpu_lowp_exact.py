@@ -1,0 +1,89 @@
+"""The 8-bit product and the mixture-of-experts layer where a sum's low bits,
+a factor's range or an infinite operand decides the result."""
+import numpy as np
+import pytest
+
+import fp32_gemm_tile_amd as fg
+from oracle import lowp
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    fg.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+# ---- product -----------------------------------------------------------------
+
+def on_device(codes, scales):
+    """Codes in rows of whole 16 bytes, and scales, on the device."""
+    import torch
+    q = torch.zeros(codes.shape[0], -(-codes.shape[1] // 16) * 16, dtype=torch.uint8, device="cuda")
+    q[:, :codes.shape[1]] = torch.from_numpy(codes).cuda()
+    return q[:, :codes.shape[1]], torch.from_numpy(scales).cuda()
+
+
+def product(A, SA, B, SB, dt, C=None, **kw):
+    import torch
+    M, N, K = A.shape[0], B.shape[0], A.shape[1]
+    if C is None:
+        C = torch.empty(M, N, dtype=dt, device="cuda")
+    ws = torch.empty(max(16, fg.fg_gemm_fp8_workspace_size(M, N, K)), dtype=torch.uint8,
+                     device="cuda")
+    print("  product", M, N, K, tuple(SB.shape), dt, kw, flush=True)
+    fg.gemm_fp8(*on_device(A, SA), *on_device(B, SB), C, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    return C
+
+
+def cancelling(rng, M, N, K, tall):
+    """Codes whose blocks hold 448 * 448 and -448 * 448 beside products of
+    integers -8 .. 8, unit scales, and the exact product."""
+    ints = lowp.nearest_codes(np.arange(-8, 9).astype(np.float64))
+    A, B = rng.choice(ints, (M, K)), rng.choice(ints, (N, K))
+    top, bottom = lowp.nearest_codes(np.array([448.0, -448.0]))
+    for k in range(0, K - 1, 128):
+        i, j = k + rng.permutation(min(128, K - k))[:2]
+        A[:, i], A[:, j], B[:, i], B[:, j] = top, top, top, bottom
+    SA = np.ones((lowp.cdiv(K, 128), M), np.float32)
+    SB = np.ones((lowp.cdiv(K, 128), lowp.cdiv(N, tall)), np.float32)
+    return A, SA, B, SB, lowp.values(A) @ lowp.values(B).T
+
+
+@pytest.mark.parametrize("tall", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 33, 128), (20, 100, 130), (64, 257, 1000), (130, 130, 300),
+                                   (300, 520, 640), (1100, 1030, 256), (2100, 2050, 200)])
+def test_block_sums_keep_what_large_products_leave(M, N, K, tall):
+    """Products of integers of which two per block are +-448^2: every partial
+    sum is an integer below 2^24 and so exact in binary32, whatever the order; C
+    is that sum, or the bfloat16 nearest to it."""
+    import torch
+    A, SA, B, SB, want = cancelling(np.random.default_rng(M + N + K), M, N, K, tall)
+    want = torch.from_numpy(want)
+    for dt in (torch.float32, torch.bfloat16):
+        assert torch.equal(product(A, SA, B, SB, dt).cpu(), want.to(dt))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_small_products_beside_large_ones(out):
+    """Sums of 126 products of 4 beside two of +-448^2: the bound of a binary32
+    sum (4: a unit in the last place of 2^18 for each of 128 additions) is far
+    below the 504 that a sum without the small products would lose."""
+    import torch
+    K, dt = 128, torch.float32 if out == "f32" else torch.bfloat16
+    rng = np.random.default_rng(41)
+    big, two = lowp.nearest_codes(np.array([448.0, 2.0]))
+    for M, N in ((1, 40), (64, 64), (200, 300), (700, 600)):
+        A, B = np.full((M, K), two), np.full((N, K), two)
+        A[:, 0], A[:, 1], B[:, 0], B[:, 1] = big, big | 0x80, big, big
+        perm = rng.permutation(K)
+        C = product(A[:, perm], np.ones((1, M), np.float32), B[:, perm],
+                    np.ones((1, N), np.float32), dt).double()
+        # (504 is a bfloat16; numbers next to it are 2 apart)
+        assert (C - 504.0).abs().max().item() <= 128 * 2.0 ** -5 + (1.0 if out == "bf16" else 0.0)
