@@ -418,7 +418,7 @@ fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_by
     const bool wide = p.wtype == fg::TYPE_F32;  // x and h stay binary32
     p.h_ld = (int32_t)moe_h_ld(I);
     p.h_plane = T * l.top_k * moe_h_ld(I);
-    p.h_bytes = p.h_plane * (wide ? 4 : (p.x_bf16 ? 4 : 6));
+    p.h_bytes = p.h_plane * (wide ? 4 : 6);
     // x is read in place where its rows are aligned and of the operands' type
     const int64_t extent = ((T - 1) * l.ldx + H) * (int64_t)size;
     if (p.vec_x && wide != (p.x_bf16 != 0) && (wide || p.x_bf16) && H % 8 == 0 &&
@@ -436,7 +436,7 @@ fg_status fg_moe(const fg_moe_layer* layer, void* workspace, size_t workspace_by
     }
     // groups: as many tokens as fill 16 columns with the terms of x and of h
     p.gx = fg::moe_group_size(wide || p.x_bf16 ? 1 : 3);
-    p.gh = fg::moe_group_size(wide ? 1 : (p.x_bf16 ? 2 : 3));
+    p.gh = fg::moe_group_size(wide ? 1 : 3);
     p.most_x = (int32_t)most_groups(T, l.top_k, E, p.gx);
     p.most_h = (int32_t)most_groups(T, l.top_k, E, p.gh);
     p.groups_x = reinterpret_cast<fg::MoeGroup*>(ws + space.groups_x);

@@ -23,7 +23,7 @@
 //
 // The products run on v_mfma_f32_16x16x32_bf16 with the 16 weight rows as the
 // instruction's rows and the group's tokens as its columns. e4m3 and bfloat16
-// weights are exact in bfloat16; a binary32 x or h is split into bfloat16
+// weights are exact in bfloat16; a binary32 x and every h are split into bfloat16
 // terms, x = hi + mid + lo, which hold its 24 bits, so the products lose
 // nothing. binary32 weights use v_mfma_f32_16x16x4_f32. A lane owns 32 of the
 // 128 k of a step; which ones does not matter to the sum as long as both
@@ -228,7 +228,7 @@ struct TokenStep<TYPE_F32> {
 template <int WT, bool XBF16>
 struct Terms {
     static constexpr int kX = WT == TYPE_F32 || XBF16 ? 1 : 3;
-    static constexpr int kH = WT == TYPE_F32 ? 1 : (XBF16 ? 2 : 3);
+    static constexpr int kH = WT == TYPE_F32 ? 1 : 3;
     static constexpr int kSize = WT == TYPE_F32 ? 4 : 2;
 };
 

@@ -77,9 +77,8 @@ typedef struct fg_moe_layer {
  *   23 workspace_bytes : at least fg_moe_workspace_size(T, k, E, H, I)
  *   24 stream
  * Products are exact and sums and activations binary32 for every type: an
- * operand that one bfloat16 does not hold is split into the two or three that
- * hold it to binary32's precision or far below the rounding of a bfloat16
- * result. Logits are summed in binary64, so near ones are not exchanged. A
+ * operand that one bfloat16 does not hold is split into the three that hold its
+ * 24 bits. Logits are summed in binary64, so near ones are not exchanged. A
  * token whose slots are all empty gets zeros. tokens == 0: FG_OK, nothing
  * enqueued. Repeated calls give identical bits. An expert chosen twice by one
  * token counts with the sum of the two weights.

@@ -87,3 +87,53 @@ def test_small_products_beside_large_ones(out):
                     np.ones((1, N), np.float32), dt).double()
         # (504 is a bfloat16; numbers next to it are 2 apart)
         assert (C - 504.0).abs().max().item() <= 128 * 2.0 ** -5 + (1.0 if out == "bf16" else 0.0)
+
+
+# ---- layer -------------------------------------------------------------------
+
+WEIGHTS = {"e4m3": "float8_e4m3fn", "bf16": "bfloat16", "f32": "float32"}
+
+
+def experts(values, wt, scale=1.0):
+    """[1, R, C] weights (times 1 / scale, which the codes' scales undo) and, for
+    codes, their scales."""
+    import torch
+    R, C = values.shape
+    t = torch.zeros(1, R, -(-C // 16) * 16, dtype=getattr(torch, WEIGHTS[wt]), device="cuda")
+    t[0, :, :C] = torch.from_numpy(values / scale).float().to(t.dtype).cuda()
+    s = torch.full((1, lowp.cdiv(C, 128), lowp.cdiv(R, 128)), scale, device="cuda")
+    return t[:, :, :C], s
+
+
+def one_expert(x, gate, up, down, wt, scale=1.0, act="none", weight=1.0):
+    """The layer with one expert, which every token chooses."""
+    import torch
+    T = x.shape[0]
+    (g, sg), (u, su), (d, sd) = (experts(v, wt, scale if wt == "e4m3" else 1.0)
+                                 for v in (gate, up, down))
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), weight, device="cuda")
+    print("  layer", T, gate.shape, wt, x.dtype, act, flush=True)
+    out = fg.moe(x, g, u, d, ids, w, torch.empty(T, down.shape[0], dtype=x.dtype, device="cuda"),
+                 scales=(sg, su, sd) if wt == "e4m3" else None, activation=act)
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("wt", ["e4m3", "bf16", "f32"])
+@pytest.mark.parametrize("xt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_h_keeps_its_bits(T, xt, wt):
+    """h[0] = (1 + 2^-12)(1 + 2^-10) and h[1] = 1 + 2^-10 + 2^-12 are binary32
+    numbers whose difference is 2^-22, exact through every sum."""
+    import torch
+    H, I = 24, 20
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -10, 2.0 ** -12
+    gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+    gate[0, [0, 2]], up[0, [0, 1]] = 1.0, 1.0
+    gate[1, 0], up[1, [0, 1, 2]] = 1.0, 1.0
+    down[3, 0], down[3, 1], down[4, 1] = 1.0, -1.0, 2.0
+    out = one_expert(x.to(getattr(torch, xt)), gate, up, down, wt)
+    assert (out[:, 3] == 2.0 ** -22).all()
+    assert (np.abs(out[:, 4] - 2.0) < 2.0 ** -7).all() and (out[:, 5:] == 0).all()
