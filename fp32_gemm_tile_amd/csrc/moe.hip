@@ -60,18 +60,18 @@ __device__ __forceinline__ f4 mfma_f32(float a, float b, f4 c) {
 #endif
 }
 
-// Eight e4m3 codes (two dwords) as bfloat16, exactly.
-__device__ __forceinline__ bf8 codes_to_bf16(int lo, int hi) {
+// Eight e4m3 codes (two dwords) times a power of two as bfloat16, exactly.
+__device__ __forceinline__ bf8 codes_to_bf16(int lo, int hi, float power = 1.f) {
     bf8 v{};
 #if defined(__HIP_DEVICE_COMPILE__)
-    const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-    const bf2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-    const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-    const bf2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+    const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false);
+    const bf2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true);
+    const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false);
+    const bf2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true);
     v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
     v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
 #else
-    (void)lo, (void)hi;
+    (void)lo, (void)hi, (void)power;
 #endif
     return v;
 }
@@ -158,10 +158,10 @@ struct WeightStep {
         }
     }
 
-    // bfloat16 operand j (of 4) of the step
-    __device__ __forceinline__ bf8 frag(int j) const {
+    // bfloat16 operand j (of 4) of the step; codes times `power`
+    __device__ __forceinline__ bf8 frag(int j, float power = 1.f) const {
         if constexpr (WT == TYPE_E4M3) {
-            return codes_to_bf16(v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1]);
+            return codes_to_bf16(v[j >> 1][2 * (j & 1)], v[j >> 1][2 * (j & 1) + 1], power);
         } else {
             return __builtin_bit_cast(bf8, v[j]);
         }
@@ -190,9 +190,10 @@ struct TokenStep {
             t[j] = load16(r, row == kNowhere || k >= cols ? kNowhere : row + (uint32_t)k * 2u);
         }
     }
-    __device__ __forceinline__ f4 times(const WeightStep<WT>& w, f4 c) const {
+    __device__ __forceinline__ f4 times(const WeightStep<WT>& w, f4 c, float power = 1.f) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c = mfma_bf16(w.frag(j), __builtin_bit_cast(bf8, t[j]), c);
+        for (int j = 0; j < 4; ++j)
+            c = mfma_bf16(w.frag(j, power), __builtin_bit_cast(bf8, t[j]), c);
         return c;
     }
 };
@@ -218,6 +219,56 @@ struct TokenStep<TYPE_F32> {
         return c;
     }
 };
+
+// acc[i] += f[i] * (step of w[i] times x), for N matrices: of codes with their
+// block's scale f, else without.
+template <int N, int WT>
+__device__ __forceinline__ void add_step(f4 (&acc)[N], const WeightStep<WT> (&w)[N],
+                                         const TokenStep<WT>& x, const float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (WT == TYPE_E4M3) {
+            const f4 b = x.times(w[i], f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(f[i], b[c], acc[i][c]);
+        } else {
+            acc[i] = x.times(w[i], acc[i]);
+        }
+    }
+}
+
+// A block's sum of codes is taken before its scale, and passes the largest
+// binary32 (a code of 448 beside a value from 2^119 on) where the scaled sum need
+// not. What follows is then infinite or NaN, so that it shows at the end and the
+// loops need not look: where `passed`, they are gone through again with
+// add_step_wide, which takes such a sum from codes times 2^-16, of which 128 add
+// up to less than 1; 2^16 goes into the scale, or into the sum beside a scale that
+// it would make infinite. (A look at every sum cost 4 % of the 16-token layer.)
+template <int N>
+__device__ __forceinline__ bool passed(const f4 (&acc)[N]) {
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) over |= !__builtin_isfinite(acc[i][c]);
+    return __builtin_expect(__ballot(over) != 0, false);
+}
+template <int N, int WT>
+__device__ __forceinline__ void add_step_wide(f4 (&acc)[N], const WeightStep<WT> (&w)[N],
+                                              const TokenStep<WT>& x, const float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const f4 b = x.times(w[i], f4{0.f, 0.f, 0.f, 0.f});
+        const f4 low = x.times(w[i], f4{0.f, 0.f, 0.f, 0.f}, 0x1p-16f);
+        const bool large = fabsf(f[i]) >= 0x1p64f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const bool in = __builtin_isfinite(b[c]);
+            const float v = in ? b[c] : (large ? low[c] * 0x1p16f : low[c]);
+            acc[i][c] = fmaf(in || large ? f[i] : f[i] * 0x1p16f, v, acc[i][c]);
+        }
+    }
+}
 
 // Terms of one value of x and of h, and bytes of one of them. The terms of a
 // token are columns of the matrix instruction next to each other, summed at
@@ -721,20 +772,10 @@ __global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoePar
                 v.f[i] = scale_at(s[i], b * (i & 1 ? p.up.lds : p.gate.lds));
         }
     };
-    auto use = [&](Step& v, int kb) {
+    auto clear = [&](Step& v, int kb) {
         if (kb == steps - 1) {
 #pragma unroll
             for (int i = 0; i < kStreams; ++i) v.w[i].clear_tail(kb, p.H, g);
-        }
-#pragma unroll
-        for (int i = 0; i < kStreams; ++i) {
-            if constexpr (WT == TYPE_E4M3) {
-                const f4 b = v.x.times(v.w[i], f4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(v.f[i], b[c], acc[i][c]);
-            } else {
-                acc[i] = v.x.times(v.w[i], acc[i]);
-            }
         }
     };
     Step v[D];
@@ -744,7 +785,20 @@ __global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoePar
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             fetch(v[(d + D - 1) % D], kb + (d + D - 1) * NW);
-            use(v[d], kb + d * NW);
+            clear(v[d], kb + d * NW);
+            add_step<kStreams, WT>(acc, v[d].w, v[d].x, v[d].f);
+        }
+    }
+    if constexpr (WT == TYPE_E4M3) {
+        if (passed(acc)) {
+#pragma unroll
+            for (int i = 0; i < kStreams; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int kb = wave; kb < steps; kb += NW) {
+                fetch(v[0], kb);
+                clear(v[0], kb);
+                add_step_wide<kStreams, WT>(acc, v[0].w, v[0].x, v[0].f);
+            }
         }
     }
 
@@ -853,32 +907,63 @@ __global__ void __launch_bounds__(64 * down_waves(WT), 2) down_kernel(MoeParams 
         k += stride_k;
         if (k >= steps) k -= steps, ++a;
     };
+    auto expert_of = [&](int a) { return __builtin_amdgcn_readfirstlane(groups[a].expert); };
+    auto row_of = [&](int a) {
+        return n16 / N::kH < groups[a].count
+                   ? (uint32_t)groups[a].pair[n16 / N::kH] * (uint32_t)(p.h_ld * N::kSize) +
+                         (uint32_t)(n16 % N::kH) * (uint32_t)(p.h_plane * N::kSize)
+                   : kNowhere;
+    };
+    // step k of expert e and the lane's row of h; in == false: reads nowhere
+    auto load = [&](Unit& v, int e, uint32_t h_row, int step, bool in) {
+        const int k = in ? step : steps;
+        const __amdgpu_buffer_rsrc_t r = expert_rows<WT>(p.down, e, row0, rows, p.I);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) v.w[i].load(r, at[i], k, p.I, g);
+        v.h.load(rh, h_row, k, p.h_ld, g);
+        if constexpr (WT == TYPE_E4M3) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                v.f[i] = scale_at(p.down.s, e * p.down.s_stride + step * p.down.lds + sb[i]);
+        }
+    };
     auto fetch = [&](Unit& v) {
         const int a = fa < total ? fa : total - 1;
         if (a != last) {
             last = a;
-            fe = __builtin_amdgcn_readfirstlane(groups[a].expert);
-            frow = n16 / N::kH < groups[a].count
-                       ? (uint32_t)groups[a].pair[n16 / N::kH] * (uint32_t)(p.h_ld * N::kSize) +
-                             (uint32_t)(n16 % N::kH) * (uint32_t)(p.h_plane * N::kSize)
-                       : kNowhere;
+            fe = expert_of(a);
+            frow = row_of(a);
         }
-        const int k = fa < total ? fk : steps;  // past the last unit: reads nowhere
-        const __amdgpu_buffer_rsrc_t r = expert_rows<WT>(p.down, fe, row0, rows, p.I);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) v.w[i].load(r, at[i], k, p.I, g);
-        v.h.load(rh, frow, k, p.h_ld, g);
-        if constexpr (WT == TYPE_E4M3) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                v.f[i] = scale_at(p.down.s, fe * p.down.s_stride + fk * p.down.lds + sb[i]);
-        }
+        load(v, fe, frow, fk, fa < total);
         next(fa, fk);
+    };
+    auto clear = [&](Unit& v, int k) {
+        if (k == steps - 1) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) v.w[r].clear_tail(k, p.I, g);
+        }
     };
     f4 acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = f4{0.f, 0.f, 0.f, 0.f};
     auto flush = [&](int a) {
+        if constexpr (WT == TYPE_E4M3) {
+            if (passed(acc)) {  // this wave's units of group a again
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r] = f4{0.f, 0.f, 0.f, 0.f};
+                const int e = expert_of(a);
+                const uint32_t row = row_of(a);
+                int k = first - a * steps;
+                if (k < 0) k += (stride - 1 - k) / stride * stride;
+#pragma unroll 1
+                for (; k < steps; k += stride) {
+                    Unit v;
+                    load(v, e, row, k, true);
+                    clear(v, k);
+                    add_step_wide<RT, WT>(acc, v.w, v.h, v.f);
+                }
+            }
+        }
         // a token's terms are next to each other: their sum in the first
         const int c = n16 / N::kH;
         const bool have = n16 % N::kH == 0 && c < groups[a].count;
@@ -899,17 +984,8 @@ __global__ void __launch_bounds__(64 * down_waves(WT), 2) down_kernel(MoeParams 
         }
     };
     auto use = [&](Unit& v) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (uk == steps - 1) v.w[r].clear_tail(uk, p.I, g);
-            if constexpr (WT == TYPE_E4M3) {
-                const f4 b = v.h.times(v.w[r], f4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(v.f[r], b[i], acc[r][i]);
-            } else {
-                acc[r] = v.h.times(v.w[r], acc[r]);
-            }
-        }
+        clear(v, uk);
+        add_step<RT, WT>(acc, v.w, v.h, v.f);
         const int a = ua;
         next(ua, uk);
         if (ua != a) flush(a);

@@ -137,3 +137,50 @@ def test_h_keeps_its_bits(T, xt, wt):
     out = one_expert(x.to(getattr(torch, xt)), gate, up, down, wt)
     assert (out[:, 3] == 2.0 ** -22).all()
     assert (np.abs(out[:, 4] - 2.0) < 2.0 ** -7).all() and (out[:, 5:] == 0).all()
+
+
+@pytest.mark.parametrize("xt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 6, 64])
+@pytest.mark.parametrize("H,I", [(300, 40), (210, 3000)])
+def test_codes_of_scaled_weights_reach_the_largest_values(H, I, T, xt):
+    """A weight of 1 held as code 256 with scale 2^-8: x and h up to the largest
+    number of their type stay finite, and cancel, though 256 x does not."""
+    import torch
+    dt = getattr(torch, xt)
+    top = float(torch.finfo(dt).max)
+    x = torch.zeros(T, H, device="cuda", dtype=dt)
+    x[:, 0], x[:, 1], x[:, 2], x[:, 200] = top, -top, 2.0 ** -100, 0.5
+    gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+    gate[0, 0], up[0, 2] = 1.0, 1.0                       # h[0] = top 2^-100
+    gate[1, [0, 1, 200]], up[1, 200] = 1.0, 1.0           # h[1] = (top - top + 0.5) 0.5
+    gate[2, 1], up[2, 200] = 1.0, 1.0                  # h[2] = -top / 2
+    gate[3, 200], up[3, 0] = 1.0, 1.0                     # h[3] = top / 2
+    gate[I - 1], up[I - 1] = gate[3], up[3]               # h[I - 1] = top / 2
+    down[0, 0], down[1, 1], down[2, 2], down[3, [2, 3]] = 1.0, 1.0, 1.0, 1.0
+    down[4, 1], down[H - 1, I - 1] = 0.5, 1.0
+    out = one_expert(x, gate, up, down, "e4m3", scale=2.0 ** -8)
+    want = np.array([top * 2.0 ** -100, 0.25, -top / 2, 0.0, 0.125])
+    # (products by powers of two, sums that cancel exactly: every step is exact)
+    np.testing.assert_array_equal(out[:, :5], np.tile(want, (T, 1)))
+    assert (out[:, 5:H - 1] == 0).all() and (out[:, H - 1] == top / 2).all()
+
+
+def test_codes_beside_scales_of_any_size():
+    """Large weights on small tokens and small weights on large ones: the
+    result, not code * x, decides what is finite."""
+    import torch
+    H, I = 140, 33
+    for e in (-126, -60, 0, 60, 119):
+        x = torch.zeros(5, H, device="cuda")
+        x[:, 0], x[:, 130] = 2.0 ** min(127, 8 - e), 1.0
+        gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+        gate[0, 0] = 2.0 ** e * 256
+        g, sg = experts(gate, "e4m3", 2.0 ** e)
+        up[0, 130] = 1.0
+        u, su = experts(up, "e4m3")
+        down[0, 0] = 1.0
+        d, sd = experts(down, "e4m3")
+        ids = torch.zeros(5, 1, dtype=torch.int32, device="cuda")
+        out = fg.moe(x, g, u, d, ids, torch.ones(5, 1, device="cuda"),
+                     torch.empty(5, H, device="cuda"), scales=(sg, su, sd), activation="none")
+        assert (out[:, 0].double() == 2.0 ** (e + 8 + min(127, 8 - e))).all(), e
