@@ -7,8 +7,8 @@
 // instruction's rows and A's its columns, so a lane holds one row of A (one SA
 // per block) and four consecutive columns of C, stored with one access.
 //
-// The codes are converted to binary16, which holds them exactly, and summed by
-// v_mfma_f32_16x16x32_f16: products are exact and sums binary32. (The fp8 matrix
+// The codes are converted to bfloat16, which holds them exactly, and summed by
+// v_mfma_f32_16x16x32_bf16: products are exact and sums binary32. (The fp8 matrix
 // instructions have twice the rate, but align the products of a group to the
 // largest and drop what lies 2^-14 below it: 448^2 + x keeps x = 8 and loses
 // x = 4, and where large products cancel the rest of a block's sum is lost, which
@@ -23,11 +23,12 @@
 //
 // Bound by the matrix cores for large results, by HBM for few rows, by the
 // latency of a block (load, LDS, one instruction after the other) in between.
-// Measured on one MI355X: 4096^3, bfloat16 C 133 us (1034 TFLOP/s; 65 with the fp8
-// instruction); 8192^3, binary32 C, beta = 0.5 1050 us
-// (1047 TFLOP/s; the library's binary16 product reaches 1149, and the sums of
-// blocks take a v_fma per element and block beside it); 32 x 8192 x 8192 13.6 us
-// (5.2 TB/s); 517 x 2047 x 3001, binary32 C 15.6 us.
+// Measured on one MI355X: 4096^3, bfloat16 C 125 us (1100 TFLOP/s; 65 us with the fp8
+// instruction); 8192^3, binary32 C, beta = 0.5 1086 us
+// (1010 TFLOP/s; the library's bfloat16 product reaches 1207, and the sums of
+// blocks take a v_fma per element and block beside it); 32 x 8192 x 8192 14.0 us
+// (4.9 TB/s); 517 x 2047 x 3001, binary32 C 15.8 us. (Factors that always fit and
+// the vote on sums that are not finite are 1.5 to 2.5 % of these.)
 #include "fg_device.h"
 #include "fg_lowp_kernels.h"
 
@@ -36,18 +37,22 @@ namespace {
 
 typedef int i8v __attribute__((ext_vector_type(8)));
 typedef int i4v __attribute__((ext_vector_type(4)));
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b4 __attribute__((ext_vector_type(4)));
 
-// Eight codes as binary16, exactly.
-__device__ __forceinline__ h8 codes_to_f16(int lo, int hi) {
-    h8 v{};
+// Eight codes times kDown as bfloat16, exactly. The products' 2^-64 goes into
+// their factor SA * SB as kUp, which so keeps all its bits however small it is (a
+// factor below 2^-190 adds less than 2^-165); one that is infinite with it, from
+// 2^64 on, leaves infinities or NaN, for which the sums are taken again.
+[[maybe_unused]] constexpr float kDown = 0x1p-32f, kUp = 0x1p64f;
+__device__ __forceinline__ bf8 codes_to_bf16(int lo, int hi) {
+    bf8 v{};
 #if defined(__HIP_DEVICE_COMPILE__)
-    const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
-    const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
-    const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
-    const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+    const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, kDown, false);
+    const bf2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, kDown, true);
+    const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, kDown, false);
+    const bf2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, kDown, true);
     v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
     v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
 #else
@@ -56,9 +61,9 @@ __device__ __forceinline__ h8 codes_to_f16(int lo, int hi) {
     return v;
 }
 
-__device__ __forceinline__ f4 mfma_f16(h8 a, h8 b, f4 c) {
+__device__ __forceinline__ f4 mfma_bf16(bf8 a, bf8 b, f4 c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 #else
     (void)a, (void)b;
     return c;
@@ -67,16 +72,16 @@ __device__ __forceinline__ f4 mfma_f16(h8 a, h8 b, f4 c) {
 
 // A lane's 32 codes as the operand of a block's sum.
 struct Operand {
-    h8 v[4];
+    bf8 v[4];
     Operand() = default;
     __device__ __forceinline__ explicit Operand(i8v c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = codes_to_f16(c[2 * j], c[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) v[j] = codes_to_bf16(c[2 * j], c[2 * j + 1]);
     }
     __device__ __forceinline__ f4 times(const Operand& o) const {
         f4 t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t = mfma_f16(v[j], o.v[j], t);
+        for (int j = 0; j < 4; ++j) t = mfma_bf16(v[j], o.v[j], t);
         return t;
     }
 };
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     // Block kb into a stage. Past the last block: buffers without a byte, zeros.
     // Every wave loads 64 scales of each operand, some of them twice, so that
     // all have the same number of loads in flight.
-    auto fetch = [&](int kb, int stage) {
+    auto fetch = [&](int kb, int stage) __attribute__((always_inline)) {
         const bool more = kb < kb1;
         const uint32_t s = lds0 + stage * kStage, sc = scales0 + stage * kScales * 4;
         const int ca = wave % (kScalesA / 64), cb = wave % (kScalesB / 64);
@@ -306,10 +311,52 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     };
 
     f4 acc[TI][TJ];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
+
+    // B_TILE: the scale of the wave's columns (0 past the last block)
+    static_assert(128 % WN == 0, "the wave's columns are in one block");
+    auto tile_scale = [&](int kb) {
+        if constexpr (!B_TILE) return 1.f;
+        const int64_t jb = (n0 + wj) >> 7;
+        const float s = scale_at(p.SB, (kb < kb1 ? kb : kb1 - 1) * p.ldsb +
+                                           (jb < (p.N + 127) >> 7 ? jb : 0));
+        return kb < kb1 ? s : 0.f;
+    };
+
+    // The block in stage `stage` with factors in binary64.
+    auto use_wide = [&](int kb, int stage) __attribute__((always_inline)) {
+        const uint8_t* const sa = lds + stage * kStage + wi * 128;
+        const uint8_t* const sb = lds + stage * kStage + (BM + wj) * 128;
+        const float* const sc = scales + stage * kScales;
+        auto codes = [&](const uint8_t* tile, int r) {
+            return Operand(keep_codes(read_frag(tile, r + n16, g), g, p.K - kb * 128));
+        };
+        fetch(kb + KG * (NS - 1), stage == 0 ? NS - 1 : stage - 1);
+        const float tile_s = tile_scale(kb);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const Operand b = codes(sb, 16 * j);
+            f4 sj = {tile_s, tile_s, tile_s, tile_s};
+            if constexpr (!B_TILE)
+                sj = *reinterpret_cast<const f4*>(sc + kScalesA + wj + 16 * j + 4 * g);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                asm volatile("" ::: "memory");  // (read again for each: few registers)
+                __builtin_amdgcn_sched_barrier(0);
+                const f4 t = b.times(codes(sa, 16 * i));
+                const double si = (double)sc[wi + 16 * i + n16] * kUp;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = (float)fma(si * (double)sj[e], (double)t[e], (double)acc[i][j][e]);
+            }
+        }
+    };
 
     // The block in stage `stage`: one matrix instruction after the other, column
     // tile by column tile; the sum of the one kAhead before is taken over while
@@ -317,7 +364,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     // kept to this order: left to itself it lines up all reads first and runs
     // out of registers.) The group's block NS - 1 further on is fetched into the
     // stage of the block before.
-    auto use = [&](int kb, int stage, auto tail) {
+    auto use = [&](int kb, int stage, auto tail) __attribute__((always_inline)) {
         constexpr bool TAIL = decltype(tail)::value;
         const int k_left = p.K - kb * 128;
         const uint8_t* const sa = lds + stage * kStage + wi * 128;
@@ -327,24 +374,15 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
             const i8v c = read_frag(tile, r + n16, g);
             return Operand(TAIL ? keep_codes(c, g, k_left) : c);
         };
-        // B_TILE: the wave's columns lie in WN / 128 blocks of columns, at least one
-        constexpr int NB = B_TILE ? (WN + 127) / 128 : 1;
-        float s[TI][NB];
+        const float tile_s = tile_scale(kb);
+        float s[TI];
         Operand a[TI], b[2];
         b[0] = codes(sb, 0);
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
             a[i] = codes(sa, 16 * i);
             const float si = sc[wi + 16 * i + n16];
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                s[i][c] = si;
-                if constexpr (B_TILE) {
-                    const int64_t jb = ((n0 + wj) >> 7) + c;
-                    s[i][c] = si * scale_at(p.SB, (kb < kb1 ? kb : kb1 - 1) * p.ldsb +
-                                                      (jb < (p.N + 127) >> 7 ? jb : 0));
-                }
-            }
+            s[i] = B_TILE ? si * kUp * tile_s : si * kUp;
         }
         constexpr int kAhead = 2, kRing = kAhead + 1, kAll = TI * TJ;
         f4 t[kRing], sj[2];
@@ -352,7 +390,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
             const int i = n % TI, j = n / TI;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float f = B_TILE ? s[i][16 * j / 128] : s[i][0] * sj[j & 1][e];
+                const float f = B_TILE ? s[i] : s[i] * sj[j & 1][e];
                 acc[i][j][e] = fmaf(f, t[n % kRing][e], acc[i][j][e]);
             }
         };
@@ -402,6 +440,37 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
         meet();
         use(kb, stage, Flag<true>{});
     }
+    // Sums that are not finite are taken again with factors in binary64: by all of
+    // the workgroup's waves, which load for each other.
+    __shared__ int votes[NW * KG];
+    f4 zero = {0.f, 0.f, 0.f, 0.f};  // (NaN where a sum is not finite)
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zero[e] = fmaf(acc[i][j][e], 0.f, zero[e]);
+    const float all = zero[0] + zero[1] + zero[2] + zero[3];
+    const int again = __ballot(all != 0.f) != 0;
+    auto done = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    if (lane == 0) votes[wave_id] = again;
+    done();
+    int any = 0;
+#pragma unroll
+    for (int w = 0; w < NW * KG; ++w) any |= votes[w];
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(any) != 0, false)) {
+        clear();
+#pragma unroll
+        for (int d = 0; d < NS - 1; ++d) fetch(kb0 + group + KG * d, d);
+        stage = 0;
+#pragma unroll 1
+        for (int r = 0; r < rounds; ++r) {
+            meet();
+            use_wide(kb0 + group + KG * r, stage);
+            stage = stage + 1 == NS ? 0 : stage + 1;
+        }
+        done();
+    }
 
     // 16 rows at a time through the waves' own parts of the LDS: the groups' sums
     // are added in order, each group taking some of the rows, and a store covers
@@ -412,7 +481,6 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN) * KG) fp8_tile_kern
     static_assert(16 % KG == 0, "rows per group");
     float* const own = reinterpret_cast<float*>(all_lds) + wave * 16 * kPitch;
     const bool plain = p.splits == 1 && n0 + wj + WN <= p.N;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     auto sync = [] {
         if constexpr (KG > 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -83,7 +83,8 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
  *                    sum_{k in block b} A(i,k) * B(j,k)  +  beta * C(i,j)
  *
  * Products are exact and sums binary32, whatever C's type. SA * SB of a block
- * is rounded to binary32 first. A's scales are FG_BLOCK_ROW, B's either kind. A linear
+ * is rounded to binary32 first, but where that would be infinite or lose bits
+ * below the smallest normal number. A's scales are FG_BLOCK_ROW, B's either kind. A linear
  * layer's three products are all of this form: Y = X W^T (X by rows, W by
  * tiles), dX = dY W (W's transposed codes), dW = dY^T X (both transposed
  * codes, by rows; beta = 1 adds to what is there).

@@ -184,3 +184,78 @@ def test_codes_beside_scales_of_any_size():
         out = fg.moe(x, g, u, d, ids, torch.ones(5, 1, device="cuda"),
                      torch.empty(5, H, device="cuda"), scales=(sg, su, sd), activation="none")
         assert (out[:, 0].double() == 2.0 ** (e + 8 + min(127, 8 - e))).all(), e
+
+
+@pytest.mark.parametrize("tall", [1, 128])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_scales_whose_product_leaves_binary32(out, tall):
+    """Factors SA * SB below the smallest and above the largest binary32 number,
+    with results that are inside: rows, columns and blocks of K of many sizes."""
+    import torch
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    rng = np.random.default_rng(43)
+    for M, N, K in ((1, 70, 300), (40, 200, 300), (130, 150, 128), (300, 700, 200)):
+        A, _ = lowp.quantize(rng.standard_normal((M, K)).astype(np.float32), 1)
+        B, _ = lowp.quantize(rng.standard_normal((N, K)).astype(np.float32), 1)
+        A[:, 5], B[:, 5] = 0x38, 0x38                        # (a product of 1 at least)
+        kb = lowp.cdiv(K, 128)
+        for lo, hi in ((-126, -100), (-70, -56), (100, 110), (50, 70), (-126, 120)):
+            e = rng.uniform(lo, hi, (kb, M))
+            SA = (2.0 ** e).astype(np.float32)
+            # results from 2^-120 to 2^100, some lost altogether
+            f = rng.uniform(-150, 90, (kb, lowp.cdiv(N, tall))) - (lo + hi) / 2
+            SB = (2.0 ** np.clip(f, -126, 127)).astype(np.float32)
+            got = product(A, SA, B, SB, dt).double().cpu().numpy()
+            want, bound = lowp.product(A, SA, B, SB, tall)
+            bound = bound + (2 * K + 8) * 2.0 ** -149
+            limit = float(torch.finfo(dt).max)
+            if out == "bf16":
+                bound = bound + lowp.bf16_half_step(np.abs(want) + bound)
+            # (a partial sum may pass the largest number where the terms' sizes do)
+            terms = np.abs(lowp.stands_for(A, SA, 1)) @ np.abs(lowp.stands_for(B, SB, tall)).T
+            inside = terms < limit / 2
+            assert inside.mean() > 0.2
+            err = np.abs(got - want)
+            assert (err <= bound)[inside].all(), (M, N, K, lo, hi)
+            over = np.abs(want) - bound > 2 * limit
+            assert not np.isfinite(got[over]).any()
+
+
+def test_scales_of_blocks_without_codes():
+    """Codes of zeros with scales at the ends: they add nothing, also where the
+    scales' product is infinite or lost."""
+    import torch
+    rng = np.random.default_rng(44)
+    ints = lowp.nearest_codes(np.arange(-8, 9).astype(np.float64))
+    for M, N, K in ((3, 40, 400), (150, 260, 400)):
+        A, B = rng.choice(ints, (M, K)), rng.choice(ints, (N, K))
+        A[M // 2, :256] = 0
+        B[N // 2:, 128:256] = 0
+        SA, SB = np.ones((4, M), np.float32), np.ones((4, N), np.float32)
+        SA[:2, M // 2] = 2.0 ** 127, 2.0 ** -126
+        SB[1, N // 2:] = 2.0 ** 120
+        SB[0, 1], SA[1, 0] = 2.0 ** 6, 2.0 ** 10
+        want = lowp.stands_for(A, SA, 1) @ lowp.stands_for(B, SB, 1).T
+        got = product(A, SA, B, SB, torch.float32)
+        assert torch.equal(got.cpu(), torch.from_numpy(want).float())
+
+
+@pytest.mark.parametrize("tall", [1, 128])
+def test_infinite_scales(tall):
+    """An infinite scale makes its own rows or columns infinite, also in the last
+    block of K, past which groups of waves have no block."""
+    import torch
+    one = 0x38                                               # the code of 1
+    for M, N, K in ((1, 40, 300), (70, 300, 130), (300, 300, 300)):
+        A, B = np.full((M, K), one, np.uint8), np.full((N, K), one, np.uint8)
+        kb = lowp.cdiv(K, 128)
+        SA, SB = np.ones((kb, M), np.float32), np.ones((kb, lowp.cdiv(N, tall)), np.float32)
+        SB[kb - 1, 0] = np.inf
+        SA[0, M - 1] = -np.inf if M > 1 else 1.0
+        got = product(A, SA, B, SB, torch.float32).cpu().numpy()
+        columns = min(tall, N)
+        assert (got[:M - 1, :columns] == np.inf).all() and (got[:M - 1, columns:] == K).all()
+        if M > 1:
+            assert np.isnan(got[M - 1, :columns]).all() and (got[M - 1, columns:] == -np.inf).all()
+        else:
+            assert (got[0, :columns] == np.inf).all() and (got[0, columns:] == K).all()
