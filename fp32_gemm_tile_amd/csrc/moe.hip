@@ -99,6 +99,13 @@ __device__ __forceinline__ void split_bf16(const float (&x)[8], bf8 (&t)[NS]) {
     }
 }
 
+// What a later term's sum adds to the first one's. An infinite weight makes the
+// first infinite (NaN beside 0), and NaN of the later ones, which may be 0 because
+// the value has no more bits.
+__device__ __forceinline__ float beside(float first, float later) {
+    return __builtin_isfinite(first) ? later : 0.f;
+}
+
 // Per weight type: bytes per element, 16-byte pieces of a lane's 32 elements,
 // and the first k (within the step of 128) of piece j of lane group g.
 template <int WT>
@@ -812,12 +819,17 @@ __global__ void __launch_bounds__(64 * NW, D == 1 ? 4 : 2) gate_up_kernel(MoePar
             const int i = row0 + 16 * r + 4 * g + wave;  // component `wave` of the four
             if (n16 < count && i < p.h_ld) {             // column n16: a token here
                 float gs = 0.f, us = 0.f;
-                for (int v = 0; v < NW; ++v)
+                for (int v = 0; v < NW; ++v) {
+                    const f4* const gv = red[v][0] + 16 * g + n16 * N::kX;
+                    const f4* const uv = red[v][1] + 16 * g + n16 * N::kX;
+                    gs += gv[0][wave];
+                    us += uv[0][wave];
 #pragma unroll
-                    for (int t = 0; t < N::kX; ++t) {
-                        gs += red[v][0][16 * g + n16 * N::kX + t][wave];
-                        us += red[v][1][16 * g + n16 * N::kX + t][wave];
+                    for (int t = 1; t < N::kX; ++t) {
+                        gs += beside(gv[0][wave], gv[t][wave]);
+                        us += beside(uv[0][wave], uv[t][wave]);
                     }
+                }
                 const float h = i < p.I ? act_exact(gs, p.act) * us : 0.f;
                 const int64_t to = (int64_t)token_pair * p.h_ld + i;
                 if constexpr (WT == TYPE_F32) {
@@ -975,7 +987,8 @@ __global__ void __launch_bounds__(64 * down_waves(WT), 2) down_kernel(MoeParams 
 #pragma unroll
             for (int t = 1; t < N::kH; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] += __shfl(acc[r][i], (lane + t) & 63, 64);
+                for (int i = 0; i < 4; ++i)
+                    s[i] += beside(acc[r][i], __shfl(acc[r][i], (lane + t) & 63, 64));
             if (have) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[to + 16 * r + i] += f * s[i];

@@ -259,3 +259,33 @@ def test_infinite_scales(tall):
             assert np.isnan(got[M - 1, :columns]).all() and (got[M - 1, columns:] == -np.inf).all()
         else:
             assert (got[0, :columns] == np.inf).all() and (got[0, columns:] == K).all()
+
+
+@pytest.mark.parametrize("wt", ["bf16", "f32"])
+@pytest.mark.parametrize("xt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 9])
+def test_infinite_weights(T, xt, wt):
+    """An infinite weight times a finite value is infinite, times 0 NaN, and
+    reaches its own row of the matrix only."""
+    import torch
+    H, I = 40, 24
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 0.5, 1.0 + 2.0 ** -20
+    gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+    gate[0, 0], up[0, 1] = np.inf, -2.0                 # h[0] = -inf
+    gate[1, 2], up[1, 0] = 1.0, 1.0                     # h[1] = x[2]
+    gate[2, 1], up[2, 3] = 1.0, np.inf                  # h[2] = 0.5 * (inf * 0) = NaN
+    down[0, 0], down[1, 1] = 1.0, -np.inf
+    down[2, 1], down[3, 2] = 1.0, 1.0
+    xx = x.to(getattr(torch, xt))
+    out = one_expert(xx, gate, up, down, wt)
+    # every row of `down` meets h[0] = -inf and h[2] = NaN: all NaN
+    assert np.isnan(out).all()
+    gate[0, 0], up[2, 3] = 1.0, 1.0                     # h[0] = -1, h[2] = 0
+    out = one_expert(xx, gate, up, down, wt)
+    assert (out[:, 0] == -1).all() and (out[:, 1] == -np.inf).all()
+    np.testing.assert_array_equal(out[:, 2], xx[:, 2].double().cpu().numpy())
+    assert (out[:, 3:] == 0).all()
+    gate[0, 0] = np.inf                                 # h[0] = -inf alone, out all of it
+    out = one_expert(xx, gate[:1], up[:1], np.full((H, 1), 0.5), wt)
+    assert (out == -np.inf).all()
