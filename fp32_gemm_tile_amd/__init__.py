@@ -196,6 +196,15 @@ def load_library(path: str = LIB_PATH):
     lib.fg_gemm_fp8.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, i32, f32,
                                 vp, i64, i32, vp, ctypes.c_size_t, vp]
     lib.fg_gemm_fp8.restype = i32
+    lib.fg_fp8_num_tiles.argtypes = []
+    lib.fg_fp8_num_tiles.restype = i32
+    lib.fg_fp8_tile.argtypes = [i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    lib.fg_fp8_tile.restype = i32
+    lib.fg_select_fp8.argtypes = [i64, i64, i64, ctypes.c_size_t, ctypes.POINTER(i32),
+                                  ctypes.POINTER(i32)]
+    lib.fg_select_fp8.restype = i32
+    lib.fg_set_fp8_tile.argtypes = [i32]
+    lib.fg_set_fp8_tile.restype = i32
     lib.fg_gemm_fp8_workspace_size.argtypes = [i64, i64, i64]
     lib.fg_gemm_fp8_workspace_size.restype = ctypes.c_size_t
     if _MOE_RECORD.size != ctypes.sizeof(fg_moe_layer):
@@ -497,6 +506,29 @@ def fg_gemm_fp8(M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, block_b, bet
 
 def fg_gemm_fp8_workspace_size(M, N, K) -> int:
     return load_library().fg_gemm_fp8_workspace_size(M, N, K)
+
+
+def fg_fp8_tiles() -> list:
+    """(rows of A, rows of B) of every tile of fg_gemm_fp8 (include/fp32gemm_tune.h)."""
+    lib, out = load_library(), []
+    for t in range(lib.fg_fp8_num_tiles()):
+        a, b = ctypes.c_int32(), ctypes.c_int32()
+        _raise_if(lib.fg_fp8_tile(t, ctypes.byref(a), ctypes.byref(b)))
+        out.append((a.value, b.value))
+    return out
+
+
+def fg_select_fp8(M, N, K, workspace_bytes=0):
+    """(tile, slices of K) that fg_gemm_fp8 runs (include/fp32gemm_tune.h)."""
+    t, s = ctypes.c_int32(), ctypes.c_int32()
+    _raise_if(load_library().fg_select_fp8(M, N, K, workspace_bytes, ctypes.byref(t),
+                                           ctypes.byref(s)))
+    return t.value, s.value
+
+
+def fg_set_fp8_tile(tile) -> int:
+    """Tile of every later fg_gemm_fp8; -1: the library's choice."""
+    return load_library().fg_set_fp8_tile(tile)
 
 
 def fg_moe(layer, workspace, workspace_bytes, stream=0):

@@ -7,10 +7,12 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "../../include/fp32gemm_fp8.h"
 #include "../../include/fp32gemm_moe.h"
+#include "../../include/fp32gemm_tune.h"
 #include "fg_host.h"
 #include "fg_lowp_kernels.h"
 
@@ -56,6 +58,9 @@ int type_size(int t) { return t == FG_TYPE_F32 ? 4 : (t == FG_TYPE_BF16 ? 2 : 1)
 
 // ---- block-scaled product ----------------------------------------------------
 
+// Tile that every call runs (fg_set_fp8_tile; -1: the cheapest).
+std::atomic<int> g_fp8_tile{-1};
+
 // Shape of the tile kernel and number of slices of K.
 struct Plan {
     int shape;
@@ -78,7 +83,9 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, size_t ws_bytes) {
     const double slice = (double)M * N * 4;
     Plan best{-1, 1};
     double best_us = 0;
+    const int only = g_fp8_tile.load();
     for (int s = 0; s < fg::fp8_num_shapes(); ++s) {
+        if (only >= 0 && s != only) continue;
         const fg::Fp8Shape sh = fg::fp8_shape(s);
         const double near_us = sh.block_us;
         const double tiles = (double)cdiv(M, sh.bm) * (double)cdiv(N, sh.bn);
@@ -155,6 +162,44 @@ fg_status fg_quantize_fp8(fg_type type, fg_block block, int64_t M, int64_t N, co
     p.bf16 = type == FG_TYPE_BF16;
     p.tile = tile;
     return launched(fg::launch_quantize_fp8(p, stream), "quantisation kernel");
+}
+
+int32_t fg_fp8_num_tiles(void) { return fg::fp8_num_shapes(); }
+
+fg_status fg_fp8_tile(int32_t tile, int32_t* rows_a, int32_t* rows_b) {
+    clear_error();
+    if (tile < 0 || tile >= fg::fp8_num_shapes())
+        return fail(FG_ERR_INVALID_ARG, 1, "no tile %d", tile);
+    if (!rows_a) return fail(FG_ERR_INVALID_ARG, 2, "rows_a is NULL");
+    if (!rows_b) return fail(FG_ERR_INVALID_ARG, 3, "rows_b is NULL");
+    *rows_a = fg::fp8_shape(tile).bm;
+    *rows_b = fg::fp8_shape(tile).bn;
+    return FG_OK;
+}
+
+fg_status fg_select_fp8(int64_t M, int64_t N, int64_t K, size_t workspace_bytes, int32_t* tile,
+                        int32_t* slices) {
+    clear_error();
+    if (M <= 0) return fail(FG_ERR_INVALID_ARG, 1, "M < 1");
+    if (N <= 0) return fail(FG_ERR_INVALID_ARG, 2, "N < 1");
+    if (K <= 0) return fail(FG_ERR_INVALID_ARG, 3, "K < 1");
+    if (!tile) return fail(FG_ERR_INVALID_ARG, 5, "tile is NULL");
+    if (!slices) return fail(FG_ERR_INVALID_ARG, 6, "slices is NULL");
+    if (M > kMaxDim || N > kMaxDim || K > FG_MAX_LD)
+        return fail(FG_ERR_UNSUPPORTED, 0, "M and N are limited to 2^30, K to FG_MAX_LD");
+    const Plan plan = plan_gemm(M, N, K, workspace_bytes);
+    if (plan.shape < 0) return fail(FG_ERR_UNSUPPORTED, 0, "2^23 or more output tiles");
+    *tile = plan.shape;
+    *slices = (int32_t)plan.splits;
+    return FG_OK;
+}
+
+fg_status fg_set_fp8_tile(int32_t tile) {
+    clear_error();
+    if (tile < -1 || tile >= fg::fp8_num_shapes())
+        return fail(FG_ERR_INVALID_ARG, 1, "no tile %d", tile);
+    g_fp8_tile.store(tile);
+    return FG_OK;
 }
 
 size_t fg_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {

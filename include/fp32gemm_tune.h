@@ -146,6 +146,27 @@ fg_status fg_get_raster(int32_t* group_m, int32_t* xcd_remap);
  */
 fg_status fg_set_streamk_policy(int32_t policy);
 
+/*
+ * Tiles of fg_gemm_fp8 (fp32gemm_fp8.h), numbered from 0. fg_fp8_num_tiles: how
+ * many there are. fg_fp8_tile: the rows of A (argument 2) and of B (3) of one
+ * workgroup of tile `tile` (1). fg_select_fp8: the tile (argument 5) and the
+ * slices of K (6) that a call of M x N x K runs with workspace_bytes (4; 0: no
+ * workspace); M, N and K positive, else bad argument 1 to 3; FG_ERR_UNSUPPORTED
+ * where the call would be. Outputs non-NULL. Host only.
+ */
+int32_t fg_fp8_num_tiles(void);
+fg_status fg_fp8_tile(int32_t tile, int32_t* rows_a, int32_t* rows_b);
+fg_status fg_select_fp8(int64_t M, int64_t N, int64_t K, size_t workspace_bytes, int32_t* tile,
+                        int32_t* slices);
+
+/*
+ * Tile of every later fg_gemm_fp8 of this process, for tests and measurements:
+ * -1 (the default) the library's choice, else a tile's number (the slices of K are
+ * then the best for it; a grid it cannot cover is FG_ERR_UNSUPPORTED). The
+ * workspace size and fg_select_fp8 follow. FG_ERR_INVALID_ARG for another number.
+ */
+fg_status fg_set_fp8_tile(int32_t tile);
+
 #ifdef __cplusplus
 }
 #endif

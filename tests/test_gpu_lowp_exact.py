@@ -289,3 +289,57 @@ def test_infinite_weights(T, xt, wt):
     gate[0, 0] = np.inf                                 # h[0] = -inf alone, out all of it
     out = one_expert(xx, gate[:1], up[:1], np.full((H, 1), 0.5), wt)
     assert (out == -np.inf).all()
+
+
+# ---- every tile of the product -------------------------------------------------
+
+@pytest.fixture
+def forced():
+    yield fg.fg_set_fp8_tile
+    assert fg.fg_set_fp8_tile(-1) == fg.FG_OK
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("tall", [1, 128])
+def test_every_tile_gives_exact_integers(tall, out, forced):
+    """Each tile kernel, whatever the library would choose: whole and partial
+    tiles, sums of one block to 71 with a partial last one, slices of K, C as it
+    is and scaled into."""
+    import torch
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    rng = np.random.default_rng(45)
+    slices = set()
+    for tile, (m, n) in enumerate(fg.fg_fp8_tiles()):
+        assert forced(tile) == fg.FG_OK
+        for M, N, K in ((1, 5, 130), (m + 3, 2 * n + 1, 300), (2 * m, n, 128), (m - 1, n - 1, 1700),
+                        (m + 1, n + 2, 9000)):
+            need = fg.fg_gemm_fp8_workspace_size(M, N, K)
+            chosen, used = fg.fg_select_fp8(M, N, K, need)
+            assert chosen == tile
+            slices.add(used)
+            A, SA, B, SB, want = cancelling(rng, M, N, K, tall)
+            want = torch.from_numpy(want)
+            print("  tile", tile, (m, n), "slices", used, flush=True)
+            assert torch.equal(product(A, SA, B, SB, dt).cpu(), want.to(dt))
+            C0 = torch.from_numpy(rng.integers(-64, 65, (M, N)).astype(np.float32)).to(dt)
+            C = product(A, SA, B, SB, dt, C0.cuda(), alpha=-2.0, beta=4.0)
+            assert torch.equal(C.cpu(), (-2.0 * want + 4.0 * C0.double()).to(dt))
+    assert 1 in slices and max(slices) > 1
+
+
+def test_every_tile_takes_its_sums_again(forced):
+    """Factors that overflow in some rows and some blocks of K, in every tile."""
+    import torch
+    rng = np.random.default_rng(46)
+    ints = lowp.nearest_codes(np.arange(-8, 9).astype(np.float64))
+    for tile, (m, n) in enumerate(fg.fg_fp8_tiles()):
+        assert forced(tile) == fg.FG_OK
+        for M, N, K, tall in ((m + 5, n + 9, 700, 1), (2 * m, n + 1, 700, 128)):
+            A, B = rng.choice(ints, (M, K)), rng.choice(ints, (N, K))
+            SA = np.ones((lowp.cdiv(K, 128), M), np.float32)
+            SB = np.ones((lowp.cdiv(K, 128), lowp.cdiv(N, tall)), np.float32)
+            A[3], SA[:, 3] = 0, 2.0 ** 127          # a row of zeros
+            SB[2], SA[2] = 2.0 ** 125, 2.0 ** -120  # a block of factors 2^5
+            want = lowp.stands_for(A, SA, 1) @ lowp.stands_for(B, SB, tall).T
+            got = product(A, SA, B, SB, torch.float32)
+            assert torch.equal(got.cpu(), torch.from_numpy(want).float())
