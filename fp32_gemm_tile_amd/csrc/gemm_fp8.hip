@@ -586,17 +586,13 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
 // 517 x 2047 x 3001 80 x 64 15.6 us, 64 x 64 19.9, 128 x 128 29.4;
 // 2048 x 1024 x 1024 128 x 64 9.3 us, 64 x 64 9.9, 128 x 128 12.1;
 // 600 x 4096 x 4096 160 x 64 26.8 us, 64 x 64 36.2, 128 x 128 34.5.
-//   A third stage pays where the load is longer than the block (bfloat16 C,
-// 128 x 64: 944 x 1675 x 5460 29.9 -> 23.9 us, 256 x 8192 x 8192 39.2 -> 29.4); at
-// 64 x 64 it costs the second workgroup on the CU, and pays for one round of
-// operands from beyond the L2s (4800 x 112 x 7125 27.6 -> 19.3 us, but
-// 256 x 8192 x 8192, two rounds, 34.5 -> 38.9).
+//   A third stage at 64 x 64 costs the second workgroup on the CU (256 x 8192 x 8192
+// 49 -> 65 us, 4800 x 112 x 7125 28.5, where 80 x 64 takes 24.8).
 constexpr Fp8Shape kShapes[] = {
     {16, 32, 1.5f, 0.074f, 0.f},
     {32, 32, 2.5f, 0.086f, 0.f},
     {64, 32, 3.0f, 0.185f, 0.f},
     {64, 64, 1.5f, 0.31f, 0.45f},
-    {64, 64, 1.5f, 0.45f, 0.f},  // three stages, one workgroup on a CU
     {80, 64, 3.4f, 0.33f, 0.f},
     {128, 64, 2.0f, 0.62f, 0.f},
     {160, 64, 3.5f, 0.65f, 0.f},
@@ -615,12 +611,11 @@ hipError_t launch_gemm_fp8(int shape, bool b_tile, const Fp8Params& p, hipStream
         case 1: return launch_tile<32, 32, 32, 32, 2, 8>(b_tile, p, stream);
         case 2: return launch_tile<64, 32, 64, 32, 3, 4>(b_tile, p, stream);
         case 3: return launch_tile<64, 64, 32, 32, 2, 2>(b_tile, p, stream);
-        case 4: return launch_tile<64, 64, 32, 32, 3, 2>(b_tile, p, stream);
-        case 5: return launch_tile<80, 64, 80, 32, 2, 4>(b_tile, p, stream);
-        case 6: return launch_tile<128, 64, 64, 32, 3, 2>(b_tile, p, stream);
-        case 7: return launch_tile<160, 64, 80, 32, 2, 2>(b_tile, p, stream);
-        case 8: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
-        case 9: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
+        case 4: return launch_tile<80, 64, 80, 32, 2, 4>(b_tile, p, stream);
+        case 5: return launch_tile<128, 64, 64, 32, 3, 2>(b_tile, p, stream);
+        case 6: return launch_tile<160, 64, 80, 32, 2, 2>(b_tile, p, stream);
+        case 7: return launch_tile<128, 128, 64, 64, 2, 2>(b_tile, p, stream);
+        case 8: return launch_tile<256, 128, 64, 64, 3, 1>(b_tile, p, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -48,3 +48,13 @@ def test_slices_need_their_workspace():
                 assert fg.fg_select_fp8(M, N, K, need - 1)[1] < slices
                 split += 1
     assert split > 0
+
+
+def test_every_tile_is_chosen_somewhere():
+    """No tile is built that no call reaches."""
+    sizes = [(1, 8192, 8192), (32, 8192, 8192), (64, 8192, 8192), (517, 2047, 3001),
+             (2048, 1024, 1024), (600, 4096, 4096), (2048, 2048, 2048), (4096, 4096, 4096)]
+    sizes += [(M, N, K) for M in (64, 128, 256, 512, 1024) for N in (512, 1000, 2048)
+              for K in (256, 1024, 4096)]
+    chosen = {fg.fg_select_fp8(*s, fg.fg_gemm_fp8_workspace_size(*s))[0] for s in sizes}
+    assert chosen == set(range(len(fg.fg_fp8_tiles())))
