@@ -574,18 +574,20 @@ hipError_t launch_tile(bool b_tile, const Fp8Params& p, hipStream_t stream) {
 
 // The tile shapes, with what one costs by estimate: microseconds for the start and
 // end of a round of 256 workgroups, and for a block of K in it, and for a block
-// that comes from beyond the L2s where that is
-// more (the latency over the loads in flight, with one workgroup on a CU). Fits to
-// 16 .. 2048 x 1024 .. 8192 x 1024 .. 8192 on one MI355X, one to twelve rounds;
-// mostly within 15 %.
+// that comes from beyond the L2s where that is more (the latency over the loads in
+// flight, with one workgroup on a CU). The estimates rank, and are no more than
+// that: at 25 sizes of 1 to 8192 rows, both types of C, operands from HBM, the tile
+// chosen took at most 13 % more than the best one, but 6 to 45 % more than its
+// estimate, which has no term for C's bytes, and 78 % more where those are most of
+// the work (7984 x 6830 x 80, binary32 C).
 //   The tiles of up to 64 x 32 are for few rows: many groups of K, so that the
-// whole of a CU's LDS is in flight (bfloat16, 1 x 8192 x 8192 11.5 us = 5.8 TB/s;
-// 32 rows 13.1 us, 64 rows 14.8, with the 64 x 64 tile 32).
+// whole of a CU's LDS is in flight (1 x 8192 x 8192 15.5 us; 32 rows 18.0,
+// 64 rows 23.7; with the 64 x 64 tile 21.2, 22.5 and 24.4).
 //   The tiles between 64 x 64 and 128 x 128 save results that a smaller tile
 // takes in two rounds and a larger one in less than one (binary32 C):
-// 517 x 2047 x 3001 80 x 64 15.6 us, 64 x 64 19.9, 128 x 128 29.4;
-// 2048 x 1024 x 1024 128 x 64 9.3 us, 64 x 64 9.9, 128 x 128 12.1;
-// 600 x 4096 x 4096 160 x 64 26.8 us, 64 x 64 36.2, 128 x 128 34.5.
+// 517 x 2047 x 3001 80 x 64 16.2 us, 64 x 64 20.8, 128 x 128 29.6;
+// 600 x 4096 x 4096 160 x 64 29.6 us, 64 x 64 38.3, 128 x 128 37.4;
+// 944 x 1675 x 5460 128 x 64 36.1 us, 80 x 64 44.8, 128 x 128 39.9.
 //   A third stage at 64 x 64 costs the second workgroup on the CU (256 x 8192 x 8192
 // 49 -> 65 us, 4800 x 112 x 7125 28.5, where 80 x 64 takes 24.8).
 constexpr Fp8Shape kShapes[] = {
