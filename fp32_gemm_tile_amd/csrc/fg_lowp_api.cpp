@@ -71,9 +71,9 @@ struct Plan {
 // blocks of K one after the other, or the stream of both operands; slices of K
 // (at most 16) cost another kernel and their partial sums' way to memory and
 // back. Slices pay for small results of long sums (bfloat16 C, the best tile each:
-// 256 x 256 x 65536 33.9 us in one slice, 21.8 in four; 1024 x 1024 x 65536 348
-// and 91 in sixteen), and cost where a sum is short (512 x 512 x 16384 16.8 us in
-// one, 22.0 in two).
+// 256 x 256 x 65536 44.0 us in one slice, 23.6 in four; 1024 x 1024 x 65536 199
+// and 136 in eight, where four are chosen, 141), and cost where a sum is short
+// (512 x 512 x 16384 19.3 us in one, 26.1 in two).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, size_t ws_bytes) {
     constexpr double kCUs = 256, kStream = 6.5e6, kPartial = 4e6;  // bytes per us
     constexpr double kLaunch = 1.6, kFirst = 1.5, kFinish = 7, kNear = 2.5;  // us

@@ -14,8 +14,8 @@
 //            atomics on values: repeated calls are identical.
 //
 // Measured (one MI355X; the experts' types e4m3, bfloat16, e4m3 and binary32):
-// 1 token, 2 of 8 experts of 1024 x 512: route 3.0 us, top-k 2.4, gate/up 6.6,
-// down 5.1; 8 tokens, 6 of 64 of 2048 x 1408: 5.5, 6.9, 79, 40; 16 tokens, 8 of
+// 1 token, 2 of 8 experts of 1024 x 512: route 3.1 us, top-k 2.4, gate/up 6.6,
+// down 5.4; 8 tokens, 6 of 64 of 2048 x 1408: 5.5, 6.9, 79, 40; 16 tokens, 8 of
 // 128 of 4096 x 1536: 7.6, 8.0, 178 (5.8 TB/s of the weights), 96 (5.4 TB/s);
 // 64 routed tokens, 2 of 16 of 2048 x 2000: plan 5, 98 (5.3 TB/s), 51 (5.1 TB/s).
 // Route, top-k and plan are chains of latencies. A read of that many bytes

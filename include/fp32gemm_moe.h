@@ -78,7 +78,7 @@ typedef struct fg_moe_layer {
  *   24 stream
  * Products are exact and sums and activations binary32 for every type: an
  * operand that one bfloat16 does not hold is split into the three that hold its
- * 24 bits. Logits are summed in binary64, so near ones are not exchanged. A
+ * 24 bits (of values below 2^-110 those down to 2^-133). Logits are summed in binary64, so near ones are not exchanged. A
  * token whose slots are all empty gets zeros. tokens == 0: FG_OK, nothing
  * enqueued. Repeated calls give identical bits. An expert chosen twice by one
  * token counts with the sum of the two weights.
