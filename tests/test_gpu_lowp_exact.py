@@ -343,3 +343,19 @@ def test_every_tile_takes_its_sums_again(forced):
             want = lowp.stands_for(A, SA, 1) @ lowp.stands_for(B, SB, tall).T
             got = product(A, SA, B, SB, torch.float32)
             assert torch.equal(got.cpu(), torch.from_numpy(want).float())
+
+
+@pytest.mark.parametrize("wt", ["e4m3", "bf16", "f32"])
+def test_small_values_keep_their_bits(wt):
+    """x and h down to 2^-109 hold 24 bits (their last terms are bfloat16 numbers
+    below the normal ones)."""
+    import torch
+    H, I = 24, 20
+    for e in (-80, -100, -105, -109):
+        small = 2.0 ** e * (1 + 2.0 ** -11 + 2.0 ** -23)
+        x = torch.zeros(3, H, device="cuda")
+        x[:, 0], x[:, 1] = small, 1.0
+        gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+        gate[2, 0], up[2, 1], down[4, 2] = 1.0, 1.0, -2.0
+        out = one_expert(x, gate, up, down, wt)
+        assert (out[:, 4] == -2.0 * small).all(), e
