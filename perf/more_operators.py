@@ -115,7 +115,6 @@ def prepare(case, seed):
             zeros = torch.round(7.5 + 1.5 * normal(cdiv(K, group), N)).clamp(0, 15).to(torch.uint8) if case["zeros"] else None
             s["weights"].append((codes, scales, zeros))
         s["out"] = torch.empty(T, N, dtype=dt, device="cuda")
-        s["workspace"] = torch.empty(16 << 20, dtype=torch.uint8, device="cuda")
         return s
     T, H, I = (case[n] for n in ("T", "H", "I"))
     s["x"] = padded(T, H, dt)
@@ -184,8 +183,8 @@ def run(s):
         import fp32_gemm_tile_amd as fg
         if case["op"] == "int4":
             if case["gated"]:
-                return fg.gated_int4(s["x"], s["weights"][0], s["weights"][1], s["out"], group=case["group"], workspace=s["workspace"])
-            return fg.gemm_int4(s["x"], s["weights"][0], s["out"], group=case["group"], workspace=s["workspace"])
+                return fg.gated_int4(s["x"], s["weights"][0], s["weights"][1], s["out"], group=case["group"])
+            return fg.gemm_int4(s["x"], s["weights"][0], s["out"], group=case["group"])
         if case["op"] == "backward":
             fg.gated_backward(s["dh"], s["x"], s["gate"], s["up"], s["saved"], s["dx"], s["dgate"], s["dup"], out=s["h"], beta=case["beta"],
                               activation=case["act"], workspace=s["workspace"])
