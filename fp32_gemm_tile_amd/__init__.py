@@ -13,6 +13,8 @@ Entry points (same names as the C ABI):
   fg_num_configs(), fg_get_config(i), fg_select_config(...)
   fg_last_bad_arg(), fg_last_error(), fg_status_string(s), fg_abi_version()
   fg_quantize_fp8(...), fg_gemm_fp8(...), fg_moe(layer, ...)
+  fg_gated(block, ...), fg_gated_backward(block, grads, ...), fg_gemm_int4(...),
+  fg_gated_int4(...)
 Convenience:
   sgemm(A, B, C, alpha, beta, transA, transB, config=-1, stream=None)
       for torch tensors on the GPU (PyTorch only supplies memory and stream).
@@ -21,6 +23,10 @@ Convenience:
       e4m3 codes with a scale for each block of 128 (include/fp32gemm_fp8.h)
   moe(x, gate, up, down, ids, weights, out, router, ...)
       a mixture-of-experts layer for a few tokens (include/fp32gemm_moe.h)
+  gated(x, gate, up, out, saved=...), gated_backward(dout, x, gate, up, saved, ...)
+      a gated feed-forward block and its gradients (include/fp32gemm_gated.h)
+  gemm_int4(x, weights, out, group), gated_int4(x, gate, up, out, group)
+      a few rows beside weights of 4 bits (include/fp32gemm_int4.h)
 """
 from __future__ import annotations
 
@@ -99,6 +105,36 @@ class fg_moe_layer(ctypes.Structure):
                 ("router", ctypes.c_void_p), ("ldr", ctypes.c_int64),
                 ("router_type", ctypes.c_int32), ("ids", ctypes.c_void_p),
                 ("weights", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64)]
+
+
+FG_SAVE_NONE, FG_SAVE_SAME, FG_SAVE_E4M3 = 0, 1, 2
+FG_INT4_MAX_ROWS = 64
+
+
+class fg_gated_block(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ldgate", ctypes.c_int64),
+                ("up", ctypes.c_void_p), ("ldup", ctypes.c_int64), ("save", ctypes.c_int32),
+                ("g", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("u", ctypes.c_void_p), ("ldu", ctypes.c_int64),
+                ("sg", ctypes.c_void_p), ("ldsg", ctypes.c_int64),
+                ("su", ctypes.c_void_p), ("ldsu", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64)]
+
+
+class fg_gated_grads(ctypes.Structure):
+    _fields_ = [("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dgate", ctypes.c_void_p), ("lddgate", ctypes.c_int64),
+                ("dup", ctypes.c_void_p), ("lddup", ctypes.c_int64), ("beta", ctypes.c_float)]
+
+
+class fg_int4(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("s", ctypes.c_void_p), ("lds", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64)]
 
 
 def make_quant(kind, out, ldq, row_factor=0):
@@ -213,6 +249,36 @@ def load_library(path: str = LIB_PATH):
     lib.fg_moe.restype = i32
     lib.fg_moe_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.fg_moe_workspace_size.restype = ctypes.c_size_t
+    size = ctypes.c_size_t
+    if (_BLOCK_RECORD.size != ctypes.sizeof(fg_gated_block)
+            or _GRADS_RECORD.size != ctypes.sizeof(fg_gated_grads)
+            or _INT4_RECORD.size != ctypes.sizeof(fg_int4)):
+        raise ImportError("gated block: the packed records do not match the structures")
+    lib.fg_gated.argtypes = [ctypes.POINTER(fg_gated_block), vp, size, vp]
+    lib.fg_gated.restype = i32
+    lib.fg_gated_backward.argtypes = [ctypes.POINTER(fg_gated_block),
+                                      ctypes.POINTER(fg_gated_grads), vp, size, vp]
+    lib.fg_gated_backward.restype = i32
+    lib.fg_gated_workspace_size.argtypes = [i64, i64, i64, i32]
+    lib.fg_gated_workspace_size.restype = size
+    lib.fg_gated_backward_min_workspace_size.argtypes = [i64, i64, i32]
+    lib.fg_gated_backward_min_workspace_size.restype = size
+    lib.fg_gated_backward_workspace_size.argtypes = [i64, i64, i64, i32]
+    lib.fg_gated_backward_workspace_size.restype = size
+    int4_args = [i64, i64, i64, i32, i32, i32, vp, i64, ctypes.POINTER(fg_int4)]
+    lib.fg_gemm_int4.argtypes = int4_args + [vp, i64, vp]
+    lib.fg_gemm_int4.restype = i32
+    lib.fg_gated_int4.argtypes = int4_args + [ctypes.POINTER(fg_int4), i32, vp, i64, vp]
+    lib.fg_gated_int4.restype = i32
+    lib.fg_gated_num_tiles.argtypes = [i32, i32]
+    lib.fg_gated_num_tiles.restype = i32
+    lib.fg_gated_tile.argtypes = [i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    lib.fg_gated_tile.restype = i32
+    lib.fg_select_gated.argtypes = [i32, i32, i64, i64, i64, size, ctypes.POINTER(i32),
+                                    ctypes.POINTER(i32)]
+    lib.fg_select_gated.restype = i32
+    lib.fg_set_gated_tile.argtypes = [i32, i32, i32, i32]
+    lib.fg_set_gated_tile.restype = i32
     lib.fg_estimate_seconds.argtypes = [i64, i64, i64, i32, i32, i32]
     lib.fg_estimate_seconds.restype = ctypes.c_double
     lib.fg_get_efficiency.argtypes = [i32, ctypes.POINTER(ctypes.c_double),
@@ -541,6 +607,72 @@ def fg_moe_workspace_size(tokens, top_k, experts, hidden, inner) -> int:
     return load_library().fg_moe_workspace_size(tokens, top_k, experts, hidden, inner)
 
 
+def fg_gated(block, workspace=0, workspace_bytes=0, stream=0):
+    """Raw call with an fg_gated_block; see include/fp32gemm_gated.h."""
+    ref = ctypes.byref(block) if block is not None else None
+    return load_library().fg_gated(ref, workspace or None, workspace_bytes, stream or None)
+
+
+def fg_gated_backward(block, grads, workspace=0, workspace_bytes=0, stream=0):
+    """Raw call with an fg_gated_block and an fg_gated_grads."""
+    ref = ctypes.byref(block) if block is not None else None
+    dref = ctypes.byref(grads) if grads is not None else None
+    return load_library().fg_gated_backward(ref, dref, workspace or None, workspace_bytes,
+                                            stream or None)
+
+
+def fg_gated_workspace_size(tokens, hidden, inner, type) -> int:
+    return load_library().fg_gated_workspace_size(tokens, hidden, inner, type)
+
+
+def fg_gated_backward_min_workspace_size(tokens, inner, type) -> int:
+    return load_library().fg_gated_backward_min_workspace_size(tokens, inner, type)
+
+
+def fg_gated_backward_workspace_size(tokens, hidden, inner, type) -> int:
+    return load_library().fg_gated_backward_workspace_size(tokens, hidden, inner, type)
+
+
+def fg_gemm_int4(T, N, K, group, type, scale_type, x, ldx, w, out, ldo, stream=0):
+    """Raw call with an fg_int4; see include/fp32gemm_int4.h."""
+    return load_library().fg_gemm_int4(T, N, K, group, type, scale_type, x or None, ldx,
+                                       ctypes.byref(w) if w is not None else None, out or None,
+                                       ldo, stream or None)
+
+
+def fg_gated_int4(T, N, K, group, type, scale_type, x, ldx, gate, up, activation, out, ldo,
+                  stream=0):
+    """Raw call with two fg_int4; see include/fp32gemm_int4.h."""
+    return load_library().fg_gated_int4(T, N, K, group, type, scale_type, x or None, ldx,
+                                        ctypes.byref(gate) if gate is not None else None,
+                                        ctypes.byref(up) if up is not None else None, activation,
+                                        out or None, ldo, stream or None)
+
+
+def fg_gated_tiles(product, type) -> list:
+    """(rows, columns) of every tile of a product of the gated block: 0 forward,
+    1 dx, 2 dgate and dup (include/fp32gemm_tune.h)."""
+    lib, out = load_library(), []
+    for t in range(lib.fg_gated_num_tiles(product, type)):
+        a, b = ctypes.c_int32(), ctypes.c_int32()
+        _raise_if(lib.fg_gated_tile(product, type, t, ctypes.byref(a), ctypes.byref(b)))
+        out.append((a.value, b.value))
+    return out
+
+
+def fg_select_gated(product, type, T, H, I, workspace_bytes=0):
+    """(tile, slices of the sum) of a product of the gated block (include/fp32gemm_tune.h)."""
+    t, s = ctypes.c_int32(), ctypes.c_int32()
+    _raise_if(load_library().fg_select_gated(product, type, T, H, I, workspace_bytes,
+                                             ctypes.byref(t), ctypes.byref(s)))
+    return t.value, s.value
+
+
+def fg_set_gated_tile(product, type, tile=-1, slices=0) -> int:
+    """Tile and slices of every later product of that kind; -1, 0: the library's choice."""
+    return load_library().fg_set_gated_tile(product, type, tile, slices)
+
+
 def configs() -> list:
     return [fg_get_config(i) for i in range(fg_num_configs())]
 
@@ -846,4 +978,171 @@ def moe(x, gate, up, down, ids, weights, out, router=None, renormalize=True, sca
         1 if renormalize else 0, x.data_ptr(), _ld(x, "x"), *g, *u, *d, rp, ldr, rt,
         ids.data_ptr(), weights.data_ptr(), out.data_ptr(), _ld(out, "out")))
     _run_on(torch, dev, stream, load_library().fg_moe, (layer, ws, ws_bytes))
+    return out
+
+
+# ---- gated feed-forward block and 4-bit weights -------------------------------
+
+# the structures as packed records (quicker than ctypes constructors)
+_BLOCK_RECORD = struct.Struct("@3q2iPqPqPqiPqPqPqPqPq")
+_GRADS_RECORD = struct.Struct("@PqPqPqPqf0q")
+_INT4_RECORD = struct.Struct("@PqPqPq")
+
+
+def _matrix(t, name, dev, rows, cols, dtype, align=1):
+    """(address, leading dimension) of a rows x cols tensor; align: elements whose
+    multiples rows start at (one row's stride is free)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (rows, cols) or t.get_device() != dev:
+        _wrong(name, f"be {rows} x {cols} on device {dev}, is {tuple(t.shape)} on {t.device}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        _wrong(name, "have unit stride along its rows")
+    if rows <= 1 or cols == 0:
+        ld = (max(1, cols) + align - 1) // align * align
+    return t.data_ptr(), ld
+
+
+def _kept(torch, types, saved, dev, T, I, dtype):
+    """fg_save and the addresses and leading dimensions of (G, U) or of (codes and
+    scales of G, codes and scales of U)."""
+    if saved is None:
+        return FG_SAVE_NONE, (0, 1, 0, 1, 0, 1, 0, 1)
+    if len(saved) == 2:
+        return FG_SAVE_SAME, (*_matrix(saved[0], "saved gate", dev, T, I, dtype),
+                              *_matrix(saved[1], "saved up", dev, T, I, dtype), 0, 1, 0, 1)
+    if len(saved) != 4:
+        raise ValueError("saved must be (G, U) or (G's codes, G's scales, U's codes, U's scales)")
+    gq, gs, uq, us = saved
+    ldg, ldu = _codes(types, gq, "saved gate", dev, T, I), _codes(types, uq, "saved up", dev, T, I)
+    kb = (I + 127) // 128
+    ldsg = _scales(torch, gs, "scales of saved gate", dev, kb, T)
+    ldsu = _scales(torch, us, "scales of saved up", dev, kb, T)
+    return FG_SAVE_E4M3, (gq.data_ptr(), ldg, uq.data_ptr(), ldu, gs.data_ptr(), ldsg,
+                          us.data_ptr(), ldsu)
+
+
+def _scratch(torch, dev, stream, need):
+    """A workspace from torch, on the stream that the call uses."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        raise ValueError("a raw stream handle needs a workspace")
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+        return torch.empty(max(16, need), dtype=torch.uint8, device=torch.device("cuda", dev))
+
+
+def gated(x, gate, up, out, activation="silu", saved=None, workspace=None, stream=None):
+    """out <- act(x @ gate.T) * (x @ up.T) for x [T, H], gate and up [I, H], out [T, I],
+    all float32 or all bfloat16; rows of x, gate and up start at multiples of 16 bytes.
+    saved: tensors that x @ gate.T and x @ up.T are written to for gated_backward: two
+    [T, I] of x's type, or (codes, scales, codes, scales) as empty_fp8(T, I) makes them,
+    or None. workspace: a contiguous GPU tensor that no call running at the same time
+    uses (fg_gated_workspace_size bytes are useful), or None. Returns out. Enqueued on
+    ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
+    dev = _gpu(x, "x")
+    ty, dt = _value_type(types, x, "x"), x.dtype
+    (T, H), I = x.shape, gate.shape[0]
+    per = 4 if ty == FG_TYPE_F32 else 8
+    save, kept = _kept(torch, types, saved, dev, T, I, dt)
+    ws, ws_bytes = _workspace(workspace, dev)
+    block = fg_gated_block.from_buffer_copy(_BLOCK_RECORD.pack(
+        T, H, I, ty, activation_code(activation), *_matrix(x, "x", dev, T, H, dt, per),
+        *_matrix(gate, "gate", dev, I, H, dt, per), *_matrix(up, "up", dev, I, H, dt, per),
+        save, *kept, *_matrix(out, "out", dev, T, I, dt)))
+    _run_on(torch, dev, stream, load_library().fg_gated, (block, ws, ws_bytes))
+    return out
+
+
+def gated_backward(dout, x, gate, up, saved, dx=None, dgate=None, dup=None, out=None, beta=0.0,
+                   activation="silu", workspace=None, stream=None):
+    """Gradients of gated from out's, dout [T, I], and what it saved: dx [T, H], dgate and
+    dup [I, H] (added to beta times what they hold), and out [T, I] itself again; each may be
+    None, dgate and dup together. workspace: a contiguous GPU tensor of at least
+    fg_gated_backward_min_workspace_size(T, I, type) bytes (more is used up to
+    fg_gated_backward_workspace_size) that no call running at the same time uses; None
+    allocates one with torch. Enqueued on ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
+    dev = _gpu(dout, "dout")
+    ty, dt = _value_type(types, dout, "dout"), dout.dtype
+    (T, I), H = dout.shape, x.shape[1]
+    per = 4 if ty == FG_TYPE_F32 else 8
+    save, kept = _kept(torch, types, saved, dev, T, I, dt)
+
+    def given(t, name, rows, cols):
+        return (0, max(1, cols)) if t is None else _matrix(t, name, dev, rows, cols, dt)
+
+    block = fg_gated_block.from_buffer_copy(_BLOCK_RECORD.pack(
+        T, H, I, ty, activation_code(activation), *_matrix(x, "x", dev, T, H, dt, per),
+        *_matrix(gate, "gate", dev, I, H, dt, per), *_matrix(up, "up", dev, I, H, dt, per),
+        save, *kept, *given(out, "out", T, I)))
+    grads = fg_gated_grads.from_buffer_copy(_GRADS_RECORD.pack(
+        *_matrix(dout, "dout", dev, T, I, dt), *given(dx, "dx", T, H),
+        *given(dgate, "dgate", I, H), *given(dup, "dup", I, H), beta))
+    if workspace is None:
+        workspace = _scratch(torch, dev, stream, fg_gated_backward_workspace_size(T, H, I, ty))
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run_on(torch, dev, stream, load_library().fg_gated_backward, (block, grads, ws, ws_bytes))
+
+
+def _int4(torch, types, w, name, dev, N, K, group):
+    """fg_type of the scales and the fg_int4 of (codes, scales, zero points or None)."""
+    q, s, z = w
+    if q.dtype != torch.uint8:
+        raise TypeError(f"codes of {name} must be uint8")
+    half, groups = (K + 1) // 2, (K + group - 1) // group
+    if q.shape != (N, half) or s.shape != (groups, N) or not q.get_device() == s.get_device() == dev:
+        _wrong(name, f"have {N} x {half} bytes of codes and {groups} x {N} scales on device {dev}")
+    ty = _value_type(types, s, f"scales of {name}")
+    ldq, iq = q.stride()
+    lds, is_ = s.stride()
+    if (half > 1 and iq != 1) or (N > 1 and is_ != 1):
+        _wrong(name, "have unit stride along its rows")
+    zp = ldz = 0
+    if z is not None:
+        if z.dtype != torch.uint8:
+            raise TypeError(f"zero points of {name} must be uint8")
+        ldz, iz = z.stride() if z.dim() == 2 else (0, 0)
+        if z.shape != (groups, N) or z.get_device() != dev or (N > 1 and iz != 1):
+            _wrong(f"zero points of {name}", f"be {groups} x {N} on device {dev}")
+        zp = z.data_ptr()
+    return ty, fg_int4.from_buffer_copy(_INT4_RECORD.pack(
+        q.data_ptr(), ldq if N > 1 and half else (half + 15) // 16 * 16, s.data_ptr(),
+        lds if groups > 1 else max(N, 1), zp, ldz if groups > 1 else max(N, 1)))
+
+
+def gemm_int4(x, weights, out, group=128, stream=None):
+    """out <- x @ W.T for at most 64 rows x [T, K] (float32 or bfloat16, rows at multiples
+    of 16 bytes) and W [N, K] of 4 bits: weights = (codes, scales, zero points or None), codes
+    uint8 [N, ceil(K / 2)] with rows at multiples of 16 bytes (column c in byte c // 2, an
+    even one in the low half), scales (float32 or bfloat16) and zero points (uint8, else 8)
+    [ceil(K / group), N]; W = scale * (code - zero). group: 32, 64 or 128. Returns out.
+    Enqueued on ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
+    dev = _gpu(x, "x")
+    ty, dt = _value_type(types, x, "x"), x.dtype
+    (T, K), N = x.shape, out.shape[1]
+    st, w = _int4(torch, types, weights, "weights", dev, N, K, group)
+    xp, ldx = _matrix(x, "x", dev, T, K, dt, 4 if ty == FG_TYPE_F32 else 8)
+    _run_on(torch, dev, stream, load_library().fg_gemm_int4,
+            (T, N, K, group, ty, st, xp, ldx, w, *_matrix(out, "out", dev, T, N, dt)))
+    return out
+
+
+def gated_int4(x, gate, up, out, group=128, activation="silu", stream=None):
+    """out <- act(x @ gate.T) * (x @ up.T) for 4-bit gate and up [N, K], each (codes,
+    scales, zero points or None) as gemm_int4 takes them, with scales of one type.
+    Returns out. Enqueued on ``stream`` (default: torch's current stream)."""
+    torch, types = _torch_types()
+    dev = _gpu(x, "x")
+    ty, dt = _value_type(types, x, "x"), x.dtype
+    (T, K), N = x.shape, out.shape[1]
+    st, g = _int4(torch, types, gate, "gate", dev, N, K, group)
+    ut, u = _int4(torch, types, up, "up", dev, N, K, group)
+    if st != ut:
+        raise TypeError("scales of gate and up must have one type")
+    xp, ldx = _matrix(x, "x", dev, T, K, dt, 4 if ty == FG_TYPE_F32 else 8)
+    _run_on(torch, dev, stream, load_library().fg_gated_int4,
+            (T, N, K, group, ty, st, xp, ldx, g, u, activation_code(activation),
+             *_matrix(out, "out", dev, T, N, dt)))
     return out

@@ -1,0 +1,104 @@
+// Internal interface between the host side of the gated feed-forward and 4-bit
+// entry points (fg_gated_api.cpp) and their kernels. Not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fg_lowp_kernels.h"
+
+namespace fg {
+
+enum : int32_t { SAVE_NONE = 0, SAVE_SAME = 1, SAVE_E4M3 = 2 };
+
+// ---- a few rows of x beside weights that are streamed once -------------------
+
+// A matrix of weights, N x K: values of x's type, or 4-bit codes with a scale (and
+// a zero point, or 8) for each `group` columns of a row.
+struct RowsWeights {
+    const uint8_t* w;
+    int64_t ld;            // bytes
+    const void* s;         // S[b * lds + n]
+    int64_t lds;
+    const uint8_t* z;      // Z[b * ldz + n], or null
+    int64_t ldz;
+};
+struct RowsParams {
+    int32_t T, N, K;
+    int32_t x_bf16;
+    int32_t act;           // gated only
+    int32_t group;         // 4-bit codes; 0: weights of x's type
+    int32_t s_bf16;
+    int32_t matrices;      // 1: out = x W^T; 2: out = act(x W0^T) * (x W1^T)
+    const void* x;
+    int64_t ldx;           // elements
+    RowsWeights w[2];
+    void* out;
+    int64_t ldo;
+    void* save[2];         // both products in x's type, or null
+    int64_t ld_save[2];
+};
+constexpr int kRowsMaxTokens = 64;
+hipError_t launch_rows(const RowsParams& p, hipStream_t stream);
+
+
+// ---- many rows: tile kernels ---------------------------------------------------
+
+// The three products of the gated block. Two matrices each of what differs between
+// gate and up; K and the steps below count one of them.
+//   FORWARD  G = A B0^T, U = A B1^T, C[0] = act(G) * U; A is T x H, B I x H
+//   DX       C[0] = A0 B0 + A1 B1; A (the gradients of G and U) T x I, B I x H
+//   DW       C[i] = Ai^T B0 + beta C[i]; A T x I, B0 (x) T x H
+enum : int32_t { GATED_FORWARD = 0, GATED_DX = 1, GATED_DW = 2 };
+struct GatedTileParams {
+    const void* A[2];
+    const void* B[2];
+    int64_t lda, ldb[2];   // elements
+    int32_t M, N, K;       // rows and columns of C, length of one sum
+    void* C[2];
+    int64_t ldc[2];
+    float beta;
+    // FORWARD: what is kept of G and U (values, or codes with their scales)
+    int32_t act, save;
+    void* saved[2];
+    int64_t ld_saved[2];
+    float* scales[2];
+    int64_t ld_scales[2];
+    // Slices of the sum: slice s takes steps [s * per_split, (s + 1) * per_split),
+    // its partial sums of matrix i are the dense M x N ws + (2 s + i) M N (DX: one
+    // matrix, ws + s M N).
+    int32_t steps, per_split, splits;
+    float* ws;
+};
+struct GatedShape {
+    int bm, bn;            // rows and columns of C per workgroup
+    int kb;                // bytes of k per step
+    float start_us;        // of a round of 256 workgroups
+    float step_us;         // of a step in it
+};
+int gated_num_shapes(int op, bool bf16);
+GatedShape gated_shape(int op, bool bf16, int shape);
+hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
+                             hipStream_t stream);
+// What follows a launch with several slices.
+hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream);
+
+// Gradients of G and U from h's: du = dh * act(g), dg = dh * u * act'(g), both T x I
+// with rows of ld_d elements (a multiple of 64, zeros past I), and h = act(g) * u
+// (or null).
+struct GatedGradParams {
+    int32_t T, I, act, save;   // SAVE_SAME or SAVE_E4M3
+    const void* dh;
+    int64_t lddh;
+    const void* saved[2];
+    int64_t ld_saved[2];
+    const float* scales[2];
+    int64_t ld_scales[2];
+    void *dg, *du;
+    int64_t ld_d;
+    void* h;
+    int64_t ldh;
+};
+hipError_t launch_gated_grad(bool bf16, const GatedGradParams& p, hipStream_t stream);
+
+}  // namespace fg

@@ -1,0 +1,751 @@
+// The products of a gated feed-forward block on the matrix cores, for many rows:
+//
+//   FORWARD  G = x Wg^T, U = x Wu^T, h = act(G) * U; G and U kept in h's type, as
+//            e4m3 codes with a scale per 1 x 128 block, or not at all
+//   DX       dx = dG Wg + dU Wu
+//   DW       dWg = dG^T x, dWu = dU^T x (+ beta times what was there)
+//
+// One kernel for all: B's rows are the instruction's rows and A's its columns, so a
+// lane holds one row of C and four consecutive columns of it. FORWARD's tile of B
+// is half gate and half up, divided so that a wave has both products of the same columns and
+// the activation needs no exchange. DX runs through gate's steps and then up's into
+// the same sums. bfloat16 products are exact and their sums binary32
+// (v_mfma_f32_16x16x32_bf16); binary32 uses v_mfma_f32_16x16x4_f32.
+//
+// Tiles go from memory straight to LDS, NS stages, the next ones in flight while
+// one is used. An operand stored along k (x and the weights in FORWARD, dG and dU in
+// DX) has rows of KB bytes of k whose 16-byte chunks are exchanged so that the 16
+// rows a wave reads together fall on different banks. One stored along m or n (the
+// weights in DX, all of DW) keeps its order in memory, a row of LDS per k, and is
+// transposed by the read (ds_read_b64_tr_b16: 4 k of 16 columns per 16 lanes), so no
+// transposed copy is ever made.
+#include "fg_device.h"
+#include "fg_e4m3.h"
+#include "fg_gated_kernels.h"
+#include "fg_lds_tile.h"
+
+namespace fg {
+namespace {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+template <bool BF16>
+__device__ __forceinline__ f4 mfma(i4v a, i4v b, f4 c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (BF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
+                                                       __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    } else {
+        const f4 fa = __builtin_bit_cast(f4, a), fb = __builtin_bit_cast(f4, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
+    }
+#else
+    (void)a, (void)b;
+#endif
+    return c;
+}
+
+// 4 k of 16 columns per 16 lanes: lane l gives the address of row l / 4, columns
+// 4 (l % 4), and gets column l of the four rows.
+__device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                   (__attribute__((address_space(3))) s4*)(uint32_t)(uintptr_t)(
+                       __attribute__((address_space(3))) const uint8_t*)p));
+#else
+    (void)p;
+    return uint2{0, 0};
+#endif
+}
+
+// Elements [0, left) of a 16-byte chunk, zeros after them.
+template <bool BF16>
+__device__ __forceinline__ i4v keep(i4v v, int left) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        if constexpr (!BF16) {
+            v[d] = d < left ? v[d] : 0;
+        } else {
+            const int n = left - 2 * d;
+            v[d] &= n >= 2 ? -1 : (n == 1 ? 0xFFFF : 0);
+        }
+    }
+    return v;
+}
+
+// A tile of R rows (of m or n) and KB bytes of k, and how it gets to LDS and back.
+// ALONG_K: stored with k along its rows.
+template <bool BF16, bool ALONG_K, int R, int KB, int NW>
+struct Tile {
+    static constexpr int kSize = BF16 ? 2 : 4;
+    static constexpr int kBytes = R * KB;
+    static constexpr int kParts = kBytes / 1024 / NW;         // loads of one wave
+    static_assert(kBytes % (1024 * NW) == 0, "whole loads per wave");
+    static constexpr int kSteps = KB / kSize;                 // k of a step
+    static constexpr int kRowBytes = ALONG_K ? KB : R * kSize;  // of a row in LDS
+    static constexpr int kLanesPerRow = kRowBytes / 16;
+    static constexpr int kRowsPerLoad = 64 / kLanesPerRow;
+    static_assert(ALONG_K || (BF16 && R >= 64), "only 16-bit elements are transposed");
+
+    // Exchange of the 16-byte chunks of LDS row r: chunk c is at position c ^ turn(r).
+    // ALONG_K: the 16 rows read together cover the 256 bytes of all banks once.
+    // Else the eight rows that 32 lanes read together do.
+    static __device__ __forceinline__ int turn(int r) {
+        if constexpr (ALONG_K) return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+        else if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
+        else return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
+    }
+    // Byte offset, from the tile's first element, of what lane `lane` loads in load i
+    // of the tile.
+    static __device__ __forceinline__ uint32_t source(int i, int lane, int64_t ld) {
+        const int r = i * kRowsPerLoad + lane / kLanesPerRow;
+        const int c = (lane % kLanesPerRow) ^ turn(r);
+        return (uint32_t)(r * ld * kSize) + (uint32_t)(c * 16);
+    }
+    // The chunk of 16 k-bytes of row r0 + n16 (r0 a multiple of 16) that lane (n16,
+    // g) gives to the instruction, in sub-step `sub` of 64 bytes of k: k = 8 g .. 8 g + 7
+    // (4 g .. 4 g + 3 for binary32) either way.
+    static __device__ __forceinline__ i4v read(const uint8_t* tile, int r0, int sub, int lane) {
+        const int n16 = lane & 15, g = lane >> 4;
+        if constexpr (ALONG_K) {
+            return *reinterpret_cast<const i4v*>(tile + (r0 + n16) * KB +
+                                                 (((sub * 4 + g) ^ turn(n16)) << 4));
+        } else {
+            const int k = 32 * sub + 8 * g + (n16 >> 2);
+            const uint8_t* at = tile + k * kRowBytes + (n16 & 1) * 8 +
+                                (((r0 / 8 + ((n16 >> 1) & 1)) ^ turn(8 * g + (n16 >> 2))) << 4);
+            const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * kRowBytes);
+            return i4v{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+        }
+    }
+};
+
+// Four values of C's type at an element of any alignment.
+template <bool BF16>
+struct Quad {
+    uint32_t u[BF16 ? 2 : 4];
+    __device__ __forceinline__ void load(const uint8_t* c) { __builtin_memcpy(u, c, sizeof u); }
+    __device__ __forceinline__ f4 values() const {
+        f4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = __builtin_bit_cast(float, !BF16 ? u[e % (BF16 ? 2 : 4)]
+                                                   : (e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16));
+        return v;
+    }
+    __device__ __forceinline__ explicit Quad(f4 v) {
+        if constexpr (BF16) {
+            typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+            const b4 r = __builtin_convertvector(v, b4);
+            __builtin_memcpy(u, &r, sizeof u);
+        } else {
+            __builtin_memcpy(u, &v, sizeof u);
+        }
+    }
+    Quad() = default;
+    // the first n of them
+    __device__ __forceinline__ void store(uint8_t* c, int n) const {
+        if (n >= 4) {
+            __builtin_memcpy(c, u, sizeof u);
+        } else if constexpr (BF16) {
+            for (int e = 0; e < n; ++e)
+                reinterpret_cast<uint16_t*>(c)[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+        } else {
+            for (int e = 0; e < n; ++e) reinterpret_cast<uint32_t*>(c)[e] = u[e];
+        }
+    }
+};
+
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(GatedTileParams p) {
+    constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
+    constexpr int TI = WM / 16, TJ = WN / 16;
+    constexpr int SIZE = BF16 ? 2 : 4;
+    constexpr bool kDual = OP == GATED_FORWARD;
+    // (FORWARD: BN rows of B are BN / 2 of gate and BN / 2 of up)
+    constexpr int kCols = kDual ? BN / 2 : BN;       // columns of C per workgroup
+    constexpr int kWaveCols = kDual ? WN / 2 : WN;
+    constexpr int PJ = kDual ? TJ / 2 : TJ;          // column tiles of one matrix
+    using TA = Tile<BF16, OP != GATED_DW, BM, KB, NW>;
+    using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW>;
+    constexpr int kStage = TA::kBytes + TB::kBytes;
+    constexpr int K1 = TA::kSteps;                   // k of a step
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage];
+
+    const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wi = (wave % NWM) * WM, wj = (wave / NWM) * kWaveCols;
+    const int tiles_m = (p.M + BM - 1) / BM;
+    int tm, tn;
+    tile_of(blockIdx.x, gridDim.x, OP == GATED_DW ? 2 * tiles_m : tiles_m,
+            (p.N + kCols - 1) / kCols, tm, tn);
+    const int which = OP == GATED_DW && tm >= tiles_m ? 1 : 0;
+    if (OP == GATED_DW && which) tm -= tiles_m;
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kCols;
+    const int rows = p.M - m0 < BM ? (int)(p.M - m0) : BM;
+    const int cols = p.N - n0 < kCols ? (int)(p.N - n0) : kCols;
+    const int split = blockIdx.y;
+    const int s0 = split * p.per_split;
+    const int s1 = s0 + p.per_split < p.steps ? s0 + p.per_split : p.steps;
+    const int half = OP == GATED_DX ? p.steps / 2 : p.steps;   // steps of one matrix
+
+    // 16-byte pieces that exist in a row of n elements, in bytes
+    auto whole = [](int64_t n) { return (n * SIZE + 15) & ~15ll; };
+    uint32_t src_a[TA::kParts], src_b[TB::kParts];
+#pragma unroll
+    for (int q = 0; q < TA::kParts; ++q) src_a[q] = TA::source(wave + NW * q, lane, p.lda);
+    // (FORWARD: the second half of B's rows are up's first ones)
+    constexpr int kHalfLoads = TB::kBytes / 1024 / 2;
+#pragma unroll
+    for (int q = 0; q < TB::kParts; ++q) {
+        const int i = wave + NW * q;
+        if constexpr (kDual) {
+            const int u = i >= kHalfLoads;
+            src_b[q] = TB::source(i - u * kHalfLoads, lane, p.ldb[u]);
+        } else {
+            src_b[q] = TB::source(i, lane, OP == GATED_DX ? p.ldb[0] : p.ldb[0]);
+        }
+    }
+    auto at = [](const void* base, int64_t element) {
+        return static_cast<const uint8_t*>(base) + element * SIZE;
+    };
+    auto bounded = [](int64_t bytes) {
+        return bytes < 0 ? (int64_t)0 : (bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes);
+    };
+    const uint32_t lds0 = lds_address(lds);
+
+    // Step s into a stage; past the last one buffers without a byte, which read as zero.
+    auto fetch = [&](int s, int stage) __attribute__((always_inline)) {
+        const uint32_t to = lds0 + stage * kStage;
+        const bool more = s < s1;
+        const int m = OP == GATED_DX && s >= half ? 1 : 0;
+        const int64_t k = (int64_t)(s - (m ? half : 0)) * K1;
+        i4v ra, rb[2];
+        if constexpr (OP == GATED_DW) {
+            ra = buffer_words(at(p.A[which], k * p.lda + m0),
+                              bounded((p.K - k - 1) * p.lda * SIZE + whole(p.M) - m0 * SIZE));
+        } else {
+            const int64_t row = whole(p.K) - k * SIZE;
+            ra = buffer_words(at(p.A[m], m0 * p.lda + k), bounded((rows - 1) * p.lda * SIZE + row));
+        }
+        if constexpr (kDual) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                rb[u] = buffer_words(at(p.B[u], n0 * p.ldb[u] + k),
+                                     bounded((cols - 1) * p.ldb[u] * SIZE + whole(p.K) - k * SIZE));
+        } else {
+            rb[0] = buffer_words(at(p.B[m], k * p.ldb[m] + n0),
+                                 bounded((p.K - k - 1) * p.ldb[m] * SIZE + whole(p.N) - n0 * SIZE));
+        }
+        if (!more) ra[2] = rb[0][2] = 0;
+        if (kDual && !more) rb[1][2] = 0;
+#pragma unroll
+        for (int q = 0; q < TA::kParts; ++q) dma16(ra, to + (wave + NW * q) * 1024, src_a[q]);
+#pragma unroll
+        for (int q = 0; q < TB::kParts; ++q) {
+            const int i = wave + NW * q;
+            dma16(kDual && i >= kHalfLoads ? rb[1] : rb[0], to + TA::kBytes + i * 1024, src_b[q]);
+        }
+    };
+
+    f4 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+
+    // row of B's tile that column tile j of the wave starts at
+    auto b_row = [&](int j) {
+        return kDual ? (j < PJ ? 0 : BN / 2) + wj + 16 * (j % PJ) : wj + 16 * j;
+    };
+    auto use = [&](int stage, int left, auto tail) __attribute__((always_inline)) {
+        const uint8_t* const ta = lds + stage * kStage;
+        const uint8_t* const tb = ta + TA::kBytes;
+#pragma unroll
+        for (int sub = 0; sub < KB / 64; ++sub) {
+            i4v a[TI], b[TJ];
+            auto kept = [&](i4v v) {
+                constexpr int kPer = 16 / SIZE;
+                if constexpr (decltype(tail)::value) return keep<BF16>(v, left - (sub * 4 + g) * kPer);
+                else return v;
+            };
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) b[j] = kept(TB::read(tb, b_row(j), sub, lane));
+#pragma unroll
+            for (int i = 0; i < TI; ++i) a[i] = kept(TA::read(ta, wi + 16 * i, sub, lane));
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) acc[i][j] = mfma<BF16>(b[j], a[i], acc[i][j]);
+        }
+    };
+
+    constexpr int kLoads = TA::kParts + TB::kParts;
+    static_assert((NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
+    auto meet = [] {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
+                     : "memory");
+    };
+    // (FORWARD: the last step may end inside a row; elsewhere k runs over rows, of
+    // which those past the last are zeros)
+    const bool partial = kDual && s1 == p.steps && p.K % K1 != 0;
+    const int whole_end = partial ? s1 - 1 : s1;
+    int stage = 0;
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d) fetch(s0 + d, d);
+    for (int s = s0; s < whole_end; ++s) {
+        meet();
+        fetch(s + NS - 1, stage == 0 ? NS - 1 : stage - 1);
+        use(stage, 0, Flag<false>{});
+        stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+    if constexpr (kDual) {
+        if (partial) {
+            meet();
+            fetch(s1 + NS - 2, stage == 0 ? NS - 1 : stage - 1);
+            use(stage, p.K - (s1 - 1) * K1, Flag<true>{});
+        }
+    }
+    auto all_done = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    all_done();
+
+    // The wave's 16 rows at a time through its own part of the LDS, so that a store
+    // covers consecutive elements of a row.
+    constexpr int kPitch = kWaveCols + 4, kLanes = kWaveCols / 4, kRows = 64 / kLanes;
+    static_assert(NW * 16 * kPitch * 4 + (kDual ? 2 * NWN * BM * 4 : 0) <= NS * kStage,
+                  "the stages hold the waves' rows");
+    float* const own = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+    const int er = lane / kLanes, ec = (lane % kLanes) * 4;
+    auto settle = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+    // of(j): column tile j of row tile i; to(row, column, value) for every quad
+    auto by_rows = [&](int i, auto of, auto to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < PJ; ++j)
+            *reinterpret_cast<f4*>(own + n16 * kPitch + 16 * j + 4 * g) = of(j);
+        settle();
+        f4 v[16 / kRows];
+#pragma unroll
+        for (int r = 0; r < 16 / kRows; ++r)
+            v[r] = *reinterpret_cast<const f4*>(own + (r * kRows + er) * kPitch + ec);
+        settle();
+#pragma unroll
+        for (int r = 0; r < 16 / kRows; ++r) {
+            const int64_t row = m0 + wi + 16 * i + r * kRows + er, col = n0 + wj + ec;
+            if (row < p.M && col < p.N) to(row, col, v[r]);
+        }
+    };
+    auto put = [&](void* base, int64_t ld, int64_t row, int64_t col, const f4& v) {
+        const int n = p.N - col < 4 ? (int)(p.N - col) : 4;
+        Quad<BF16>(v).store(static_cast<uint8_t*>(base) + (row * ld + col) * SIZE, n);
+    };
+    if (p.splits > 1) {
+        const int64_t slice = (int64_t)p.M * p.N;
+        constexpr int kEach = OP == GATED_DX ? 1 : 2;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int m = 0; m < (kDual ? 2 : 1); ++m)
+                by_rows(i, [&](int j) { return acc[i][m * PJ + j]; },
+                        [&](int64_t row, int64_t col, const f4& v) {
+                            const int n = p.N - col < 4 ? (int)(p.N - col) : 4;
+                            Quad<false>(v).store(
+                                reinterpret_cast<uint8_t*>(p.ws + (split * kEach + which + m) * slice +
+                                                           row * p.N + col), n);
+                        });
+        return;
+    }
+    if constexpr (kDual) {
+        if (p.save == SAVE_E4M3) {
+            // The largest finite magnitude of each row in the workgroup's 128 columns:
+            // of the wave's, then of its neighbours' along the row.
+            static_assert(kCols % 128 == 0 || kCols < 128, "whole blocks, or no codes");
+            if constexpr (kCols % 128 == 0) {
+                uint32_t* const most = reinterpret_cast<uint32_t*>(lds + NW * 16 * kPitch * 4);
+                constexpr int kPerBlock = 128 / kWaveCols;   // waves
+                const int wn = wave / NWM;
+                uint32_t mine[2][TI];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < TI; ++i) {
+                        uint32_t v = 0;
+#pragma unroll
+                        for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v = max(v, finite_magnitude(acc[i][m * PJ + j][e]));
+                        v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+                        v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+                        mine[m][i] = v;
+                        if (g == 0) most[(m * NWN + wn) * BM + wi + 16 * i + n16] = v;
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t v = mine[m][i];
+                        const int w0 = wn / kPerBlock * kPerBlock;
+#pragma unroll
+                        for (int w = 0; w < kPerBlock; ++w)
+                            v = max(v, most[(m * NWN + w0 + w) * BM + wi + 16 * i + n16]);
+                        const float s = scale_of(v);
+                        const Divisor d = divisor_of(s);
+                        const int64_t row = m0 + wi + 16 * i + n16, col = n0 + wj;
+                        if (g == 0 && wn == w0 && row < p.M)
+                            p.scales[m][col / 128 * p.ld_scales[m] + row] = s;
+                        // codes: a dword per lane and column tile, rows of kWaveCols bytes
+                        uint8_t* const bytes = reinterpret_cast<uint8_t*>(own);
+#pragma unroll
+                        for (int j = 0; j < PJ; ++j)
+                            *reinterpret_cast<uint32_t*>(bytes + n16 * (kWaveCols + 4) + 16 * j + 4 * g) =
+                                codes4(acc[i][m * PJ + j], [&](int) { return d[0]; }, [&](int) { return d; });
+                        settle();
+                        uint32_t c[16 / kRows];
+#pragma unroll
+                        for (int r = 0; r < 16 / kRows; ++r)
+                            c[r] = *reinterpret_cast<const uint32_t*>(
+                                bytes + (r * kRows + er) * (kWaveCols + 4) + ec);
+                        settle();
+#pragma unroll
+                        for (int r = 0; r < 16 / kRows; ++r) {
+                            const int64_t cr = m0 + wi + 16 * i + r * kRows + er, cc = n0 + wj + ec;
+                            if (cr >= p.M || cc >= p.N) continue;
+                            uint8_t* q = static_cast<uint8_t*>(p.saved[m]) + cr * p.ld_saved[m] + cc;
+                            if (cc + 4 <= p.N) *reinterpret_cast<uint32_t*>(q) = c[r];
+                            else
+                                for (int e = 0; e < 3 && cc + e < p.N; ++e) q[e] = (uint8_t)(c[r] >> (8 * e));
+                        }
+                    }
+            }
+        } else if (p.save == SAVE_SAME) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    by_rows(i, [&](int j) { return acc[i][m * PJ + j]; },
+                            [&](int64_t row, int64_t col, const f4& v) {
+                                put(p.saved[m], p.ld_saved[m], row, col, v);
+                            });
+        }
+        auto products = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                by_rows(i,
+                        [&](int j) {
+                            f4 h;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = activate_t<decltype(act)::value>(acc[i][j][e]) * acc[i][PJ + j % PJ][e];
+                            return h;
+                        },
+                        [&](int64_t row, int64_t col, const f4& v) { put(p.C[0], p.ldc[0], row, col, v); });
+        };
+        if (p.act == ACT_SILU) products(ActTag<ACT_SILU>{});
+        else if (p.act == ACT_GELU) products(ActTag<ACT_GELU>{});
+        else if (p.act == ACT_RELU) products(ActTag<ACT_RELU>{});
+        else products(ActTag<ACT_NONE>{});
+    } else {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            by_rows(i, [&](int j) { return acc[i][j]; },
+                    [&](int64_t row, int64_t col, f4 v) {
+                        if (OP == GATED_DW && p.beta != 0.f) {
+                            const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) +
+                                               (row * p.ldc[which] + col) * SIZE;
+                            Quad<BF16> old{};
+                            if (col + 4 <= p.N) {
+                                old.load(c);
+                            } else if constexpr (BF16) {
+                                for (int e = 0; e < 3 && col + e < p.N; ++e)
+                                    old.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(c)[e] << (16 * (e & 1));
+                            } else {
+                                for (int e = 0; e < 3 && col + e < p.N; ++e)
+                                    old.u[e] = reinterpret_cast<const uint32_t*>(c)[e];
+                            }
+                            const f4 o = old.values();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = fmaf(p.beta, o[e], v[e]);
+                        }
+                        put(p.C[which], p.ldc[which], row, col, v);
+                    });
+    }
+}
+
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
+    constexpr int threads = 64 * (BM / WM) * (BN / WN);
+    constexpr int kCols = OP == GATED_FORWARD ? BN / 2 : BN;
+    const int64_t tiles = ((p.M + BM - 1) / BM) * (int64_t)((p.N + kCols - 1) / kCols) *
+                          (OP == GATED_DW ? 2 : 1);
+    const dim3 grid((unsigned)tiles, (unsigned)p.splits);
+    hipLaunchKernelGGL((gated_tile_kernel<OP, BF16, BM, BN, WM, WN, KB, NS>), grid, dim3(threads), 0,
+                       stream, p);
+    return hipGetLastError();
+}
+
+// Sums of the slices in ascending order, and what a launch with one slice does to
+// them: half a wave per 128 columns of a row, four columns per lane.
+template <int OP, bool BF16>
+__global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
+    constexpr int SIZE = BF16 ? 2 : 4;
+    const int64_t nb = (p.N + 127) / 128, units = nb * p.M * (OP == GATED_DW ? 2 : 1);
+    const int64_t slice = (int64_t)p.M * p.N;
+    constexpr int kEach = OP == GATED_DX ? 1 : 2;
+    const int l = threadIdx.x & 31;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units;
+         u += (int64_t)gridDim.x * 8) {
+        const int which = OP == GATED_DW && u >= nb * p.M ? 1 : 0;
+        const int64_t v = u - (which ? nb * p.M : 0);
+        const int64_t row = v / nb, block = v - row * nb, col = block * 128 + 4 * l;
+        const int n = p.N - col < 4 ? (int)(p.N - col) : 4;   // (may be below 1)
+        auto sum = [&](int m) {
+            f4 s = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < p.splits; ++k) {
+                const float* w = p.ws + (k * kEach + which + m) * slice + row * p.N + col;
+                f4 a = {0.f, 0.f, 0.f, 0.f};
+                if (n >= 4) __builtin_memcpy(&a, w, sizeof a);
+                else
+                    for (int e = 0; e < n; ++e) a[e] = w[e];
+                s = s + a;
+            }
+            return s;
+        };
+        auto put = [&](void* base, int64_t ld, const f4& x) {
+            if (n > 0) Quad<BF16>(x).store(static_cast<uint8_t*>(base) + (row * ld + col) * SIZE, n);
+        };
+        const f4 a = sum(0);
+        if constexpr (OP == GATED_FORWARD) {
+            const f4 b = sum(1);
+            f4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = activate(a[e], p.act) * b[e];
+            put(p.C[0], p.ldc[0], h);
+            if (p.save == SAVE_SAME) {
+                put(p.saved[0], p.ld_saved[0], a);
+                put(p.saved[1], p.ld_saved[1], b);
+            } else if (p.save == SAVE_E4M3) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const f4 x = m ? b : a;
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) most = max(most, finite_magnitude(x[e]));
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o, 64));
+                    const float s = scale_of(most);
+                    const Divisor d = divisor_of(s);
+                    const uint32_t c = codes4(x, [&](int) { return d[0]; }, [&](int) { return d; });
+                    if (l == 0) p.scales[m][block * p.ld_scales[m] + row] = s;
+                    uint8_t* q = static_cast<uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
+                    if (n >= 4) *reinterpret_cast<uint32_t*>(q) = c;
+                    else
+                        for (int e = 0; e < n; ++e) q[e] = (uint8_t)(c >> (8 * e));
+                }
+            }
+        } else {
+            f4 v4 = a;
+            if (OP == GATED_DW && p.beta != 0.f) {
+                const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) + (row * p.ldc[which] + col) * SIZE;
+                Quad<BF16> old{};
+                if (n >= 4) old.load(c);
+                else if constexpr (BF16)
+                    for (int e = 0; e < n; ++e)
+                        old.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(c)[e] << (16 * (e & 1));
+                else
+                    for (int e = 0; e < n; ++e) old.u[e] = reinterpret_cast<const uint32_t*>(c)[e];
+                const f4 o = old.values();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v4[e] = fmaf(p.beta, o[e], v4[e]);
+            }
+            put(p.C[which], p.ldc[which], v4);
+        }
+    }
+}
+
+constexpr GatedShape kForwardBf16[] = {
+    {256, 128, 64, 6.0f, 0.50f},
+    {128, 128, 64, 4.0f, 0.33f},
+    {128, 64, 128, 3.0f, 0.40f},
+    {64, 128, 128, 3.0f, 0.40f},
+};
+constexpr GatedShape kForwardF32[] = {
+    {128, 128, 64, 6.0f, 3.6f},
+    {128, 64, 64, 4.0f, 1.8f},
+    {64, 64, 128, 4.0f, 2.0f},
+};
+constexpr GatedShape kBackward[] = {
+    {256, 256, 64, 6.0f, 0.50f},
+    {128, 128, 128, 4.0f, 0.50f},
+    {64, 128, 128, 3.0f, 0.35f},
+};
+
+}  // namespace
+
+int gated_num_shapes(int op, bool bf16) {
+    if (op != GATED_FORWARD) return bf16 ? (int)(sizeof kBackward / sizeof kBackward[0]) : 0;
+    return bf16 ? (int)(sizeof kForwardBf16 / sizeof kForwardBf16[0])
+                : (int)(sizeof kForwardF32 / sizeof kForwardF32[0]);
+}
+GatedShape gated_shape(int op, bool bf16, int shape) {
+    if (op != GATED_FORWARD) return kBackward[shape];
+    return bf16 ? kForwardBf16[shape] : kForwardF32[shape];
+}
+
+hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
+                             hipStream_t stream) {
+    if (op == GATED_FORWARD && bf16) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, true, 128, 128, 64, 64, 128, 4>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 128, 3>(p, stream);
+        }
+    } else if (op == GATED_FORWARD) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 64, 128, 3>(p, stream);
+        }
+    } else if (op == GATED_DX && bf16) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 128, 4>(p, stream);
+            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 4>(p, stream);
+        }
+    } else if (op == GATED_DW && bf16) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 128, 4>(p, stream);
+            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 4>(p, stream);
+        }
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream) {
+    const int64_t units = ((int64_t)p.N + 127) / 128 * p.M * (op == GATED_DW ? 2 : 1);
+    const int64_t wgs = (units + 7) / 8;
+    const dim3 grid((unsigned)(wgs < 16384 ? wgs : 16384));
+    auto kernel = op == GATED_FORWARD ? (bf16 ? gated_finish_kernel<GATED_FORWARD, true>
+                                              : gated_finish_kernel<GATED_FORWARD, false>)
+                : op == GATED_DX      ? gated_finish_kernel<GATED_DX, true>
+                                      : gated_finish_kernel<GATED_DW, true>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+// ---- gradients of the pre-activations -----------------------------------------
+
+namespace {
+
+// act(x) and act'(x). Where sigma or Phi has run out (x far below 0) both are 0, and
+// far above 0 the derivative is 1, also at the infinities.
+template <int ACT>
+__device__ __forceinline__ void activate_both(float x, float& a, float& d) {
+    if constexpr (ACT == ACT_RELU) {
+        a = x < 0.f ? 0.f : x;
+        d = x > 0.f ? 1.f : (x <= 0.f ? 0.f : x);   // (NaN stays)
+    } else if constexpr (ACT == ACT_GELU) {
+        const float e = erf_as7126(x * 0.70710678118654752f), phi = 0.5f * (1.f + e);
+        const float bell = 0.39894228040143268f * __expf(-0.5f * x * x);
+        a = x * phi;
+        d = bell == 0.f ? phi : fmaf(x, bell, phi);
+    } else if constexpr (ACT == ACT_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-x));
+        const float t = __builtin_amdgcn_rcpf(1.f + __expf(x));   // sigma(-x)
+        a = x * s;
+        const float st = s * t;
+        d = st == 0.f ? s : fmaf(x, st, s);
+    } else {
+        a = x;
+        d = 1.f;
+    }
+}
+
+template <bool BF16, bool CODES, int ACT>
+__global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
+    constexpr int SIZE = BF16 ? 2 : 4;
+    const int per_row = (int)(p.ld_d / 4);
+    const int64_t units = (int64_t)p.T * per_row;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units;
+         u += (int64_t)gridDim.x * 256) {
+        const int64_t row = u / per_row;
+        const int col = (int)(u - row * per_row) * 4;
+        const int n = p.I - col < 4 ? p.I - col : 4;
+        auto get = [&](const void* base, int64_t ld) {
+            const uint8_t* at = static_cast<const uint8_t*>(base) + (row * ld + col) * SIZE;
+            Quad<BF16> q{};
+            if (n >= 4) q.load(at);
+            else if constexpr (BF16)
+                for (int e = 0; e < n; ++e)
+                    q.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(at)[e] << (16 * (e & 1));
+            else
+                for (int e = 0; e < n; ++e) q.u[e] = reinterpret_cast<const uint32_t*>(at)[e];
+            return q.values();
+        };
+        f4 pre[2], dg = {0.f, 0.f, 0.f, 0.f}, du = dg, h = dg;
+        if (n > 0) {
+            const f4 dh = get(p.dh, p.lddh);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if constexpr (CODES) {
+                    uint32_t c = 0;
+                    const uint8_t* at = static_cast<const uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
+                    if (n >= 4) c = *reinterpret_cast<const uint32_t*>(at);
+                    else
+                        for (int e = 0; e < n; ++e) c |= (uint32_t)at[e] << (8 * e);
+                    const float s = p.scales[m][(col >> 7) * p.ld_scales[m] + row];
+                    pre[m][0] = s * __builtin_amdgcn_cvt_f32_fp8(c, 0);
+                    pre[m][1] = s * __builtin_amdgcn_cvt_f32_fp8(c, 1);
+                    pre[m][2] = s * __builtin_amdgcn_cvt_f32_fp8(c, 2);
+                    pre[m][3] = s * __builtin_amdgcn_cvt_f32_fp8(c, 3);
+                } else {
+                    pre[m] = get(p.saved[m], p.ld_saved[m]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e >= n) continue;
+                float a, d;
+                activate_both<ACT>(pre[0][e], a, d);
+                du[e] = dh[e] * a;
+                dg[e] = dh[e] * pre[1][e] * d;
+                h[e] = a * pre[1][e];
+            }
+        }
+        // (rows of dg and du end with zeros)
+        const int64_t at = (row * p.ld_d + col) * SIZE;
+        Quad<BF16>(dg).store(static_cast<uint8_t*>(p.dg) + at, 4);
+        Quad<BF16>(du).store(static_cast<uint8_t*>(p.du) + at, 4);
+        if (p.h && n > 0) Quad<BF16>(h).store(static_cast<uint8_t*>(p.h) + (row * p.ldh + col) * SIZE, n);
+    }
+}
+
+template <bool BF16, bool CODES>
+void launch_grad(const GatedGradParams& p, dim3 grid, hipStream_t stream) {
+    auto kernel = p.act == ACT_SILU   ? gated_grad_kernel<BF16, CODES, ACT_SILU>
+                  : p.act == ACT_GELU ? gated_grad_kernel<BF16, CODES, ACT_GELU>
+                  : p.act == ACT_RELU ? gated_grad_kernel<BF16, CODES, ACT_RELU>
+                                      : gated_grad_kernel<BF16, CODES, ACT_NONE>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_gated_grad(bool bf16, const GatedGradParams& p, hipStream_t stream) {
+    const int64_t wgs = (p.T * (p.ld_d / 4) + 255) / 256;
+    const dim3 grid((unsigned)(wgs < 65536 ? wgs : 65536));
+    const bool codes = p.save == SAVE_E4M3;
+    if (bf16 && codes) launch_grad<true, true>(p, grid, stream);
+    else if (bf16) launch_grad<true, false>(p, grid, stream);
+    else if (codes) launch_grad<false, true>(p, grid, stream);
+    else launch_grad<false, false>(p, grid, stream);
+    return hipGetLastError();
+}
+
+}  // namespace fg

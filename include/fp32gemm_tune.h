@@ -167,6 +167,32 @@ fg_status fg_select_fp8(int64_t M, int64_t N, int64_t K, size_t workspace_bytes,
  */
 fg_status fg_set_fp8_tile(int32_t tile);
 
+/*
+ * Tiles of the products of fg_gated and fg_gated_backward (fp32gemm_gated.h).
+ * product (argument 1): 0 the forward product, and with bfloat16 only 1 dx and 2
+ * dgate and dup (binary32 gradients run fg_sgemm); type (2): FG_TYPE_F32 (0) or
+ * FG_TYPE_BF16 (1). fg_gated_num_tiles: how many tiles there are (0 for another
+ * product or type). fg_gated_tile: rows (4) and columns (5) of the result of one
+ * workgroup of tile `tile` (3). fg_select_gated: the tile (7) and the slices of the sum
+ * (8) that a call with T, H and I (3 to 5, positive) and workspace_bytes (6)
+ * for its partial sums runs; tile -1: not a tile kernel (forward products of few
+ * tokens stream the weights); FG_ERR_UNSUPPORTED where the call would be. Host only.
+ */
+int32_t fg_gated_num_tiles(int32_t product, int32_t type);
+fg_status fg_gated_tile(int32_t product, int32_t type, int32_t tile, int32_t* rows,
+                        int32_t* columns);
+fg_status fg_select_gated(int32_t product, int32_t type, int64_t T, int64_t H, int64_t I,
+                          size_t workspace_bytes, int32_t* tile, int32_t* slices);
+
+/*
+ * Tile of every later product of that kind in this process, for tests and
+ * measurements, and its slices: -1 and 0 (the default) the library's choice.
+ * Slices need the workspace for them (else as many as fit). Where G and U are kept in
+ * 8 bits, a tile of less than 128 columns is not used. FG_ERR_INVALID_ARG for
+ * another number.
+ */
+fg_status fg_set_gated_tile(int32_t product, int32_t type, int32_t tile, int32_t slices);
+
 #ifdef __cplusplus
 }
 #endif
