@@ -1,7 +1,8 @@
 """Build libfp32gemm.so (the C-ABI library) for gfx950 with hipcc, in-tree.
 
 Every source compiles to its own object in parallel, then one shared link.
-The matrix-core kernels compile once per line of the instance list
+The few-row kernels of 4-bit weights and the gated block (few_rows.hip) compile
+once per kind of operands; the matrix-core kernels compile once per line of the instance list
 (csrc/fg_mfma_instances.inc) and operand layout: sgemm_mfma_inst.hip with
 that line's shape, one translation unit per kernel.
 Flags:
@@ -35,7 +36,9 @@ INSTANCES = os.path.join(CSRC, "fg_mfma_instances.inc")
 SOURCES = ["fg_api.cpp", "fg_mfma_dispatch.cpp", "sgemm_valu.hip", "sgemm_skinny.hip",
            "fg_elementwise.hip", "fg_probe.hip", "fg_noalloc.hip",
            "fg_lowp_api.cpp", "quant_fp8.hip", "gemm_fp8.hip", "moe.hip",
-           "fg_gated_api.cpp", "gated_tile.hip", "few_rows.hip"]
+           "fg_gated_api.cpp", "gated_tile.hip"]
+# few_rows.hip compiles once per (4-bit weights, bfloat16 x, matrices)
+FEW_ROWS = [(0, 0, 2), (0, 1, 2), (1, 0, 1), (1, 0, 2), (1, 1, 1), (1, 1, 2)]
 ENTRY_FIELDS = ("id", "bm", "bn", "waves_m", "waves_n", "bk", "mr", "stages", "dmab", "occ",
                 "wps", "fallback")
 
@@ -138,6 +141,11 @@ def build(verbose: bool = False, instances: str = INSTANCES, tuned: str | None =
     for s in SOURCES:
         work.append((os.path.join(CSRC, s),
                      os.path.join(build_dir, os.path.splitext(s)[0] + ".o"), defs))
+    for int4, bf16, matrices in FEW_ROWS:
+        work.append((os.path.join(CSRC, "few_rows.hip"),
+                     os.path.join(build_dir, f"few_rows_{int4}{bf16}{matrices}.o"),
+                     defs + [f"-DFG_ROWS_INT4={int4}", f"-DFG_ROWS_BF16={bf16}",
+                             f"-DFG_ROWS_MATRICES={matrices}"]))
     entries = read_instances(instances)
     for e in entries:
         want = set(map(tuple, (layouts or {}).get(e["id"], [(0, 0), (0, 1), (1, 0), (1, 1)])))

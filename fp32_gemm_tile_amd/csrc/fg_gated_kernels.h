@@ -39,7 +39,22 @@ struct RowsParams {
     int64_t ld_save[2];
 };
 constexpr int kRowsMaxTokens = 64;
-hipError_t launch_rows(const RowsParams& p, hipStream_t stream);
+// launch_rows_<4-bit><bfloat16 x><matrices>, each a translation unit of few_rows.hip
+hipError_t launch_rows_002(const RowsParams& p, hipStream_t stream);
+hipError_t launch_rows_012(const RowsParams& p, hipStream_t stream);
+hipError_t launch_rows_101(const RowsParams& p, hipStream_t stream);
+hipError_t launch_rows_102(const RowsParams& p, hipStream_t stream);
+hipError_t launch_rows_111(const RowsParams& p, hipStream_t stream);
+hipError_t launch_rows_112(const RowsParams& p, hipStream_t stream);
+inline hipError_t launch_rows(const RowsParams& p, hipStream_t stream) {
+    if (p.T < 1 || p.T > kRowsMaxTokens) return hipErrorInvalidValue;
+    if (!p.group) {
+        if (p.matrices != 2) return hipErrorInvalidValue;
+        return p.x_bf16 ? launch_rows_012(p, stream) : launch_rows_002(p, stream);
+    }
+    if (p.matrices == 1) return p.x_bf16 ? launch_rows_111(p, stream) : launch_rows_101(p, stream);
+    return p.x_bf16 ? launch_rows_112(p, stream) : launch_rows_102(p, stream);
+}
 
 
 // ---- many rows: tile kernels ---------------------------------------------------
