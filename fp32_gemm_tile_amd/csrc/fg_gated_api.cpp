@@ -498,7 +498,9 @@ fg_status check_int4(const fg_int4* w, int64_t N, int64_t K, int64_t group, int6
                     (long long)N);
     if (w->z && w->ldz < N)
         return fail(FG_ERR_INVALID_ARG, arg, "zero points of %s: ldz < %lld", name, (long long)N);
-    (void)group;
+    const int64_t groups = cdiv(K, group), most = 1ll << 31;
+    if (groups > 0 && (w->lds >= most / scale_size / groups || (w->z && w->ldz >= most / groups)))
+        return fail(FG_ERR_UNSUPPORTED, arg, "scales or zero points of %s of 2 GiB or more", name);
     return FG_OK;
 }
 
