@@ -30,22 +30,39 @@ namespace {
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-template <bool BF16>
-__device__ __forceinline__ f4 mfma(i4v a, i4v b, f4 c) {
+// Sums of an MR x MR block as a lane holds them: quads of consecutive columns of C, MR
+// / 4 apart times the lane groups.
+template <int MR>
+struct Block {
+    typedef float vec __attribute__((ext_vector_type(MR * MR / 64)));
+    vec v;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int e = 0; e < MR * MR / 64; ++e) v[e] = 0.f;
+    }
+    __device__ __forceinline__ f4 quad(int q) const {
+        return f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    }
+};
+
+template <bool BF16, int MR>
+__device__ __forceinline__ void mfma(i4v a, i4v b, Block<MR>& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (BF16) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
-                                                       __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    if constexpr (BF16 && MR == 32) {
+        c.v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a),
+                                                      __builtin_bit_cast(bf8, b), c.v, 0, 0, 0);
+    } else if constexpr (BF16) {
+        c.v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
+                                                      __builtin_bit_cast(bf8, b), c.v, 0, 0, 0);
     } else {
         const f4 fa = __builtin_bit_cast(f4, a), fb = __builtin_bit_cast(f4, b);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
+            c.v = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c.v, 0, 0, 0);
     }
 #else
-    (void)a, (void)b;
+    (void)a, (void)b, (void)c;
 #endif
-    return c;
 }
 
 // 4 k of 16 columns per 16 lanes: lane l gives the address of row l / 4, columns
@@ -79,7 +96,7 @@ __device__ __forceinline__ i4v keep(i4v v, int left) {
 
 // A tile of R rows (of m or n) and KB bytes of k, and how it gets to LDS and back.
 // ALONG_K: stored with k along its rows.
-template <bool BF16, bool ALONG_K, int R, int KB, int NW>
+template <bool BF16, bool ALONG_K, int R, int KB, int NW, int MR>
 struct Tile {
     static constexpr int kSize = BF16 ? 2 : 4;
     static constexpr int kBytes = R * KB;
@@ -92,10 +109,14 @@ struct Tile {
     static_assert(ALONG_K || (BF16 && R >= 64), "only 16-bit elements are transposed");
 
     // Exchange of the 16-byte chunks of LDS row r: chunk c is at position c ^ turn(r).
-    // ALONG_K: the 16 rows read together cover the 256 bytes of all banks once.
+    // ALONG_K: a 128-bit read of 16 rows (the 16 lanes that are served together are not
+    // neighbours) covers all banks evenly; found by trying, 4 cycles a read, and 8 with
+    // (r >> 2) & 3 for 64-byte rows.
     // Else the eight rows that 32 lanes read together do.
     static __device__ __forceinline__ int turn(int r) {
-        if constexpr (ALONG_K) return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+        if constexpr (ALONG_K && KB == 128) return (r >> 1) & 7;
+        else if constexpr (ALONG_K) return MR == 32 ? ((r >> 3) & 1) | ((r >> 1) & 2) : (r >> 2) & 2;
+        else if constexpr (MR == 32) return 4 * (r & 3);
         else if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
         else return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
     }
@@ -106,18 +127,19 @@ struct Tile {
         const int c = (lane % kLanesPerRow) ^ turn(r);
         return (uint32_t)(r * ld * kSize) + (uint32_t)(c * 16);
     }
-    // The chunk of 16 k-bytes of row r0 + n16 (r0 a multiple of 16) that lane (n16,
-    // g) gives to the instruction, in sub-step `sub` of 64 bytes of k: k = 8 g .. 8 g + 7
-    // (4 g .. 4 g + 3 for binary32) either way.
+    // What lane (n, g) = (lane % MR, lane / MR) gives to the instruction in sub-step
+    // `sub`: the 16 bytes of k from 16 (64 / MR sub + g) of row r0 + n (r0 a multiple of
+    // MR), the same k from a tile of either kind.
     static __device__ __forceinline__ i4v read(const uint8_t* tile, int r0, int sub, int lane) {
-        const int n16 = lane & 15, g = lane >> 4;
+        const int n = lane % MR, g = lane / MR;
         if constexpr (ALONG_K) {
-            return *reinterpret_cast<const i4v*>(tile + (r0 + n16) * KB +
-                                                 (((sub * 4 + g) ^ turn(n16)) << 4));
+            return *reinterpret_cast<const i4v*>(tile + (r0 + n) * KB +
+                                                 (((sub * (64 / MR) + g) ^ turn(n)) << 4));
         } else {
-            const int k = 32 * sub + 8 * g + (n16 >> 2);
-            const uint8_t* at = tile + k * kRowBytes + (n16 & 1) * 8 +
-                                (((r0 / 8 + ((n16 >> 1) & 1)) ^ turn(8 * g + (n16 >> 2))) << 4);
+            const int i = lane & 15, k = 8 * g + (i >> 2);
+            const int c = r0 / 8 + (MR == 32 ? (lane >> 3) & 2 : 0) + ((i >> 1) & 1);
+            const uint8_t* at = tile + (sub * (512 / MR) + k) * kRowBytes + (i & 1) * 8 +
+                                ((c ^ turn(k)) << 4);
             const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * kRowBytes);
             return i4v{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
         }
@@ -151,32 +173,40 @@ struct Quad {
     __device__ __forceinline__ void store(uint8_t* c, int n) const {
         if (n >= 4) {
             __builtin_memcpy(c, u, sizeof u);
-        } else if constexpr (BF16) {
-            for (int e = 0; e < n; ++e)
-                reinterpret_cast<uint16_t*>(c)[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
-        } else {
-            for (int e = 0; e < n; ++e) reinterpret_cast<uint32_t*>(c)[e] = u[e];
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (e >= n) continue;
+            if constexpr (BF16) reinterpret_cast<uint16_t*>(c)[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+            else reinterpret_cast<uint32_t*>(c)[e] = u[e];
         }
     }
 };
 
-template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+// PIPE: the operands of a step are in registers before it begins, those of the next
+// are read during it, and so a stage is free for its next load a step earlier.
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS, bool PIPE, int MR>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(GatedTileParams p) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
-    constexpr int TI = WM / 16, TJ = WN / 16;
+    constexpr int TI = WM / MR, TJ = WN / MR;
     constexpr int SIZE = BF16 ? 2 : 4;
     constexpr bool kDual = OP == GATED_FORWARD;
     // (FORWARD: BN rows of B are BN / 2 of gate and BN / 2 of up)
     constexpr int kCols = kDual ? BN / 2 : BN;       // columns of C per workgroup
     constexpr int kWaveCols = kDual ? WN / 2 : WN;
     constexpr int PJ = kDual ? TJ / 2 : TJ;          // column tiles of one matrix
-    using TA = Tile<BF16, OP != GATED_DW, BM, KB, NW>;
-    using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW>;
+    using TA = Tile<BF16, OP != GATED_DW, BM, KB, NW, MR>;
+    using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW, MR>;
     constexpr int kStage = TA::kBytes + TB::kBytes;
     constexpr int K1 = TA::kSteps;                   // k of a step
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage];
+    // (the results' way out: MR rows of every wave, and the rows' largest magnitudes)
+    constexpr int kPitch = kWaveCols + 4;
+    constexpr int kOut = NW * MR * kPitch * 4 + (kDual ? 2 * NWN * BM * 4 : 0);
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kOut ? NS * kStage : kOut];
 
-    const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, n16 = lane % MR, g = lane / MR;
+    constexpr int kSubs = KB * MR / 1024;   // instructions along k in a step
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = (wave % NWM) * WM, wj = (wave / NWM) * kWaveCols;
     const int tiles_m = (p.M + BM - 1) / BM;
@@ -195,97 +225,127 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
 
     // 16-byte pieces that exist in a row of n elements, in bytes
     auto whole = [](int64_t n) { return (n * SIZE + 15) & ~15ll; };
-    uint32_t src_a[TA::kParts], src_b[TB::kParts];
+    auto at = [](const void* base, int64_t element) {
+        return static_cast<const uint8_t*>(base) + element * SIZE;
+    };
+    const uint32_t lds0 = lds_address(lds);
+
+    // Where the next step's loads come from. Steps are fetched one after the other, so
+    // little is left to do for each: an operand stored along k moves its lanes' offsets
+    // (rows past the matrix and the row's end stay past the buffer's), another its base,
+    // by the rows of a step, of which the last step has fewer.
+    const int first_m = OP == GATED_DX && s0 >= half ? 1 : 0;
+    const int64_t first_k = (int64_t)(s0 - first_m * half) * K1;
+    const int k_last = p.K % K1 ? p.K % K1 : K1;
+    auto bytes_of = [&](int64_t n, int64_t ld, int64_t row) { return (uint32_t)((n - 1) * ld * SIZE + row); };
+    // A
+    constexpr bool kAlongA = OP != GATED_DW;
+    const int64_t row_a = whole(kAlongA ? p.K : p.M) - (kAlongA ? 0 : m0 * SIZE);
+    const uint8_t* base_a = kAlongA ? at(p.A[first_m], m0 * p.lda) : at(p.A[which], first_k * p.lda + m0);
+    const uint32_t full_a = bytes_of(kAlongA ? rows : K1, p.lda, row_a);
+    const uint32_t last_a = kAlongA ? full_a : bytes_of(k_last, p.lda, row_a);
+    uint32_t cur_a[TA::kParts];
 #pragma unroll
-    for (int q = 0; q < TA::kParts; ++q) src_a[q] = TA::source(wave + NW * q, lane, p.lda);
-    // (FORWARD: the second half of B's rows are up's first ones)
+    for (int q = 0; q < TA::kParts; ++q)
+        cur_a[q] = TA::source(wave + NW * q, lane, p.lda) + (kAlongA ? (uint32_t)first_k * SIZE : 0u);
+    // B (FORWARD: the second half of its rows are up's first ones; DX: up's steps follow
+    // gate's, with another leading dimension)
     constexpr int kHalfLoads = TB::kBytes / 1024 / 2;
+    static_assert(!kDual || kHalfLoads % NW == 0, "a load of every wave is of one matrix");
+    constexpr int kGateParts = kDual ? kHalfLoads / NW : TB::kParts;
+    const int64_t row_b = whole(kDual ? p.K : p.N) - (kDual ? 0 : n0 * SIZE);
+    const uint8_t* base_b[2];
+    uint32_t full_b[2], last_b[2], cur_b[TB::kParts];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int u = OP == GATED_DW ? 0 : m;
+        base_b[m] = kDual ? at(p.B[u], n0 * p.ldb[u])
+                          : at(p.B[u], (OP == GATED_DX && m != first_m ? 0 : first_k) * p.ldb[u] + n0);
+        full_b[m] = bytes_of(kDual ? cols : K1, p.ldb[u], row_b);
+        last_b[m] = kDual ? full_b[m] : bytes_of(k_last, p.ldb[u], row_b);
+    }
+    if (OP == GATED_DX && first_m) base_b[0] = base_b[1];   // (the one that is read)
 #pragma unroll
     for (int q = 0; q < TB::kParts; ++q) {
         const int i = wave + NW * q;
         if constexpr (kDual) {
-            const int u = i >= kHalfLoads;
-            src_b[q] = TB::source(i - u * kHalfLoads, lane, p.ldb[u]);
+            const int u = q >= kGateParts;
+            cur_b[q] = TB::source(i - u * kHalfLoads, lane, p.ldb[u]) + (uint32_t)first_k * SIZE;
         } else {
-            src_b[q] = TB::source(i, lane, OP == GATED_DX ? p.ldb[0] : p.ldb[0]);
+            cur_b[q] = TB::source(i, lane, first_m ? +p.ldb[1] : +p.ldb[0]);
         }
     }
-    auto at = [](const void* base, int64_t element) {
-        return static_cast<const uint8_t*>(base) + element * SIZE;
-    };
-    auto bounded = [](int64_t bytes) {
-        return bytes < 0 ? (int64_t)0 : (bytes > 0xFFFFFFFFll ? 0xFFFFFFFFll : bytes);
-    };
-    const uint32_t lds0 = lds_address(lds);
-
-    // Step s into a stage; past the last one buffers without a byte, which read as zero.
+    // (A unary plus makes a value of an operand of ?:, which else chooses between two
+    // places, and they then live in memory.)
+    // Step s, the one after the last fetched, into a stage; past the last one buffers
+    // without a byte, which read as zero.
     auto fetch = [&](int s, int stage) __attribute__((always_inline)) {
         const uint32_t to = lds0 + stage * kStage;
         const bool more = s < s1;
-        const int m = OP == GATED_DX && s >= half ? 1 : 0;
-        const int64_t k = (int64_t)(s - (m ? half : 0)) * K1;
-        i4v ra, rb[2];
-        if constexpr (OP == GATED_DW) {
-            ra = buffer_words(at(p.A[which], k * p.lda + m0),
-                              bounded((p.K - k - 1) * p.lda * SIZE + whole(p.M) - m0 * SIZE));
-        } else {
-            const int64_t row = whole(p.K) - k * SIZE;
-            ra = buffer_words(at(p.A[m], m0 * p.lda + k), bounded((rows - 1) * p.lda * SIZE + row));
-        }
-        if constexpr (kDual) {
+        const bool up = OP == GATED_DX && s >= half;
+        const bool last = s == half - 1 || (OP == GATED_DX && s == 2 * half - 1);
+        if constexpr (OP == GATED_DX) {
+            if (s == half && s != s0) {   // from gate to up
+                base_a = at(p.A[1], m0 * p.lda);
+                base_b[0] = base_b[1];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                rb[u] = buffer_words(at(p.B[u], n0 * p.ldb[u] + k),
-                                     bounded((cols - 1) * p.ldb[u] * SIZE + whole(p.K) - k * SIZE));
-        } else {
-            rb[0] = buffer_words(at(p.B[m], k * p.ldb[m] + n0),
-                                 bounded((p.K - k - 1) * p.ldb[m] * SIZE + whole(p.N) - n0 * SIZE));
-        }
-        if (!more) ra[2] = rb[0][2] = 0;
-        if (kDual && !more) rb[1][2] = 0;
+                for (int q = 0; q < TA::kParts; ++q) cur_a[q] = TA::source(wave + NW * q, lane, p.lda);
 #pragma unroll
-        for (int q = 0; q < TA::kParts; ++q) dma16(ra, to + (wave + NW * q) * 1024, src_a[q]);
+                for (int q = 0; q < TB::kParts; ++q) cur_b[q] = TB::source(wave + NW * q, lane, p.ldb[1]);
+            }
+        }
+        const i4v ra = buffer_words(base_a, more ? (last ? +last_a : +full_a) : 0u);
+#pragma unroll
+        for (int q = 0; q < TA::kParts; ++q) {
+            dma16(ra, to + (wave + NW * q) * 1024, cur_a[q]);
+            if constexpr (kAlongA) cur_a[q] += KB;
+        }
+        const uint32_t size0 = up ? (last ? +last_b[1] : +full_b[1]) : (last ? +last_b[0] : +full_b[0]);
+        const i4v rb0 = buffer_words(base_b[0], more ? size0 : 0u);
+        const i4v rb1 = buffer_words(base_b[1], more ? full_b[1] : 0u);
 #pragma unroll
         for (int q = 0; q < TB::kParts; ++q) {
-            const int i = wave + NW * q;
-            dma16(kDual && i >= kHalfLoads ? rb[1] : rb[0], to + TA::kBytes + i * 1024, src_b[q]);
+            dma16(kDual && q >= kGateParts ? +rb1 : +rb0, to + TA::kBytes + (wave + NW * q) * 1024, cur_b[q]);
+            if constexpr (kDual) cur_b[q] += KB;
         }
+        if constexpr (!kAlongA) base_a += K1 * p.lda * SIZE;
+        if constexpr (!kDual) base_b[0] += K1 * (up ? +p.ldb[1] : +p.ldb[0]) * SIZE;
     };
 
-    f4 acc[TI][TJ];
+    Block<MR> acc[TI][TJ];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < TJ; ++j) acc[i][j].clear();
 
     // row of B's tile that column tile j of the wave starts at
     auto b_row = [&](int j) {
-        return kDual ? (j < PJ ? 0 : BN / 2) + wj + 16 * (j % PJ) : wj + 16 * j;
+        return kDual ? (j < PJ ? 0 : BN / 2) + wj + MR * (j % PJ) : wj + MR * j;
     };
     auto use = [&](int stage, int left, auto tail) __attribute__((always_inline)) {
         const uint8_t* const ta = lds + stage * kStage;
         const uint8_t* const tb = ta + TA::kBytes;
 #pragma unroll
-        for (int sub = 0; sub < KB / 64; ++sub) {
+        for (int sub = 0; sub < kSubs; ++sub) {
             i4v a[TI], b[TJ];
             auto kept = [&](i4v v) {
                 constexpr int kPer = 16 / SIZE;
-                if constexpr (decltype(tail)::value) return keep<BF16>(v, left - (sub * 4 + g) * kPer);
+                if constexpr (decltype(tail)::value) return keep<BF16>(v, left - (sub * (64 / MR) + g) * kPer);
                 else return v;
             };
 #pragma unroll
             for (int j = 0; j < TJ; ++j) b[j] = kept(TB::read(tb, b_row(j), sub, lane));
 #pragma unroll
-            for (int i = 0; i < TI; ++i) a[i] = kept(TA::read(ta, wi + 16 * i, sub, lane));
+            for (int i = 0; i < TI; ++i) a[i] = kept(TA::read(ta, wi + MR * i, sub, lane));
 #pragma unroll
             for (int i = 0; i < TI; ++i)
 #pragma unroll
-                for (int j = 0; j < TJ; ++j) acc[i][j] = mfma<BF16>(b[j], a[i], acc[i][j]);
+                for (int j = 0; j < TJ; ++j) mfma<BF16, MR>(b[j], a[i], acc[i][j]);
         }
     };
 
     constexpr int kLoads = TA::kParts + TB::kParts;
-    static_assert((NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
+    static_assert((PIPE ? NS - 1 : NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
     auto meet = [] {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
                      : "memory");
@@ -294,47 +354,122 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
     // which those past the last are zeros)
     const bool partial = kDual && s1 == p.steps && p.K % K1 != 0;
     const int whole_end = partial ? s1 - 1 : s1;
-    int stage = 0;
+    if constexpr (PIPE) {
+        struct Operands {
+            i4v a[kSubs][TI], b[kSubs][TJ];
+        };
+        auto read = [&](int stage, Operands& o) __attribute__((always_inline)) {
+            const uint8_t* const ta = lds + stage * kStage;
 #pragma unroll
-    for (int d = 0; d < NS - 1; ++d) fetch(s0 + d, d);
-    for (int s = s0; s < whole_end; ++s) {
-        meet();
-        fetch(s + NS - 1, stage == 0 ? NS - 1 : stage - 1);
-        use(stage, 0, Flag<false>{});
-        stage = stage + 1 == NS ? 0 : stage + 1;
-    }
-    if constexpr (kDual) {
-        if (partial) {
+            for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) o.b[u][j] = TB::read(ta + TA::kBytes, b_row(j), u, lane);
+#pragma unroll
+                for (int i = 0; i < TI; ++i) o.a[u][i] = TA::read(ta, wi + MR * i, u, lane);
+            }
+        };
+        auto row = [&](const Operands& o, int u, int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) mfma<BF16, MR>(o.b[u][j], o.a[u][i], acc[i][j]);
+        };
+        // Step s, its operands in `now`: stage s + 1 is there for everyone and everyone
+        // has read stage s, which is loaded again. The matrix instructions begin at
+        // once, the loads go out after the first row of them, and the reads between
+        // the others.
+        int stage = 0;
+        auto step = [&](int s, const Operands& now, Operands& next) __attribute__((always_inline)) {
             meet();
-            fetch(s1 + NS - 2, stage == 0 ? NS - 1 : stage - 1);
-            use(stage, p.K - (s1 - 1) * K1, Flag<true>{});
+            __builtin_amdgcn_s_setprio(1);
+            row(now, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(s + NS, stage);
+            stage = stage + 1 == NS ? 0 : stage + 1;
+            __builtin_amdgcn_sched_barrier(0);
+            read(stage, next);
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                for (int i = u == 0 ? 1 : 0; i < TI; ++i) row(now, u, i);
+            constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? 2 : 1) + TJ * (kDual ? 1 : 2));
+            constexpr int kLeft = kSubs * TI * TJ - TJ;
+#pragma unroll
+            for (int k = 0; k < kReads; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+                __builtin_amdgcn_sched_group_barrier(0x008, kLeft / kReads, 0);          // matrix
+            }
+        };
+        Operands o[2];
+#pragma unroll
+        for (int d = 0; d < NS; ++d) fetch(s0 + d, d);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 1) * kLoads) : "memory");
+        read(0, o[0]);
+        int s = s0;
+        for (; s + 2 <= whole_end; s += 2) {
+            step(s, o[0], o[1]);
+            step(s + 1, o[1], o[0]);
+        }
+        if (s < whole_end) {
+            step(s, o[0], o[1]);
+            if constexpr (kDual) o[0] = o[1];
+        }
+        if constexpr (kDual) {
+            if (partial) {
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u) {
+                    const int left = p.K - (s1 - 1) * K1 - (u * (64 / MR) + g) * (16 / SIZE);
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) o[0].b[u][j] = keep<BF16>(o[0].b[u][j], left);
+#pragma unroll
+                    for (int i = 0; i < TI; ++i) o[0].a[u][i] = keep<BF16>(o[0].a[u][i], left);
+#pragma unroll
+                    for (int i = 0; i < TI; ++i) row(o[0], u, i);
+                }
+            }
+        }
+    } else {
+        int stage = 0;
+#pragma unroll
+        for (int d = 0; d < NS - 1; ++d) fetch(s0 + d, d);
+        for (int s = s0; s < whole_end; ++s) {
+            meet();
+            fetch(s + NS - 1, stage == 0 ? NS - 1 : stage - 1);
+            use(stage, 0, Flag<false>{});
+            stage = stage + 1 == NS ? 0 : stage + 1;
+        }
+        if constexpr (kDual) {
+            if (partial) {
+                meet();
+                fetch(s1 + NS - 2, stage == 0 ? NS - 1 : stage - 1);
+                use(stage, p.K - (s1 - 1) * K1, Flag<true>{});
+            }
         }
     }
     auto all_done = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     all_done();
 
-    // The wave's 16 rows at a time through its own part of the LDS, so that a store
+    // The wave's MR rows at a time through its own part of the LDS, so that a store
     // covers consecutive elements of a row.
-    constexpr int kPitch = kWaveCols + 4, kLanes = kWaveCols / 4, kRows = 64 / kLanes;
-    static_assert(NW * 16 * kPitch * 4 + (kDual ? 2 * NWN * BM * 4 : 0) <= NS * kStage,
-                  "the stages hold the waves' rows");
-    float* const own = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+    constexpr int kLanes = kWaveCols / 4, kRows = 64 / kLanes;
+    float* const own = reinterpret_cast<float*>(lds) + wave * MR * kPitch;
     const int er = lane / kLanes, ec = (lane % kLanes) * 4;
     auto settle = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-    // of(j): column tile j of row tile i; to(row, column, value) for every quad
+    constexpr int kQuads = MR * MR / 256, kApart = 4 * 64 / MR;   // quads of a block, columns between them
+    // of(j, q): quad q of column tile j of row tile i; to(row, column, value) for each
     auto by_rows = [&](int i, auto of, auto to) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < PJ; ++j)
-            *reinterpret_cast<f4*>(own + n16 * kPitch + 16 * j + 4 * g) = of(j);
-        settle();
-        f4 v[16 / kRows];
 #pragma unroll
-        for (int r = 0; r < 16 / kRows; ++r)
+            for (int q = 0; q < kQuads; ++q)
+                *reinterpret_cast<f4*>(own + n16 * kPitch + MR * j + kApart * q + 4 * g) = of(j, q);
+        settle();
+        f4 v[MR / kRows];
+#pragma unroll
+        for (int r = 0; r < MR / kRows; ++r)
             v[r] = *reinterpret_cast<const f4*>(own + (r * kRows + er) * kPitch + ec);
         settle();
 #pragma unroll
-        for (int r = 0; r < 16 / kRows; ++r) {
-            const int64_t row = m0 + wi + 16 * i + r * kRows + er, col = n0 + wj + ec;
+        for (int r = 0; r < MR / kRows; ++r) {
+            const int64_t row = m0 + wi + MR * i + r * kRows + er, col = n0 + wj + ec;
             if (row < p.M && col < p.N) to(row, col, v[r]);
         }
     };
@@ -349,7 +484,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
         for (int i = 0; i < TI; ++i)
 #pragma unroll
             for (int m = 0; m < (kDual ? 2 : 1); ++m)
-                by_rows(i, [&](int j) { return acc[i][m * PJ + j]; },
+                by_rows(i, [&](int j, int q) { return acc[i][m * PJ + j].quad(q); },
                         [&](int64_t row, int64_t col, const f4& v) {
                             const int n = p.N - col < 4 ? (int)(p.N - col) : 4;
                             Quad<false>(v).store(
@@ -364,7 +499,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
             // of the wave's, then of its neighbours' along the row.
             static_assert(kCols % 128 == 0 || kCols < 128, "whole blocks, or no codes");
             if constexpr (kCols % 128 == 0) {
-                uint32_t* const most = reinterpret_cast<uint32_t*>(lds + NW * 16 * kPitch * 4);
+                uint32_t* const most = reinterpret_cast<uint32_t*>(lds + NW * MR * kPitch * 4);
                 constexpr int kPerBlock = 128 / kWaveCols;   // waves
                 const int wn = wave / NWM;
                 uint32_t mine[2][TI];
@@ -376,12 +511,12 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
 #pragma unroll
                         for (int j = 0; j < PJ; ++j)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v = max(v, finite_magnitude(acc[i][m * PJ + j][e]));
-                        v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-                        v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+                            for (int e = 0; e < MR * MR / 64; ++e)
+                                v = max(v, finite_magnitude(acc[i][m * PJ + j].v[e]));
+#pragma unroll
+                        for (int o = MR; o < 64; o *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
                         mine[m][i] = v;
-                        if (g == 0) most[(m * NWN + wn) * BM + wi + 16 * i + n16] = v;
+                        if (g == 0) most[(m * NWN + wn) * BM + wi + MR * i + n16] = v;
                     }
                 __syncthreads();
 #pragma unroll
@@ -392,28 +527,30 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
                         const int w0 = wn / kPerBlock * kPerBlock;
 #pragma unroll
                         for (int w = 0; w < kPerBlock; ++w)
-                            v = max(v, most[(m * NWN + w0 + w) * BM + wi + 16 * i + n16]);
+                            v = max(v, most[(m * NWN + w0 + w) * BM + wi + MR * i + n16]);
                         const float s = scale_of(v);
                         const Divisor d = divisor_of(s);
-                        const int64_t row = m0 + wi + 16 * i + n16, col = n0 + wj;
+                        const int64_t row = m0 + wi + MR * i + n16, col = n0 + wj;
                         if (g == 0 && wn == w0 && row < p.M)
                             p.scales[m][col / 128 * p.ld_scales[m] + row] = s;
                         // codes: a dword per lane and column tile, rows of kWaveCols bytes
                         uint8_t* const bytes = reinterpret_cast<uint8_t*>(own);
 #pragma unroll
                         for (int j = 0; j < PJ; ++j)
-                            *reinterpret_cast<uint32_t*>(bytes + n16 * (kWaveCols + 4) + 16 * j + 4 * g) =
-                                codes4(acc[i][m * PJ + j], [&](int) { return d[0]; }, [&](int) { return d; });
-                        settle();
-                        uint32_t c[16 / kRows];
 #pragma unroll
-                        for (int r = 0; r < 16 / kRows; ++r)
+                            for (int q = 0; q < kQuads; ++q)
+                                *reinterpret_cast<uint32_t*>(bytes + n16 * (kWaveCols + 4) + MR * j + kApart * q + 4 * g) =
+                                    codes4(acc[i][m * PJ + j].quad(q), [&](int) { return d[0]; }, [&](int) { return d; });
+                        settle();
+                        uint32_t c[MR / kRows];
+#pragma unroll
+                        for (int r = 0; r < MR / kRows; ++r)
                             c[r] = *reinterpret_cast<const uint32_t*>(
                                 bytes + (r * kRows + er) * (kWaveCols + 4) + ec);
                         settle();
 #pragma unroll
-                        for (int r = 0; r < 16 / kRows; ++r) {
-                            const int64_t cr = m0 + wi + 16 * i + r * kRows + er, cc = n0 + wj + ec;
+                        for (int r = 0; r < MR / kRows; ++r) {
+                            const int64_t cr = m0 + wi + MR * i + r * kRows + er, cc = n0 + wj + ec;
                             if (cr >= p.M || cc >= p.N) continue;
                             uint8_t* q = static_cast<uint8_t*>(p.saved[m]) + cr * p.ld_saved[m] + cc;
                             if (cc + 4 <= p.N) *reinterpret_cast<uint32_t*>(q) = c[r];
@@ -427,7 +564,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
             for (int i = 0; i < TI; ++i)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
-                    by_rows(i, [&](int j) { return acc[i][m * PJ + j]; },
+                    by_rows(i, [&](int j, int q) { return acc[i][m * PJ + j].quad(q); },
                             [&](int64_t row, int64_t col, const f4& v) {
                                 put(p.saved[m], p.ld_saved[m], row, col, v);
                             });
@@ -436,11 +573,11 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
 #pragma unroll
             for (int i = 0; i < TI; ++i)
                 by_rows(i,
-                        [&](int j) {
+                        [&](int j, int q) {
+                            const f4 a = acc[i][j].quad(q), u = acc[i][PJ + j % PJ].quad(q);
                             f4 h;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] = activate_t<decltype(act)::value>(acc[i][j][e]) * acc[i][PJ + j % PJ][e];
+                            for (int e = 0; e < 4; ++e) h[e] = activate_t<decltype(act)::value>(a[e]) * u[e];
                             return h;
                         },
                         [&](int64_t row, int64_t col, const f4& v) { put(p.C[0], p.ldc[0], row, col, v); });
@@ -452,7 +589,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
     } else {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-            by_rows(i, [&](int j) { return acc[i][j]; },
+            by_rows(i, [&](int j, int q) { return acc[i][j].quad(q); },
                     [&](int64_t row, int64_t col, f4 v) {
                         if (OP == GATED_DW && p.beta != 0.f) {
                             const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) +
@@ -476,14 +613,14 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
     }
 }
 
-template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS, bool PIPE = false, int MR = 16>
 hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN);
     constexpr int kCols = OP == GATED_FORWARD ? BN / 2 : BN;
     const int64_t tiles = ((p.M + BM - 1) / BM) * (int64_t)((p.N + kCols - 1) / kCols) *
                           (OP == GATED_DW ? 2 : 1);
     const dim3 grid((unsigned)tiles, (unsigned)p.splits);
-    hipLaunchKernelGGL((gated_tile_kernel<OP, BF16, BM, BN, WM, WN, KB, NS>), grid, dim3(threads), 0,
+    hipLaunchKernelGGL((gated_tile_kernel<OP, BF16, BM, BN, WM, WN, KB, NS, PIPE, MR>), grid, dim3(threads), 0,
                        stream, p);
     return hipGetLastError();
 }
@@ -600,7 +737,7 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
                              hipStream_t stream) {
     if (op == GATED_FORWARD && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 64, 64, 4>(p, stream);
             case 2: return launch_tile<GATED_FORWARD, true, 128, 128, 64, 64, 128, 4>(p, stream);
             case 3: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 128, 3>(p, stream);
@@ -613,13 +750,13 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
         }
     } else if (op == GATED_DX && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 128, 4>(p, stream);
             case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 4>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 128, 4>(p, stream);
             case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 4>(p, stream);
         }

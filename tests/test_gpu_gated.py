@@ -245,6 +245,27 @@ def test_backward_every_tile(product):
 
 
 @pytest.mark.parametrize("ty", ["f32", "bf16"])
+def test_gate_and_up_of_different_strides(ty):
+    import torch
+    for T, H, I in ((7, 70, 45), (150, 330, 300)):
+        c = Case(T, H, I, ty, seed=6)
+        wide = torch.full((I, (H + 47) // 8 * 8), float("nan"), dtype=c.up.dtype, device="cuda")
+        at = wide[:, 8:8 + H]
+        at.copy_(c.up)
+        c.up = at
+        code = int(ty == "bf16")
+        try:
+            for tile, slices in ((-1, 0), (0, 2), (1, 1), (2, 4)):
+                for product in (0, 1) if code else (0,):
+                    fg.fg_set_gated_tile(product, code, tile, slices)
+                c.forward("same")
+                c.backward("same", parts=("dx",))
+        finally:
+            for product in (0, 1) if code else (0,):
+                fg.fg_set_gated_tile(product, code)
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
 def test_empty_sizes(ty):
     import torch
     dt = dtype_of(ty)
