@@ -187,7 +187,7 @@ struct Quad {
 // PIPE: the operands of a step are in registers before it begins, those of the next
 // are read during it, and so a stage is free for its next load a step earlier.
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS, bool PIPE, int MR>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(GatedTileParams p) {
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kernel(GatedTileParams p) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
     constexpr int TI = WM / MR, TJ = WN / MR;
     constexpr int SIZE = BF16 ? 2 : 4;
@@ -200,9 +200,11 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
     using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW, MR>;
     constexpr int kStage = TA::kBytes + TB::kBytes;
     constexpr int K1 = TA::kSteps;                   // k of a step
-    // (the results' way out: MR rows of every wave, and the rows' largest magnitudes)
+    // (the results' way out: MR rows of every wave, of both products, and what the
+    // codes of their rows are found with)
     constexpr int kPitch = kWaveCols + 4;
-    constexpr int kOut = NW * MR * kPitch * 4 + (kDual ? 2 * NWN * BM * 4 : 0);
+    constexpr int kOut = kDual ? 2 * NW * MR * kPitch * 4 + 2 * NWN * BM * 4 + 2 * (kCols / 128) * BM * 16
+                               : NW * MR * kPitch * 4;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kOut ? NS * kStage : kOut];
 
     const int lane = threadIdx.x & 63, n16 = lane % MR, g = lane / MR;
@@ -494,15 +496,16 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
         return;
     }
     if constexpr (kDual) {
-        if (p.save == SAVE_E4M3) {
-            // The largest finite magnitude of each row in the workgroup's 128 columns:
-            // of the wave's, then of its neighbours' along the row.
-            static_assert(kCols % 128 == 0 || kCols < 128, "whole blocks, or no codes");
-            if constexpr (kCols % 128 == 0) {
-                uint32_t* const most = reinterpret_cast<uint32_t*>(lds + NW * MR * kPitch * 4);
-                constexpr int kPerBlock = 128 / kWaveCols;   // waves
-                const int wn = wave / NWM;
-                uint32_t mine[2][TI];
+        // What dividing by the scale of a row in its block of 128 columns needs, from the
+        // row's largest finite magnitude in the block: of the wave's columns, then of its
+        // neighbours' along the row.
+        constexpr int kPerBlock = 128 / kWaveCols;   // waves
+        constexpr int kBlocks = kCols / 128;
+        uint32_t* const most = reinterpret_cast<uint32_t*>(lds + 2 * NW * MR * kPitch * 4);
+        Divisor* const by = reinterpret_cast<Divisor*>(most + 2 * NWN * BM);
+        if constexpr (kBlocks > 0) {
+            static_assert(kCols % 128 == 0, "whole blocks, or no codes");
+            if (p.save == SAVE_E4M3) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -515,77 +518,89 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) gated_tile_kernel(
                                 v = max(v, finite_magnitude(acc[i][m * PJ + j].v[e]));
 #pragma unroll
                         for (int o = MR; o < 64; o *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-                        mine[m][i] = v;
-                        if (g == 0) most[(m * NWN + wn) * BM + wi + MR * i + n16] = v;
+                        if (g == 0) most[(m * NWN + wave / NWM) * BM + wi + MR * i + n16] = v;
                     }
                 __syncthreads();
+                for (int k = threadIdx.x; k < 2 * kBlocks * BM; k += 64 * NW) {
+                    const int m = k / (kBlocks * BM), block = k / BM % kBlocks, r = k % BM;
+                    uint32_t v = 0;
 #pragma unroll
-                for (int i = 0; i < TI; ++i)
+                    for (int w = 0; w < kPerBlock; ++w)
+                        v = max(v, most[(m * NWN + block * kPerBlock + w) * BM + r]);
+                    const float s = scale_of(v);
+                    by[k] = divisor_of(s);
+                    if (m0 + r < p.M && n0 + block * 128 < p.N)
+                        (m ? +p.scales[1] : +p.scales[0])[(n0 / 128 + block) *
+                            (m ? +p.ld_scales[1] : +p.ld_scales[0]) + m0 + r] = s;
+                }
+                __syncthreads();
+            }
+        }
+        // Row tile by row tile in one loop, whose code is fetched once (unrolled it was 130
+        // KB, and a tile's end took 23 us with codes, 11 with values, against ...).
+        float* const own_u = own + NW * MR * kPitch;
+        constexpr int kTurns = MR / kRows;
+        auto codes_out = [&](int m, const f4& v, const Divisor& d, int64_t row, int64_t col) __attribute__((always_inline)) {
+            const uint32_t c = codes4(v, [&](int) { return d[0]; }, [&](int) { return d; });
+            uint8_t* const to = static_cast<uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
+            if (col + 4 <= p.N) {
+                *reinterpret_cast<uint32_t*>(to) = c;
+            } else {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t v = mine[m][i];
-                        const int w0 = wn / kPerBlock * kPerBlock;
+                for (int e = 0; e < 3; ++e)
+                    if (col + e < p.N) to[e] = (uint8_t)(c >> (8 * e));
+            }
+        };
+        auto out = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (int i = 0; i < TI; ++i) {
 #pragma unroll
-                        for (int w = 0; w < kPerBlock; ++w)
-                            v = max(v, most[(m * NWN + w0 + w) * BM + wi + MR * i + n16]);
-                        const float s = scale_of(v);
-                        const Divisor d = divisor_of(s);
-                        const int64_t row = m0 + wi + MR * i + n16, col = n0 + wj;
-                        if (g == 0 && wn == w0 && row < p.M)
-                            p.scales[m][col / 128 * p.ld_scales[m] + row] = s;
-                        // codes: a dword per lane and column tile, rows of kWaveCols bytes
-                        uint8_t* const bytes = reinterpret_cast<uint8_t*>(own);
+                for (int k = 0; k < TI; ++k) {
+                    if (__builtin_amdgcn_readfirstlane(i) != k) continue;   // (k stays a constant)
 #pragma unroll
-                        for (int j = 0; j < PJ; ++j)
+                    for (int j = 0; j < PJ; ++j)
 #pragma unroll
-                            for (int q = 0; q < kQuads; ++q)
-                                *reinterpret_cast<uint32_t*>(bytes + n16 * (kWaveCols + 4) + MR * j + kApart * q + 4 * g) =
-                                    codes4(acc[i][m * PJ + j].quad(q), [&](int) { return d[0]; }, [&](int) { return d; });
-                        settle();
-                        uint32_t c[MR / kRows];
+                        for (int q = 0; q < kQuads; ++q) {
+                            const int to = n16 * kPitch + MR * j + kApart * q + 4 * g;
+                            *reinterpret_cast<f4*>(own + to) = acc[k][j].quad(q);
+                            *reinterpret_cast<f4*>(own_u + to) = acc[k][PJ + j % PJ].quad(q);
+                        }
+                }
+                settle();
+                f4 vg[kTurns], vu[kTurns];
 #pragma unroll
-                        for (int r = 0; r < MR / kRows; ++r)
-                            c[r] = *reinterpret_cast<const uint32_t*>(
-                                bytes + (r * kRows + er) * (kWaveCols + 4) + ec);
-                        settle();
+                for (int r = 0; r < kTurns; ++r) {
+                    vg[r] = *reinterpret_cast<const f4*>(own + (r * kRows + er) * kPitch + ec);
+                    vu[r] = *reinterpret_cast<const f4*>(own_u + (r * kRows + er) * kPitch + ec);
+                }
+                const int64_t col = n0 + wj + ec;
 #pragma unroll
-                        for (int r = 0; r < MR / kRows; ++r) {
-                            const int64_t cr = m0 + wi + MR * i + r * kRows + er, cc = n0 + wj + ec;
-                            if (cr >= p.M || cc >= p.N) continue;
-                            uint8_t* q = static_cast<uint8_t*>(p.saved[m]) + cr * p.ld_saved[m] + cc;
-                            if (cc + 4 <= p.N) *reinterpret_cast<uint32_t*>(q) = c[r];
-                            else
-                                for (int e = 0; e < 3 && cc + e < p.N; ++e) q[e] = (uint8_t)(c[r] >> (8 * e));
+                for (int r = 0; r < kTurns; ++r) {
+                    const int in = wi + MR * i + r * kRows + er;
+                    const int64_t row = m0 + in;
+                    if (row >= p.M || col >= p.N) continue;
+                    f4 h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = activate_t<decltype(act)::value>(vg[r][e]) * vu[r][e];
+                    put(p.C[0], p.ldc[0], row, col, h);
+                    if (p.save == SAVE_SAME) {
+                        put(p.saved[0], p.ld_saved[0], row, col, vg[r]);
+                        put(p.saved[1], p.ld_saved[1], row, col, vu[r]);
+                    }
+                    if constexpr (kBlocks > 0) {
+                        if (p.save == SAVE_E4M3) {
+                            const Divisor* const d = by + (wj + ec) / 128 * BM + in;
+                            codes_out(0, vg[r], d[0], row, col);
+                            codes_out(1, vu[r], d[kBlocks * BM], row, col);
                         }
                     }
+                }
             }
-        } else if (p.save == SAVE_SAME) {
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    by_rows(i, [&](int j, int q) { return acc[i][m * PJ + j].quad(q); },
-                            [&](int64_t row, int64_t col, const f4& v) {
-                                put(p.saved[m], p.ld_saved[m], row, col, v);
-                            });
-        }
-        auto products = [&](auto act) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                by_rows(i,
-                        [&](int j, int q) {
-                            const f4 a = acc[i][j].quad(q), u = acc[i][PJ + j % PJ].quad(q);
-                            f4 h;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) h[e] = activate_t<decltype(act)::value>(a[e]) * u[e];
-                            return h;
-                        },
-                        [&](int64_t row, int64_t col, const f4& v) { put(p.C[0], p.ldc[0], row, col, v); });
         };
-        if (p.act == ACT_SILU) products(ActTag<ACT_SILU>{});
-        else if (p.act == ACT_GELU) products(ActTag<ACT_GELU>{});
-        else if (p.act == ACT_RELU) products(ActTag<ACT_RELU>{});
-        else products(ActTag<ACT_NONE>{});
+        if (p.act == ACT_SILU) out(ActTag<ACT_SILU>{});
+        else if (p.act == ACT_GELU) out(ActTag<ACT_GELU>{});
+        else if (p.act == ACT_RELU) out(ActTag<ACT_RELU>{});
+        else out(ActTag<ACT_NONE>{});
     } else {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
@@ -630,25 +645,36 @@ hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
 template <int OP, bool BF16>
 __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;
-    const int64_t nb = (p.N + 127) / 128, units = nb * p.M * (OP == GATED_DW ? 2 : 1);
+    const int nb = (p.N + 127) / 128, all = p.M * (OP == GATED_DW ? 2 : 1);
     const int64_t slice = (int64_t)p.M * p.N;
     constexpr int kEach = OP == GATED_DX ? 1 : 2;
-    const int l = threadIdx.x & 31;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units;
-         u += (int64_t)gridDim.x * 8) {
-        const int which = OP == GATED_DW && u >= nb * p.M ? 1 : 0;
-        const int64_t v = u - (which ? nb * p.M : 0);
-        const int64_t row = v / nb, block = v - row * nb, col = block * 128 + 4 * l;
-        const int n = p.N - col < 4 ? (int)(p.N - col) : 4;   // (may be below 1)
+    const int l = threadIdx.x & 31, block = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (block >= nb) return;
+    const int64_t col = (int64_t)block * 128 + 4 * l;
+    const int n = p.N - col < 4 ? (int)(p.N - col) : 4;   // (may be below 1)
+    for (int v = blockIdx.y; v < all; v += gridDim.y) {
+        const int which = OP == GATED_DW && v >= p.M ? 1 : 0;
+        const int64_t row = v - (which ? p.M : 0);
         auto sum = [&](int m) {
             f4 s = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < p.splits; ++k) {
-                const float* w = p.ws + (k * kEach + which + m) * slice + row * p.N + col;
-                f4 a = {0.f, 0.f, 0.f, 0.f};
-                if (n >= 4) __builtin_memcpy(&a, w, sizeof a);
-                else
-                    for (int e = 0; e < n; ++e) a[e] = w[e];
-                s = s + a;
+            const float* const w = p.ws + (which + m) * slice + row * p.N + col;
+            for (int k = 0; k < p.splits; k += 4) {
+                f4 a[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q] = f4{0.f, 0.f, 0.f, 0.f};
+                    if (k + q >= p.splits) continue;
+                    const float* const at = w + (int64_t)(k + q) * kEach * slice;
+                    if (n >= 4) {
+                        __builtin_memcpy(&a[q], at, sizeof a[q]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (e < n) a[q][e] = at[e];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s = s + a[q];
             }
             return s;
         };
@@ -717,7 +743,7 @@ constexpr GatedShape kForwardF32[] = {
 };
 constexpr GatedShape kBackward[] = {
     {256, 256, 64, 6.0f, 0.50f},
-    {128, 128, 128, 4.0f, 0.50f},
+    {128, 256, 64, 4.0f, 0.33f},
     {64, 128, 128, 3.0f, 0.35f},
 };
 
@@ -738,7 +764,7 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
     if (op == GATED_FORWARD && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 64, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
             case 2: return launch_tile<GATED_FORWARD, true, 128, 128, 64, 64, 128, 4>(p, stream);
             case 3: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 128, 3>(p, stream);
         }
@@ -751,13 +777,13 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
     } else if (op == GATED_DX && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 128, 4>(p, stream);
+            case 1: return launch_tile<GATED_DX, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
             case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 4>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 128, 4>(p, stream);
+            case 1: return launch_tile<GATED_DW, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
             case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 4>(p, stream);
         }
     }
@@ -765,9 +791,8 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
 }
 
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream) {
-    const int64_t units = ((int64_t)p.N + 127) / 128 * p.M * (op == GATED_DW ? 2 : 1);
-    const int64_t wgs = (units + 7) / 8;
-    const dim3 grid((unsigned)(wgs < 16384 ? wgs : 16384));
+    const int64_t rows = (int64_t)p.M * (op == GATED_DW ? 2 : 1);
+    const dim3 grid((unsigned)((((int64_t)p.N + 127) / 128 + 7) / 8), (unsigned)(rows < 65535 ? rows : 65535));
     auto kernel = op == GATED_FORWARD ? (bf16 ? gated_finish_kernel<GATED_FORWARD, true>
                                               : gated_finish_kernel<GATED_FORWARD, false>)
                 : op == GATED_DX      ? gated_finish_kernel<GATED_DX, true>
@@ -807,13 +832,14 @@ __device__ __forceinline__ void activate_both(float x, float& a, float& d) {
 template <bool BF16, bool CODES, int ACT>
 __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;
-    const int per_row = (int)(p.ld_d / 4);
-    const int64_t units = (int64_t)p.T * per_row;
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * 256) {
-        const int64_t row = u / per_row;
-        const int col = (int)(u - row * per_row) * 4;
-        const int n = p.I - col < 4 ? p.I - col : 4;
+    // a workgroup: 1024 columns of a row, or as many short rows as fit
+    const int per_row = (int)(p.ld_d / 4), tid = threadIdx.x;
+    const int rows = per_row < 256 ? 256 / per_row : 1;
+    const int in = per_row < 256 ? tid / per_row : 0;
+    const int col = 4 * (per_row < 256 ? tid - in * per_row : (int)blockIdx.x * 256 + tid);
+    if (in >= rows || col >= p.ld_d) return;
+    const int n = p.I - col < 4 ? p.I - col : 4;
+    for (int64_t row = (int64_t)blockIdx.y * rows + in; row < p.T; row += (int64_t)gridDim.y * rows) {
         auto get = [&](const void* base, int64_t ld) {
             const uint8_t* at = static_cast<const uint8_t*>(base) + (row * ld + col) * SIZE;
             Quad<BF16> q{};
@@ -875,8 +901,10 @@ void launch_grad(const GatedGradParams& p, dim3 grid, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_gated_grad(bool bf16, const GatedGradParams& p, hipStream_t stream) {
-    const int64_t wgs = (p.T * (p.ld_d / 4) + 255) / 256;
-    const dim3 grid((unsigned)(wgs < 65536 ? wgs : 65536));
+    const int64_t per_row = p.ld_d / 4, rows = per_row < 256 ? 256 / per_row : 1;
+    const int64_t groups = (p.T + rows - 1) / rows;
+    const dim3 grid((unsigned)(per_row < 256 ? 1 : (per_row + 255) / 256),
+                    (unsigned)(groups < 65535 ? groups : 65535));
     const bool codes = p.save == SAVE_E4M3;
     if (bf16 && codes) launch_grad<true, true>(p, grid, stream);
     else if (bf16) launch_grad<true, false>(p, grid, stream);
