@@ -90,36 +90,45 @@ Sizes sizes_of(int op, int64_t T, int64_t H, int64_t I) {
     return {I, H, T, 2, 1};
 }
 
+// The cheapest by estimate: rounds of as many workgroups as run together, the last of
+// which may have one to a CU; slices of the sum cost a kernel and their partial sums'
+// way to memory and back. codes: a block of 128 columns has to be in one workgroup,
+// or in the kernel that joins slices.
 Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) {
     constexpr double kCUs = 256, kPartial = 4e6;  // bytes per us
-    constexpr double kFinish = 7;                 // us
+    constexpr double kFinish = 4;                 // us
     constexpr double kMaxTiles = 1 << 23;         // of 512 threads: a grid has fewer than 2^32
     Forced& forced = g_forced[op][bf16];
     const int only = forced.tile.load(), slices = forced.slices.load();
     const double slice = (double)z.M * (double)z.N * 4 * z.results;
     Plan best{-1, 0, 0, 1};
     double best_us = 0;
-    for (int s = 0; s < fg::gated_num_shapes(op, bf16); ++s) {
-        const fg::GatedShape sh = fg::gated_shape(op, bf16, s);
-        const bool usable = !codes || sh.bn % 128 == 0;
-        if (!usable || (only >= 0 && s != only && !(codes && fg::gated_shape(op, bf16, only).bn % 128)))
-            continue;
-        const double tiles = (double)cdiv(z.M, sh.bm) * (double)cdiv(z.N, sh.bn) *
-                             (op == fg::GATED_DW ? 2 : 1);
-        if (tiles >= kMaxTiles) continue;
-        const int64_t steps = cdiv(z.K * (bf16 ? 2 : 4), sh.kb) * z.terms;
-        for (int64_t n = 1; n <= 16; n *= 2) {
-            const int64_t per = cdiv(steps, n), used = cdiv(steps, per);
-            if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
-            const double rounds = std::ceil(tiles * (double)n / kCUs);
-            double us = rounds * (sh.start_us + (double)per * sh.step_us);
-            if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
-            if (slices > 0 && n == slices) us = -1;   // (as asked)
-            if (best.shape < 0 || us < best_us) {
-                best = Plan{s, steps, per, n};
-                best_us = us;
+    for (int pass = 0; pass < 2 && best.shape < 0; ++pass) {   // (1: the forced tile cannot)
+        for (int s = 0; s < fg::gated_num_shapes(op, bf16); ++s) {
+            const fg::GatedShape sh = fg::gated_shape(op, bf16, s);
+            if (pass == 0 && only >= 0 && s != only) continue;
+            const double tiles = (double)cdiv(z.M, sh.bm) * (double)cdiv(z.N, sh.bn) *
+                                 (op == fg::GATED_DW ? 2 : 1);
+            if (tiles >= kMaxTiles) continue;
+            const int64_t steps = cdiv(z.K * (bf16 ? 2 : 4), sh.kb) * z.terms;
+            for (int64_t n = 1; n <= 16; n *= 2) {
+                const int64_t per = cdiv(steps, n), used = cdiv(steps, per);
+                if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
+                if (n == 1 && codes && sh.bn % 128) continue;
+                const double slots = kCUs * sh.per_cu, full = std::floor(tiles * (double)n / slots);
+                const double rest = tiles * (double)n - full * slots;
+                double us = full * (sh.start_us + (double)per * sh.full_us);
+                if (rest > 0)
+                    us += sh.start_us + (double)per * (rest <= kCUs ? sh.step_us : sh.full_us);
+                if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
+                if (pass == 0 && slices > 0 && n == slices) us = -1;   // (as asked)
+                if (best.shape < 0 || us < best_us) {
+                    best = Plan{s, steps, per, n};
+                    best_us = us;
+                }
             }
         }
+        if (only < 0) break;
     }
     return best;
 }

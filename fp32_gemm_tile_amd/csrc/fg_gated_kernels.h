@@ -89,8 +89,10 @@ struct GatedTileParams {
 struct GatedShape {
     int bm, bn;            // rows and columns of C per workgroup
     int kb;                // bytes of k per step
-    float start_us;        // of a round of 256 workgroups
-    float step_us;         // of a step in it
+    int per_cu;            // workgroups that run on a CU together
+    float start_us;        // of a round: one workgroup on a CU, or per_cu
+    float step_us;         // of a step of one workgroup alone on its CU
+    float full_us;         // of a step of per_cu workgroups
 };
 int gated_num_shapes(int op, bool bf16);
 GatedShape gated_shape(int op, bool bf16, int shape);

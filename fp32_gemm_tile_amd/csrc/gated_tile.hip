@@ -151,6 +151,21 @@ template <bool BF16>
 struct Quad {
     uint32_t u[BF16 ? 2 : 4];
     __device__ __forceinline__ void load(const uint8_t* c) { __builtin_memcpy(u, c, sizeof u); }
+    // the first n of them, zeros after them
+    __device__ __forceinline__ void load(const uint8_t* c, int n) {
+        if (n >= 4) {
+            load(c);
+            return;
+        }
+#pragma unroll
+        for (int d = 0; d < (BF16 ? 2 : 4); ++d) u[d] = 0;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (e >= n) continue;
+            if constexpr (BF16) u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(c)[e] << (16 * (e & 1));
+            else u[e] = reinterpret_cast<const uint32_t*>(c)[e];
+        }
+    }
     __device__ __forceinline__ f4 values() const {
         f4 v;
 #pragma unroll
@@ -394,10 +409,11 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
                 for (int i = u == 0 ? 1 : 0; i < TI; ++i) row(now, u, i);
             constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? 2 : 1) + TJ * (kDual ? 1 : 2));
             constexpr int kLeft = kSubs * TI * TJ - TJ;
+            constexpr int kGroups = kReads < kLeft ? kReads : kLeft;
 #pragma unroll
-            for (int k = 0; k < kReads; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
-                __builtin_amdgcn_sched_group_barrier(0x008, kLeft / kReads, 0);          // matrix
+            for (int k = 0; k < kGroups; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kGroups - 1) / kGroups, 0);   // LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x008, kLeft / kGroups, 0);                    // matrix
             }
         };
         Operands o[2];
@@ -609,16 +625,8 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
                         if (OP == GATED_DW && p.beta != 0.f) {
                             const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) +
                                                (row * p.ldc[which] + col) * SIZE;
-                            Quad<BF16> old{};
-                            if (col + 4 <= p.N) {
-                                old.load(c);
-                            } else if constexpr (BF16) {
-                                for (int e = 0; e < 3 && col + e < p.N; ++e)
-                                    old.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(c)[e] << (16 * (e & 1));
-                            } else {
-                                for (int e = 0; e < 3 && col + e < p.N; ++e)
-                                    old.u[e] = reinterpret_cast<const uint32_t*>(c)[e];
-                            }
+                            Quad<BF16> old;
+                            old.load(c, p.N - col < 4 ? (int)(p.N - col) : 4);
                             const f4 o = old.values();
 #pragma unroll
                             for (int e = 0; e < 4; ++e) v[e] = fmaf(p.beta, o[e], v[e]);
@@ -705,22 +713,21 @@ __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
                     const uint32_t c = codes4(x, [&](int) { return d[0]; }, [&](int) { return d; });
                     if (l == 0) p.scales[m][block * p.ld_scales[m] + row] = s;
                     uint8_t* q = static_cast<uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
-                    if (n >= 4) *reinterpret_cast<uint32_t*>(q) = c;
-                    else
-                        for (int e = 0; e < n; ++e) q[e] = (uint8_t)(c >> (8 * e));
+                    if (n >= 4) {
+                        *reinterpret_cast<uint32_t*>(q) = c;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (e < n) q[e] = (uint8_t)(c >> (8 * e));
+                    }
                 }
             }
         } else {
             f4 v4 = a;
             if (OP == GATED_DW && p.beta != 0.f) {
                 const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) + (row * p.ldc[which] + col) * SIZE;
-                Quad<BF16> old{};
-                if (n >= 4) old.load(c);
-                else if constexpr (BF16)
-                    for (int e = 0; e < n; ++e)
-                        old.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(c)[e] << (16 * (e & 1));
-                else
-                    for (int e = 0; e < n; ++e) old.u[e] = reinterpret_cast<const uint32_t*>(c)[e];
+                Quad<BF16> old;
+                old.load(c, n);
                 const f4 o = old.values();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v4[e] = fmaf(p.beta, o[e], v4[e]);
@@ -730,33 +737,43 @@ __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
     }
 }
 
+// The tiles, with what one costs by estimate: the start and end of a round, and a step
+// of 64 bytes of k for a workgroup alone on its CU and for as many as fit. From times
+// of 1 to 1024 workgroups of 16 and 64 steps (128 and 32 for binary32).
 constexpr GatedShape kForwardBf16[] = {
-    {256, 128, 64, 6.0f, 0.50f},
-    {128, 128, 64, 4.0f, 0.33f},
-    {128, 64, 128, 3.0f, 0.40f},
-    {64, 128, 128, 3.0f, 0.40f},
+    {256, 128, 64, 1, 9.5f, 0.78f, 0.78f},
+    {128, 128, 64, 2, 8.0f, 0.48f, 0.93f},
+    {64, 128, 64, 1, 6.5f, 0.39f, 0.39f},
+    {64, 64, 64, 2, 4.8f, 0.18f, 0.42f},
 };
 constexpr GatedShape kForwardF32[] = {
-    {128, 128, 64, 6.0f, 3.6f},
-    {128, 64, 64, 4.0f, 1.8f},
-    {64, 64, 128, 4.0f, 2.0f},
+    {128, 128, 64, 1, 10.0f, 1.83f, 1.83f},
+    {128, 64, 64, 2, 7.0f, 0.97f, 1.82f},
+    {64, 64, 64, 2, 5.0f, 0.56f, 0.98f},
 };
-constexpr GatedShape kBackward[] = {
-    {256, 256, 64, 6.0f, 0.50f},
-    {128, 256, 64, 4.0f, 0.33f},
-    {64, 128, 128, 3.0f, 0.35f},
+constexpr GatedShape kDx[] = {
+    {256, 256, 64, 1, 8.0f, 0.81f, 0.81f},
+    {128, 128, 64, 2, 5.5f, 0.37f, 0.54f},
+    {64, 128, 64, 2, 4.8f, 0.29f, 0.40f},
+};
+constexpr GatedShape kDw[] = {
+    {256, 256, 64, 1, 8.0f, 0.76f, 0.76f},
+    {128, 128, 64, 2, 5.5f, 0.34f, 0.47f},
+    {64, 128, 64, 2, 4.8f, 0.23f, 0.33f},
 };
 
 }  // namespace
 
 int gated_num_shapes(int op, bool bf16) {
-    if (op != GATED_FORWARD) return bf16 ? (int)(sizeof kBackward / sizeof kBackward[0]) : 0;
-    return bf16 ? (int)(sizeof kForwardBf16 / sizeof kForwardBf16[0])
-                : (int)(sizeof kForwardF32 / sizeof kForwardF32[0]);
+    if (op == GATED_FORWARD)
+        return bf16 ? (int)(sizeof kForwardBf16 / sizeof kForwardBf16[0])
+                    : (int)(sizeof kForwardF32 / sizeof kForwardF32[0]);
+    if (!bf16) return 0;
+    return op == GATED_DX ? (int)(sizeof kDx / sizeof kDx[0]) : (int)(sizeof kDw / sizeof kDw[0]);
 }
 GatedShape gated_shape(int op, bool bf16, int shape) {
-    if (op != GATED_FORWARD) return kBackward[shape];
-    return bf16 ? kForwardBf16[shape] : kForwardF32[shape];
+    if (op == GATED_FORWARD) return bf16 ? kForwardBf16[shape] : kForwardF32[shape];
+    return op == GATED_DX ? kDx[shape] : kDw[shape];
 }
 
 hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
@@ -765,26 +782,26 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
         switch (shape) {
             case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, true, 128, 128, 64, 64, 128, 4>(p, stream);
-            case 3: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 128, 3>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 64, 6, true>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
         }
     } else if (op == GATED_FORWARD) {
         switch (shape) {
-            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 64, 4>(p, stream);
-            case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 64, 128, 3>(p, stream);
+            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 64, 4, true>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4, true>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 64, 64, 6, true>(p, stream);
         }
     } else if (op == GATED_DX && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DX, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
-            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 4>(p, stream);
+            case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
+            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DW, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
-            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 4>(p, stream);
+            case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
+            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
         }
     }
     return hipErrorInvalidValue;
@@ -840,37 +857,43 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
     if (in >= rows || col >= p.ld_d) return;
     const int n = p.I - col < 4 ? p.I - col : 4;
     for (int64_t row = (int64_t)blockIdx.y * rows + in; row < p.T; row += (int64_t)gridDim.y * rows) {
-        auto get = [&](const void* base, int64_t ld) {
-            const uint8_t* at = static_cast<const uint8_t*>(base) + (row * ld + col) * SIZE;
-            Quad<BF16> q{};
-            if (n >= 4) q.load(at);
-            else if constexpr (BF16)
-                for (int e = 0; e < n; ++e)
-                    q.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(at)[e] << (16 * (e & 1));
-            else
-                for (int e = 0; e < n; ++e) q.u[e] = reinterpret_cast<const uint32_t*>(at)[e];
-            return q.values();
-        };
-        f4 pre[2], dg = {0.f, 0.f, 0.f, 0.f}, du = dg, h = dg;
-        if (n > 0) {
-            const f4 dh = get(p.dh, p.lddh);
+        f4 dg = {0.f, 0.f, 0.f, 0.f}, du = dg, h = dg;
+        auto gradients = [&](int n) __attribute__((always_inline)) {
+            auto get = [&](const void* base, int64_t ld) {
+                Quad<BF16> q;
+                q.load(static_cast<const uint8_t*>(base) + (row * ld + col) * SIZE, n);
+                return q;
+            };
+            const Quad<BF16> dhq = get(p.dh, p.lddh);
+            f4 pre[2];
+            if constexpr (CODES) {
+                uint32_t c[2] = {0, 0};
+                float s[2];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if constexpr (CODES) {
-                    uint32_t c = 0;
+                for (int m = 0; m < 2; ++m) {
                     const uint8_t* at = static_cast<const uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
-                    if (n >= 4) c = *reinterpret_cast<const uint32_t*>(at);
-                    else
-                        for (int e = 0; e < n; ++e) c |= (uint32_t)at[e] << (8 * e);
-                    const float s = p.scales[m][(col >> 7) * p.ld_scales[m] + row];
-                    pre[m][0] = s * __builtin_amdgcn_cvt_f32_fp8(c, 0);
-                    pre[m][1] = s * __builtin_amdgcn_cvt_f32_fp8(c, 1);
-                    pre[m][2] = s * __builtin_amdgcn_cvt_f32_fp8(c, 2);
-                    pre[m][3] = s * __builtin_amdgcn_cvt_f32_fp8(c, 3);
-                } else {
-                    pre[m] = get(p.saved[m], p.ld_saved[m]);
+                    s[m] = p.scales[m][(col >> 7) * p.ld_scales[m] + row];
+                    if (n >= 4) {
+                        c[m] = *reinterpret_cast<const uint32_t*>(at);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            if (e < n) c[m] |= (uint32_t)at[e] << (8 * e);
+                    }
                 }
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    pre[m][0] = s[m] * __builtin_amdgcn_cvt_f32_fp8(c[m], 0);
+                    pre[m][1] = s[m] * __builtin_amdgcn_cvt_f32_fp8(c[m], 1);
+                    pre[m][2] = s[m] * __builtin_amdgcn_cvt_f32_fp8(c[m], 2);
+                    pre[m][3] = s[m] * __builtin_amdgcn_cvt_f32_fp8(c[m], 3);
+                }
+            } else {
+                const Quad<BF16> g = get(p.saved[0], p.ld_saved[0]), u = get(p.saved[1], p.ld_saved[1]);
+                pre[0] = g.values();
+                pre[1] = u.values();
             }
+            const f4 dh = dhq.values();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (e >= n) continue;
@@ -880,7 +903,9 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
                 dg[e] = dh[e] * pre[1][e] * d;
                 h[e] = a * pre[1][e];
             }
-        }
+        };
+        if (n >= 4) gradients(4);   // (all loads on their way together)
+        else if (n > 0) gradients(n);
         // (rows of dg and du end with zeros)
         const int64_t at = (row * p.ld_d + col) * SIZE;
         Quad<BF16>(dg).store(static_cast<uint8_t*>(p.dg) + at, 4);
