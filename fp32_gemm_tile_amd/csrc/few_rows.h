@@ -1,4 +1,4 @@
-// At most 64 rows of x beside weights that are streamed once:
+// A few rows of x (64, or 16 beside weights of x's type) and weights that are streamed once:
 //
 //   out = x W^T          or          out = act(x W0^T) * (x W1^T)
 //
@@ -590,9 +590,7 @@ hipError_t launch_ct(const RowsParams& p, hipStream_t stream) {
         return launch<KIND, XB, NM, RT, 4, 4, 1>(p, stream);
     } else {
         if (p.T <= 4) return launch<KIND, XB, NM, 1, 1, 1, 4>(p, stream);
-        if (p.T <= 16) return launch<KIND, XB, NM, 1, 1, 4, 4>(p, stream);
-        if (p.T <= 32) return launch<KIND, XB, NM, 2, 2, 4, 4>(p, stream);
-        return launch<KIND, XB, NM, 1, 4, 4, 4>(p, stream);
+        return launch<KIND, XB, NM, 1, 1, 4, 4>(p, stream);
     }
 }
 

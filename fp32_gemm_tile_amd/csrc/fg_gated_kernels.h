@@ -39,7 +39,11 @@ struct RowsParams {
     void* save[2];         // both products in x's type, or null
     int64_t ld_save[2];
 };
-constexpr int kRowsMaxTokens = 64;
+// Rows of x beside weights of its type. More of them, or one tile of 32 rows: 4096 x 8192
+// in bfloat16, 16 rows 33 us here and 30 in a tile, 17 rows 51 and 30; 2048 x 1408 10 and 9,
+// 16 and 9; binary32 17 and 26, 29 and 26.
+constexpr int kRowsMaxTokens = 16;
+constexpr int kInt4MaxRows = 64;   // FG_INT4_MAX_ROWS
 // launch_rows_<4-bit><bfloat16 x><matrices>, each a translation unit of few_rows.hip
 hipError_t launch_rows_002(const RowsParams& p, hipStream_t stream);
 hipError_t launch_rows_012(const RowsParams& p, hipStream_t stream);
@@ -48,7 +52,7 @@ hipError_t launch_rows_102(const RowsParams& p, hipStream_t stream);
 hipError_t launch_rows_111(const RowsParams& p, hipStream_t stream);
 hipError_t launch_rows_112(const RowsParams& p, hipStream_t stream);
 inline hipError_t launch_rows(const RowsParams& p, hipStream_t stream) {
-    if (p.T < 1 || p.T > kRowsMaxTokens) return hipErrorInvalidValue;
+    if (p.T < 1 || p.T > (p.group ? kInt4MaxRows : kRowsMaxTokens)) return hipErrorInvalidValue;
     if (!p.group) {
         if (p.matrices != 2) return hipErrorInvalidValue;
         return p.x_bf16 ? launch_rows_012(p, stream) : launch_rows_002(p, stream);

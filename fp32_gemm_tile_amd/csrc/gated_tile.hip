@@ -741,25 +741,31 @@ __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
 // of 64 bytes of k for a workgroup alone on its CU and for as many as fit. From times
 // of 1 to 1024 workgroups of 16 and 64 steps (128 and 32 for binary32).
 constexpr GatedShape kForwardBf16[] = {
-    {256, 128, 64, 1, 9.5f, 0.78f, 0.78f},
-    {128, 128, 64, 2, 8.0f, 0.48f, 0.93f},
-    {64, 128, 64, 1, 6.5f, 0.39f, 0.39f},
-    {64, 64, 64, 2, 4.8f, 0.18f, 0.42f},
+    {256, 128, 64, 1, 10.2f, 0.78f, 0.78f},
+    {128, 128, 64, 2, 9.0f, 0.49f, 0.90f},
+    {64, 64, 128, 2, 5.3f, 0.31f, 0.63f},
+    {64, 32, 128, 2, 6.0f, 0.16f, 0.35f},
+    {32, 32, 128, 2, 6.3f, 0.09f, 0.23f},
 };
 constexpr GatedShape kForwardF32[] = {
-    {128, 128, 64, 1, 10.0f, 1.83f, 1.83f},
-    {128, 64, 64, 2, 7.0f, 0.97f, 1.82f},
-    {64, 64, 64, 2, 5.0f, 0.56f, 0.98f},
+    {128, 128, 128, 1, 13.0f, 3.55f, 3.55f},
+    {128, 64, 64, 2, 8.0f, 0.98f, 1.82f},
+    {64, 64, 128, 2, 4.5f, 1.05f, 1.86f},
+    {64, 32, 128, 2, 4.0f, 0.59f, 1.03f},
+    {32, 32, 128, 2, 3.7f, 0.36f, 0.59f},
 };
 constexpr GatedShape kDx[] = {
     {256, 256, 64, 1, 8.0f, 0.81f, 0.81f},
-    {128, 128, 64, 2, 5.5f, 0.37f, 0.54f},
-    {64, 128, 64, 2, 4.8f, 0.29f, 0.40f},
+    {128, 128, 64, 2, 5.5f, 0.38f, 0.52f},
+    {64, 128, 128, 2, 5.0f, 0.46f, 0.65f},
+    {64, 64, 128, 2, 5.5f, 0.27f, 0.47f},
+    {32, 64, 128, 2, 5.5f, 0.17f, 0.36f},
 };
 constexpr GatedShape kDw[] = {
-    {256, 256, 64, 1, 8.0f, 0.76f, 0.76f},
-    {128, 128, 64, 2, 5.5f, 0.34f, 0.47f},
-    {64, 128, 64, 2, 4.8f, 0.23f, 0.33f},
+    {256, 256, 64, 1, 9.0f, 0.76f, 0.76f},
+    {128, 128, 64, 2, 5.5f, 0.33f, 0.46f},
+    {64, 128, 128, 2, 5.5f, 0.37f, 0.67f},
+    {64, 64, 128, 2, 6.5f, 0.18f, 0.46f},
 };
 
 }  // namespace
@@ -782,26 +788,32 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
         switch (shape) {
             case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, true, 64, 256, 64, 64, 64, 6, true>(p, stream);
-            case 3: return launch_tile<GATED_FORWARD, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
+            case 4: return launch_tile<GATED_FORWARD, true, 32, 64, 16, 32, 128, 6, true>(p, stream);
         }
     } else if (op == GATED_FORWARD) {
         switch (shape) {
-            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 64, 4, true>(p, stream);
+            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 128, 3, true>(p, stream);
             case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 64, 64, 6, true>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 32, 128, 3, true>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, false, 64, 64, 32, 32, 128, 4, true>(p, stream);
+            case 4: return launch_tile<GATED_FORWARD, false, 32, 64, 16, 32, 128, 6, true>(p, stream);
         }
     } else if (op == GATED_DX && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
+            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
+            case 3: return launch_tile<GATED_DX, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
+            case 4: return launch_tile<GATED_DX, true, 32, 64, 16, 32, 128, 6, true>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {
             case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
             case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 64, 6, true>(p, stream);
+            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
+            case 3: return launch_tile<GATED_DW, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
         }
     }
     return hipErrorInvalidValue;
