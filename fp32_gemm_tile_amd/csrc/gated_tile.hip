@@ -30,35 +30,20 @@ namespace {
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-// Sums of an MR x MR block as a lane holds them: quads of consecutive columns of C, MR
-// / 4 apart times the lane groups.
-template <int MR>
-struct Block {
-    typedef float vec __attribute__((ext_vector_type(MR * MR / 64)));
-    vec v;
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int e = 0; e < MR * MR / 64; ++e) v[e] = 0.f;
-    }
-    __device__ __forceinline__ f4 quad(int q) const {
-        return f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-    }
-};
-
-template <bool BF16, int MR>
-__device__ __forceinline__ void mfma(i4v a, i4v b, Block<MR>& c) {
+// 16 x 16 products: lane (n, g) = (lane % 16, lane / 16) gives row n of both operands
+// and gets columns 4 g to 4 g + 3 of row n of C (the operands are exchanged, so that a
+// lane's sums are neighbours in a row).
+template <bool BF16>
+__device__ __forceinline__ void mfma(i4v a, i4v b, f4& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (BF16 && MR == 32) {
-        c.v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a),
-                                                      __builtin_bit_cast(bf8, b), c.v, 0, 0, 0);
-    } else if constexpr (BF16) {
-        c.v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
-                                                      __builtin_bit_cast(bf8, b), c.v, 0, 0, 0);
+    if constexpr (BF16) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
+                                                    __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     } else {
         const f4 fa = __builtin_bit_cast(f4, a), fb = __builtin_bit_cast(f4, b);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            c.v = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c.v, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
     }
 #else
     (void)a, (void)b, (void)c;
@@ -96,7 +81,7 @@ __device__ __forceinline__ i4v keep(i4v v, int left) {
 
 // A tile of R rows (of m or n) and KB bytes of k, and how it gets to LDS and back.
 // ALONG_K: stored with k along its rows.
-template <bool BF16, bool ALONG_K, int R, int KB, int NW, int MR>
+template <bool BF16, bool ALONG_K, int R, int KB, int NW>
 struct Tile {
     static constexpr int kSize = BF16 ? 2 : 4;
     static constexpr int kBytes = R * KB;
@@ -115,8 +100,7 @@ struct Tile {
     // Else the eight rows that 32 lanes read together do.
     static __device__ __forceinline__ int turn(int r) {
         if constexpr (ALONG_K && KB == 128) return (r >> 1) & 7;
-        else if constexpr (ALONG_K) return MR == 32 ? ((r >> 3) & 1) | ((r >> 1) & 2) : (r >> 2) & 2;
-        else if constexpr (MR == 32) return 4 * (r & 3);
+        else if constexpr (ALONG_K) return (r >> 2) & 2;
         else if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
         else return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
     }
@@ -127,18 +111,18 @@ struct Tile {
         const int c = (lane % kLanesPerRow) ^ turn(r);
         return (uint32_t)(r * ld * kSize) + (uint32_t)(c * 16);
     }
-    // What lane (n, g) = (lane % MR, lane / MR) gives to the instruction in sub-step
-    // `sub`: the 16 bytes of k from 16 (64 / MR sub + g) of row r0 + n (r0 a multiple of
-    // MR), the same k from a tile of either kind.
+    // What lane (n, g) = (lane % 16, lane / 16) gives to the instruction in sub-step
+    // `sub`: the 16 bytes of k from 16 (4 sub + g) of row r0 + n (r0 a multiple of 16),
+    // the same k from a tile of either kind.
     static __device__ __forceinline__ i4v read(const uint8_t* tile, int r0, int sub, int lane) {
-        const int n = lane % MR, g = lane / MR;
+        const int n = lane & 15, g = lane >> 4;
         if constexpr (ALONG_K) {
             return *reinterpret_cast<const i4v*>(tile + (r0 + n) * KB +
-                                                 (((sub * (64 / MR) + g) ^ turn(n)) << 4));
+                                                 (((4 * sub + g) ^ turn(n)) << 4));
         } else {
             const int i = lane & 15, k = 8 * g + (i >> 2);
-            const int c = r0 / 8 + (MR == 32 ? (lane >> 3) & 2 : 0) + ((i >> 1) & 1);
-            const uint8_t* at = tile + (sub * (512 / MR) + k) * kRowBytes + (i & 1) * 8 +
+            const int c = r0 / 8 + ((i >> 1) & 1);
+            const uint8_t* at = tile + (32 * sub + k) * kRowBytes + (i & 1) * 8 +
                                 ((c ^ turn(k)) << 4);
             const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * kRowBytes);
             return i4v{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
@@ -199,31 +183,31 @@ struct Quad {
     }
 };
 
-// PIPE: the operands of a step are in registers before it begins, those of the next
-// are read during it, and so a stage is free for its next load a step earlier.
-template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS, bool PIPE, int MR>
+// The operands of a step are in registers before it begins, those of the next are read
+// during it, and so a stage is free for its next load a step earlier.
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kernel(GatedTileParams p) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
-    constexpr int TI = WM / MR, TJ = WN / MR;
+    constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int SIZE = BF16 ? 2 : 4;
     constexpr bool kDual = OP == GATED_FORWARD;
     // (FORWARD: BN rows of B are BN / 2 of gate and BN / 2 of up)
     constexpr int kCols = kDual ? BN / 2 : BN;       // columns of C per workgroup
     constexpr int kWaveCols = kDual ? WN / 2 : WN;
     constexpr int PJ = kDual ? TJ / 2 : TJ;          // column tiles of one matrix
-    using TA = Tile<BF16, OP != GATED_DW, BM, KB, NW, MR>;
-    using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW, MR>;
+    using TA = Tile<BF16, OP != GATED_DW, BM, KB, NW>;
+    using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW>;
     constexpr int kStage = TA::kBytes + TB::kBytes;
     constexpr int K1 = TA::kSteps;                   // k of a step
-    // (the results' way out: MR rows of every wave, of both products, and what the
+    // (the results' way out: 16 rows of every wave, of both products, and what the
     // codes of their rows are found with)
     constexpr int kPitch = kWaveCols + 4;
-    constexpr int kOut = kDual ? 2 * NW * MR * kPitch * 4 + 2 * NWN * BM * 4 + 2 * (kCols / 128) * BM * 16
-                               : NW * MR * kPitch * 4;
+    constexpr int kOut = kDual ? 2 * NW * 16 * kPitch * 4 + 2 * NWN * BM * 4 + 2 * (kCols / 128) * BM * 16
+                               : NW * 16 * kPitch * 4;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kOut ? NS * kStage : kOut];
 
-    const int lane = threadIdx.x & 63, n16 = lane % MR, g = lane / MR;
-    constexpr int kSubs = KB * MR / 1024;   // instructions along k in a step
+    const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+    constexpr int kSubs = KB / 64;   // instructions along k in a step
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = (wave % NWM) * WM, wj = (wave / NWM) * kWaveCols;
     const int tiles_m = (p.M + BM - 1) / BM;
@@ -329,40 +313,18 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
         if constexpr (!kDual) base_b[0] += K1 * (up ? +p.ldb[1] : +p.ldb[0]) * SIZE;
     };
 
-    Block<MR> acc[TI][TJ];
+    f4 acc[TI][TJ];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j].clear();
+        for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
     // row of B's tile that column tile j of the wave starts at
     auto b_row = [&](int j) {
-        return kDual ? (j < PJ ? 0 : BN / 2) + wj + MR * (j % PJ) : wj + MR * j;
+        return kDual ? (j < PJ ? 0 : BN / 2) + wj + 16 * (j % PJ) : wj + 16 * j;
     };
-    auto use = [&](int stage, int left, auto tail) __attribute__((always_inline)) {
-        const uint8_t* const ta = lds + stage * kStage;
-        const uint8_t* const tb = ta + TA::kBytes;
-#pragma unroll
-        for (int sub = 0; sub < kSubs; ++sub) {
-            i4v a[TI], b[TJ];
-            auto kept = [&](i4v v) {
-                constexpr int kPer = 16 / SIZE;
-                if constexpr (decltype(tail)::value) return keep<BF16>(v, left - (sub * (64 / MR) + g) * kPer);
-                else return v;
-            };
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) b[j] = kept(TB::read(tb, b_row(j), sub, lane));
-#pragma unroll
-            for (int i = 0; i < TI; ++i) a[i] = kept(TA::read(ta, wi + MR * i, sub, lane));
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j) mfma<BF16, MR>(b[j], a[i], acc[i][j]);
-        }
-    };
-
     constexpr int kLoads = TA::kParts + TB::kParts;
-    static_assert((PIPE ? NS - 1 : NS - 2) * kLoads < 64, "loads left in flight must fit the vmcnt field");
+    static_assert((NS - 1) * kLoads < 64, "loads left in flight must fit the vmcnt field");
     auto meet = [] {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
                      : "memory");
@@ -371,123 +333,101 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     // which those past the last are zeros)
     const bool partial = kDual && s1 == p.steps && p.K % K1 != 0;
     const int whole_end = partial ? s1 - 1 : s1;
-    if constexpr (PIPE) {
-        struct Operands {
-            i4v a[kSubs][TI], b[kSubs][TJ];
-        };
-        auto read = [&](int stage, Operands& o) __attribute__((always_inline)) {
-            const uint8_t* const ta = lds + stage * kStage;
+    struct Operands {
+        i4v a[kSubs][TI], b[kSubs][TJ];
+    };
+    auto read = [&](int stage, Operands& o) __attribute__((always_inline)) {
+        const uint8_t* const ta = lds + stage * kStage;
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) o.b[u][j] = TB::read(ta + TA::kBytes, b_row(j), u, lane);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) o.a[u][i] = TA::read(ta, wi + 16 * i, u, lane);
+        }
+    };
+    auto row = [&](const Operands& o, int u, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) mfma<BF16>(o.b[u][j], o.a[u][i], acc[i][j]);
+    };
+    // Step s, its operands in `now`: stage s + 1 is there for everyone and everyone
+    // has read stage s, which is loaded again. The matrix instructions begin at
+    // once, the loads go out after the first row of them, and the reads between
+    // the others.
+    int stage = 0;
+    auto step = [&](int s, const Operands& now, Operands& next) __attribute__((always_inline)) {
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        row(now, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(s + NS, stage);
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        __builtin_amdgcn_sched_barrier(0);
+        read(stage, next);
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+            for (int i = u == 0 ? 1 : 0; i < TI; ++i) row(now, u, i);
+        constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? 2 : 1) + TJ * (kDual ? 1 : 2));
+        constexpr int kLeft = kSubs * TI * TJ - TJ;
+        constexpr int kGroups = kReads < kLeft ? kReads : kLeft;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kGroups - 1) / kGroups, 0);   // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, kLeft / kGroups, 0);                    // matrix
+        }
+    };
+    Operands o[2];
+#pragma unroll
+    for (int d = 0; d < NS; ++d) fetch(s0 + d, d);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 1) * kLoads) : "memory");
+    read(0, o[0]);
+    int s = s0;
+    for (; s + 2 <= whole_end; s += 2) {
+        step(s, o[0], o[1]);
+        step(s + 1, o[1], o[0]);
+    }
+    if (s < whole_end) {
+        step(s, o[0], o[1]);
+        if constexpr (kDual) o[0] = o[1];
+    }
+    if constexpr (kDual) {
+        if (partial) {
 #pragma unroll
             for (int u = 0; u < kSubs; ++u) {
+                const int left = p.K - (s1 - 1) * K1 - (4 * u + g) * (16 / SIZE);
 #pragma unroll
-                for (int j = 0; j < TJ; ++j) o.b[u][j] = TB::read(ta + TA::kBytes, b_row(j), u, lane);
+                for (int j = 0; j < TJ; ++j) o[0].b[u][j] = keep<BF16>(o[0].b[u][j], left);
 #pragma unroll
-                for (int i = 0; i < TI; ++i) o.a[u][i] = TA::read(ta, wi + MR * i, u, lane);
-            }
-        };
-        auto row = [&](const Operands& o, int u, int i) __attribute__((always_inline)) {
+                for (int i = 0; i < TI; ++i) o[0].a[u][i] = keep<BF16>(o[0].a[u][i], left);
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) mfma<BF16, MR>(o.b[u][j], o.a[u][i], acc[i][j]);
-        };
-        // Step s, its operands in `now`: stage s + 1 is there for everyone and everyone
-        // has read stage s, which is loaded again. The matrix instructions begin at
-        // once, the loads go out after the first row of them, and the reads between
-        // the others.
-        int stage = 0;
-        auto step = [&](int s, const Operands& now, Operands& next) __attribute__((always_inline)) {
-            meet();
-            __builtin_amdgcn_s_setprio(1);
-            row(now, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            fetch(s + NS, stage);
-            stage = stage + 1 == NS ? 0 : stage + 1;
-            __builtin_amdgcn_sched_barrier(0);
-            read(stage, next);
-#pragma unroll
-            for (int u = 0; u < kSubs; ++u)
-#pragma unroll
-                for (int i = u == 0 ? 1 : 0; i < TI; ++i) row(now, u, i);
-            constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? 2 : 1) + TJ * (kDual ? 1 : 2));
-            constexpr int kLeft = kSubs * TI * TJ - TJ;
-            constexpr int kGroups = kReads < kLeft ? kReads : kLeft;
-#pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kGroups - 1) / kGroups, 0);   // LDS reads
-                __builtin_amdgcn_sched_group_barrier(0x008, kLeft / kGroups, 0);                    // matrix
-            }
-        };
-        Operands o[2];
-#pragma unroll
-        for (int d = 0; d < NS; ++d) fetch(s0 + d, d);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 1) * kLoads) : "memory");
-        read(0, o[0]);
-        int s = s0;
-        for (; s + 2 <= whole_end; s += 2) {
-            step(s, o[0], o[1]);
-            step(s + 1, o[1], o[0]);
-        }
-        if (s < whole_end) {
-            step(s, o[0], o[1]);
-            if constexpr (kDual) o[0] = o[1];
-        }
-        if constexpr (kDual) {
-            if (partial) {
-#pragma unroll
-                for (int u = 0; u < kSubs; ++u) {
-                    const int left = p.K - (s1 - 1) * K1 - (u * (64 / MR) + g) * (16 / SIZE);
-#pragma unroll
-                    for (int j = 0; j < TJ; ++j) o[0].b[u][j] = keep<BF16>(o[0].b[u][j], left);
-#pragma unroll
-                    for (int i = 0; i < TI; ++i) o[0].a[u][i] = keep<BF16>(o[0].a[u][i], left);
-#pragma unroll
-                    for (int i = 0; i < TI; ++i) row(o[0], u, i);
-                }
-            }
-        }
-    } else {
-        int stage = 0;
-#pragma unroll
-        for (int d = 0; d < NS - 1; ++d) fetch(s0 + d, d);
-        for (int s = s0; s < whole_end; ++s) {
-            meet();
-            fetch(s + NS - 1, stage == 0 ? NS - 1 : stage - 1);
-            use(stage, 0, Flag<false>{});
-            stage = stage + 1 == NS ? 0 : stage + 1;
-        }
-        if constexpr (kDual) {
-            if (partial) {
-                meet();
-                fetch(s1 + NS - 2, stage == 0 ? NS - 1 : stage - 1);
-                use(stage, p.K - (s1 - 1) * K1, Flag<true>{});
+                for (int i = 0; i < TI; ++i) row(o[0], u, i);
             }
         }
     }
     auto all_done = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     all_done();
 
-    // The wave's MR rows at a time through its own part of the LDS, so that a store
+    // The wave's 16 rows at a time through its own part of the LDS, so that a store
     // covers consecutive elements of a row.
     constexpr int kLanes = kWaveCols / 4, kRows = 64 / kLanes;
-    float* const own = reinterpret_cast<float*>(lds) + wave * MR * kPitch;
+    float* const own = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
     const int er = lane / kLanes, ec = (lane % kLanes) * 4;
     auto settle = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-    constexpr int kQuads = MR * MR / 256, kApart = 4 * 64 / MR;   // quads of a block, columns between them
-    // of(j, q): quad q of column tile j of row tile i; to(row, column, value) for each
+    // of(j): column tile j of row tile i; to(row, column, value) for each
     auto by_rows = [&](int i, auto of, auto to) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < PJ; ++j)
-#pragma unroll
-            for (int q = 0; q < kQuads; ++q)
-                *reinterpret_cast<f4*>(own + n16 * kPitch + MR * j + kApart * q + 4 * g) = of(j, q);
+            *reinterpret_cast<f4*>(own + n16 * kPitch + 16 * j + 4 * g) = of(j);
         settle();
-        f4 v[MR / kRows];
+        f4 v[16 / kRows];
 #pragma unroll
-        for (int r = 0; r < MR / kRows; ++r)
+        for (int r = 0; r < 16 / kRows; ++r)
             v[r] = *reinterpret_cast<const f4*>(own + (r * kRows + er) * kPitch + ec);
         settle();
 #pragma unroll
-        for (int r = 0; r < MR / kRows; ++r) {
-            const int64_t row = m0 + wi + MR * i + r * kRows + er, col = n0 + wj + ec;
+        for (int r = 0; r < 16 / kRows; ++r) {
+            const int64_t row = m0 + wi + 16 * i + r * kRows + er, col = n0 + wj + ec;
             if (row < p.M && col < p.N) to(row, col, v[r]);
         }
     };
@@ -502,7 +442,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
         for (int i = 0; i < TI; ++i)
 #pragma unroll
             for (int m = 0; m < (kDual ? 2 : 1); ++m)
-                by_rows(i, [&](int j, int q) { return acc[i][m * PJ + j].quad(q); },
+                by_rows(i, [&](int j) { return acc[i][m * PJ + j]; },
                         [&](int64_t row, int64_t col, const f4& v) {
                             const int n = p.N - col < 4 ? (int)(p.N - col) : 4;
                             Quad<false>(v).store(
@@ -517,7 +457,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
         // neighbours' along the row.
         constexpr int kPerBlock = 128 / kWaveCols;   // waves
         constexpr int kBlocks = kCols / 128;
-        uint32_t* const most = reinterpret_cast<uint32_t*>(lds + 2 * NW * MR * kPitch * 4);
+        uint32_t* const most = reinterpret_cast<uint32_t*>(lds + 2 * NW * 16 * kPitch * 4);
         Divisor* const by = reinterpret_cast<Divisor*>(most + 2 * NWN * BM);
         if constexpr (kBlocks > 0) {
             static_assert(kCols % 128 == 0, "whole blocks, or no codes");
@@ -530,11 +470,11 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
 #pragma unroll
                         for (int j = 0; j < PJ; ++j)
 #pragma unroll
-                            for (int e = 0; e < MR * MR / 64; ++e)
-                                v = max(v, finite_magnitude(acc[i][m * PJ + j].v[e]));
+                            for (int e = 0; e < 4; ++e)
+                                v = max(v, finite_magnitude(acc[i][m * PJ + j][e]));
 #pragma unroll
-                        for (int o = MR; o < 64; o *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-                        if (g == 0) most[(m * NWN + wave / NWM) * BM + wi + MR * i + n16] = v;
+                        for (int o = 16; o < 64; o *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+                        if (g == 0) most[(m * NWN + wave / NWM) * BM + wi + 16 * i + n16] = v;
                     }
                 __syncthreads();
                 for (int k = threadIdx.x; k < 2 * kBlocks * BM; k += 64 * NW) {
@@ -554,8 +494,8 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
         }
         // Row tile by row tile in one loop, whose code is fetched once (unrolled it was 130
         // KB, and a tile's end took 23 us with codes, 11 with values, against ...).
-        float* const own_u = own + NW * MR * kPitch;
-        constexpr int kTurns = MR / kRows;
+        float* const own_u = own + NW * 16 * kPitch;
+        constexpr int kTurns = 16 / kRows;
         auto codes_out = [&](int m, const f4& v, const Divisor& d, int64_t row, int64_t col) __attribute__((always_inline)) {
             const uint32_t c = codes4(v, [&](int) { return d[0]; }, [&](int) { return d; });
             uint8_t* const to = static_cast<uint8_t*>(p.saved[m]) + row * p.ld_saved[m] + col;
@@ -574,13 +514,11 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
                 for (int k = 0; k < TI; ++k) {
                     if (__builtin_amdgcn_readfirstlane(i) != k) continue;   // (k stays a constant)
 #pragma unroll
-                    for (int j = 0; j < PJ; ++j)
-#pragma unroll
-                        for (int q = 0; q < kQuads; ++q) {
-                            const int to = n16 * kPitch + MR * j + kApart * q + 4 * g;
-                            *reinterpret_cast<f4*>(own + to) = acc[k][j].quad(q);
-                            *reinterpret_cast<f4*>(own_u + to) = acc[k][PJ + j % PJ].quad(q);
-                        }
+                    for (int j = 0; j < PJ; ++j) {
+                        const int to = n16 * kPitch + 16 * j + 4 * g;
+                        *reinterpret_cast<f4*>(own + to) = acc[k][j];
+                        *reinterpret_cast<f4*>(own_u + to) = acc[k][PJ + j % PJ];
+                    }
                 }
                 settle();
                 f4 vg[kTurns], vu[kTurns];
@@ -592,7 +530,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
                 const int64_t col = n0 + wj + ec;
 #pragma unroll
                 for (int r = 0; r < kTurns; ++r) {
-                    const int in = wi + MR * i + r * kRows + er;
+                    const int in = wi + 16 * i + r * kRows + er;
                     const int64_t row = m0 + in;
                     if (row >= p.M || col >= p.N) continue;
                     f4 h;
@@ -620,7 +558,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     } else {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-            by_rows(i, [&](int j, int q) { return acc[i][j].quad(q); },
+            by_rows(i, [&](int j) { return acc[i][j]; },
                     [&](int64_t row, int64_t col, f4 v) {
                         if (OP == GATED_DW && p.beta != 0.f) {
                             const uint8_t* c = static_cast<const uint8_t*>(p.C[which]) +
@@ -636,14 +574,14 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     }
 }
 
-template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS, bool PIPE = false, int MR = 16>
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN);
     constexpr int kCols = OP == GATED_FORWARD ? BN / 2 : BN;
     const int64_t tiles = ((p.M + BM - 1) / BM) * (int64_t)((p.N + kCols - 1) / kCols) *
                           (OP == GATED_DW ? 2 : 1);
     const dim3 grid((unsigned)tiles, (unsigned)p.splits);
-    hipLaunchKernelGGL((gated_tile_kernel<OP, BF16, BM, BN, WM, WN, KB, NS, PIPE, MR>), grid, dim3(threads), 0,
+    hipLaunchKernelGGL((gated_tile_kernel<OP, BF16, BM, BN, WM, WN, KB, NS>), grid, dim3(threads), 0,
                        stream, p);
     return hipGetLastError();
 }
@@ -653,14 +591,15 @@ hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
 template <int OP, bool BF16>
 __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;
-    const int nb = (p.N + 127) / 128, all = p.M * (OP == GATED_DW ? 2 : 1);
+    const int nb = (p.N + 127) / 128;
+    const int64_t all = (int64_t)p.M * (OP == GATED_DW ? 2 : 1);
     const int64_t slice = (int64_t)p.M * p.N;
     constexpr int kEach = OP == GATED_DX ? 1 : 2;
     const int l = threadIdx.x & 31, block = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (block >= nb) return;
     const int64_t col = (int64_t)block * 128 + 4 * l;
     const int n = p.N - col < 4 ? (int)(p.N - col) : 4;   // (may be below 1)
-    for (int v = blockIdx.y; v < all; v += gridDim.y) {
+    for (int64_t v = blockIdx.y; v < all; v += gridDim.y) {
         const int which = OP == GATED_DW && v >= p.M ? 1 : 0;
         const int64_t row = v - (which ? p.M : 0);
         auto sum = [&](int m) {
@@ -738,7 +677,7 @@ __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
 }
 
 // The tiles, with what one costs by estimate: the start and end of a round, and a step
-// of 64 bytes of k for a workgroup alone on its CU and for as many as fit. From times
+// for a workgroup alone on its CU and for as many as fit. From times
 // of 1 to 1024 workgroups of 16 and 64 steps (128 and 32 for binary32).
 constexpr GatedShape kForwardBf16[] = {
     {256, 128, 64, 1, 10.2f, 0.78f, 0.78f},
@@ -786,34 +725,34 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
                              hipStream_t stream) {
     if (op == GATED_FORWARD && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 128, 64, 3, true>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
-            case 3: return launch_tile<GATED_FORWARD, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
-            case 4: return launch_tile<GATED_FORWARD, true, 32, 64, 16, 32, 128, 6, true>(p, stream);
+            case 0: return launch_tile<GATED_FORWARD, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, true, 128, 256, 64, 128, 64, 3>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, true, 64, 128, 32, 64, 128, 3>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, true, 64, 64, 32, 32, 128, 4>(p, stream);
+            case 4: return launch_tile<GATED_FORWARD, true, 32, 64, 16, 32, 128, 6>(p, stream);
         }
     } else if (op == GATED_FORWARD) {
         switch (shape) {
-            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 128, 3, true>(p, stream);
-            case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 32, 128, 3, true>(p, stream);
-            case 3: return launch_tile<GATED_FORWARD, false, 64, 64, 32, 32, 128, 4, true>(p, stream);
-            case 4: return launch_tile<GATED_FORWARD, false, 32, 64, 16, 32, 128, 6, true>(p, stream);
+            case 0: return launch_tile<GATED_FORWARD, false, 128, 256, 64, 64, 128, 3>(p, stream);
+            case 1: return launch_tile<GATED_FORWARD, false, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_FORWARD, false, 64, 128, 32, 32, 128, 3>(p, stream);
+            case 3: return launch_tile<GATED_FORWARD, false, 64, 64, 32, 32, 128, 4>(p, stream);
+            case 4: return launch_tile<GATED_FORWARD, false, 32, 64, 16, 32, 128, 6>(p, stream);
         }
     } else if (op == GATED_DX && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
-            case 3: return launch_tile<GATED_DX, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
-            case 4: return launch_tile<GATED_DX, true, 32, 64, 16, 32, 128, 6, true>(p, stream);
+            case 0: return launch_tile<GATED_DX, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 3>(p, stream);
+            case 3: return launch_tile<GATED_DX, true, 64, 64, 32, 32, 128, 4>(p, stream);
+            case 4: return launch_tile<GATED_DX, true, 32, 64, 16, 32, 128, 6>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {
-            case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4, true>(p, stream);
-            case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 64, 4, true>(p, stream);
-            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 3, true>(p, stream);
-            case 3: return launch_tile<GATED_DW, true, 64, 64, 32, 32, 128, 4, true>(p, stream);
+            case 0: return launch_tile<GATED_DW, true, 256, 256, 64, 128, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_DW, true, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 3>(p, stream);
+            case 3: return launch_tile<GATED_DW, true, 64, 64, 32, 32, 128, 4>(p, stream);
         }
     }
     return hipErrorInvalidValue;
