@@ -1,7 +1,7 @@
-// Launchers of the few-row kernels (few_rows.h), one translation unit per kind of
+// Launchers of the few-row kernels (few_rows.h, few_int4.h), one translation unit per kind of
 // weights, type of x and number of matrices (-DFG_ROWS_INT4, -DFG_ROWS_BF16,
 // -DFG_ROWS_MATRICES), so that they compile side by side.
-#include "few_rows.h"
+#include "few_int4.h"
 
 namespace fg {
 
@@ -13,7 +13,7 @@ hipError_t FG_ROWS_NAME(FG_ROWS_INT4, FG_ROWS_BF16, FG_ROWS_MATRICES)(const Rows
 #if FG_ROWS_INT4
     return launch_int4<FG_ROWS_BF16 != 0, FG_ROWS_MATRICES>(p, stream);
 #else
-    return launch_ct<Kind<FG_ROWS_BF16 ? W_BF16 : W_F32>, FG_ROWS_BF16 != 0, FG_ROWS_MATRICES>(p, stream);
+    return p.T <= 4 ? launch<FG_ROWS_BF16 != 0, 1>(p, stream) : launch<FG_ROWS_BF16 != 0, 4>(p, stream);
 #endif
 }
 

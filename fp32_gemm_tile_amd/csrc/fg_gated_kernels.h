@@ -35,7 +35,6 @@ struct RowsParams {
     RowsWeights w[2];
     void* out;
     int64_t ldo;
-    int32_t x_units;       // 4-bit codes, few rows: units of x kept in LDS at a time
     void* save[2];         // both products in x's type, or null
     int64_t ld_save[2];
 };

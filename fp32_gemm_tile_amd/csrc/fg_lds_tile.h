@@ -45,6 +45,27 @@ __device__ __forceinline__ void dma4(i4v r, uint32_t lds, uint32_t off) {
 #endif
 }
 
+// One element of SIZE bytes per lane, with zeros above it, to lds + 4 l.
+template <int SIZE>
+__device__ __forceinline__ void dma_element(i4v r, uint32_t lds, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (SIZE == 4)
+        dma4(r, lds, off);
+    else if constexpr (SIZE == 2)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, 0 offen lds"
+                     :
+                     : "s"(lds), "v"(off), "s"(r)
+                     : "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
+                     :
+                     : "s"(lds), "v"(off), "s"(r)
+                     : "m0");
+#else
+    (void)r, (void)lds, (void)off;
+#endif
+}
+
 // Workgroup id -> output tile. Consecutive ids go to the 8 XCDs in turn; XCD x
 // gets the x-th contiguous part of the tiles, numbered in bands of kBand tile
 // rows, column by column inside a band, so the tiles that run together on one
