@@ -69,8 +69,7 @@ struct Forced {
 Forced g_forced[3][2];
 
 bool known_product(int op, int type) {
-    return op >= fg::GATED_FORWARD && op <= fg::GATED_DW &&
-           (type == FG_TYPE_BF16 || (type == FG_TYPE_F32 && op == fg::GATED_FORWARD));
+    return op >= fg::GATED_FORWARD && op <= fg::GATED_DW && (type == FG_TYPE_BF16 || type == FG_TYPE_F32);
 }
 
 struct Plan {
@@ -111,7 +110,7 @@ Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) 
                                  (op == fg::GATED_DW ? 2 : 1);
             if (tiles >= kMaxTiles) continue;
             const int64_t steps = cdiv(z.K * (bf16 ? 2 : 4), sh.kb) * z.terms;
-            for (int64_t n = 1; n <= 16; n *= 2) {
+            for (const int64_t n : {1, 2, 3, 4, 6, 8, 12, 16}) {
                 const int64_t per = cdiv(steps, n), used = cdiv(steps, per);
                 if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
                 if (n == 1 && codes && sh.bn % 128) continue;
@@ -310,9 +309,10 @@ size_t fg_gated_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t 
                                         int32_t type) {
     if (!sizes_ok(tokens, hidden, inner)) return 0;
     size_t n = fg_gated_backward_min_workspace_size(tokens, inner, type);
-    if (n > 0 && type == FG_TYPE_BF16 && hidden > 0)
-        n += std::max(partial_bytes(fg::GATED_DX, true, tokens, hidden, inner),
-                      partial_bytes(fg::GATED_DW, true, tokens, hidden, inner));
+    const bool bf16 = type == FG_TYPE_BF16;
+    if (n > 0 && hidden > 0)
+        n += std::max(partial_bytes(fg::GATED_DX, bf16, tokens, hidden, inner),
+                      partial_bytes(fg::GATED_DW, bf16, tokens, hidden, inner));
     return n;
 }
 
@@ -432,23 +432,6 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
         st = launched(fg::launch_gated_grad(bf16, p, stream), "activation's gradient kernel");
         if (st != FG_OK) return st;
     }
-    if (!bf16) {
-        auto product = [&](fg_op op, int64_t M, int64_t K, const void* A, int64_t lda, const void* B,
-                           int64_t ldb, float beta, void* C, int64_t ldc) {
-            return fg_sgemm(op, FG_OP_N, M, H, K, 1.f, static_cast<const float*>(A), lda,
-                            static_cast<const float*>(B), ldb, beta, static_cast<float*>(C), ldc, stream);
-        };
-        if (want_dx) {
-            st = product(FG_OP_N, T, I, dg, ldd, b.gate, b.ldgate, 0.f, d.dx, d.lddx);
-            if (st == FG_OK && I > 0) st = product(FG_OP_N, T, I, du, ldd, b.up, b.ldup, 1.f, d.dx, d.lddx);
-            if (st != FG_OK) return st;
-        }
-        if (want_dw) {
-            st = product(FG_OP_T, I, T, dg, ldd, b.x, b.ldx, d.beta, d.dgate, d.lddgate);
-            if (st == FG_OK) st = product(FG_OP_T, I, T, du, ldd, b.x, b.ldx, d.beta, d.dup, d.lddup);
-        }
-        return st;
-    }
     void* const more = ws ? ws + 2 * each : nullptr;
     const size_t more_bytes = workspace_bytes - 2 * each;
     fg::GatedTileParams p;
@@ -463,7 +446,7 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
         p.ldb[1] = b.ldup;
         p.C[0] = d.dx;
         p.ldc[0] = d.lddx;
-        st = run_tiles(fg::GATED_DX, true, false, sizes_of(fg::GATED_DX, T, H, I), p, more,
+        st = run_tiles(fg::GATED_DX, bf16, false, sizes_of(fg::GATED_DX, T, H, I), p, more,
                        more_bytes, stream);
         if (st != FG_OK) return st;
     }
@@ -479,7 +462,7 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
         p.ldc[0] = d.lddgate;
         p.ldc[1] = d.lddup;
         p.beta = d.beta;
-        st = run_tiles(fg::GATED_DW, true, false, sizes_of(fg::GATED_DW, T, H, I), p, more,
+        st = run_tiles(fg::GATED_DW, bf16, false, sizes_of(fg::GATED_DW, T, H, I), p, more,
                        more_bytes, stream);
     }
     return st;

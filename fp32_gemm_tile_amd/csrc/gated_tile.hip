@@ -91,16 +91,17 @@ struct Tile {
     static constexpr int kRowBytes = ALONG_K ? KB : R * kSize;  // of a row in LDS
     static constexpr int kLanesPerRow = kRowBytes / 16;
     static constexpr int kRowsPerLoad = 64 / kLanesPerRow;
-    static_assert(ALONG_K || (BF16 && R >= 64), "only 16-bit elements are transposed");
+    static_assert(ALONG_K || R >= 64, "a row's chunks have 8 places or 16 to exchange");
 
     // Exchange of the 16-byte chunks of LDS row r: chunk c is at position c ^ turn(r).
     // ALONG_K: a 128-bit read of 16 rows (the 16 lanes that are served together are not
     // neighbours) covers all banks evenly; found by trying, 4 cycles a read, and 8 with
     // (r >> 2) & 3 for 64-byte rows.
-    // Else the eight rows that 32 lanes read together do.
+    // Else the eight rows that 32 lanes read together do, or the four of 64 lanes.
     static __device__ __forceinline__ int turn(int r) {
         if constexpr (ALONG_K && KB == 128) return (r >> 1) & 7;
         else if constexpr (ALONG_K) return (r >> 2) & 2;
+        else if constexpr (!BF16) return 4 * ((r >> 2) & 3);
         else if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
         else return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
     }
@@ -119,6 +120,15 @@ struct Tile {
         if constexpr (ALONG_K) {
             return *reinterpret_cast<const i4v*>(tile + (r0 + n) * KB +
                                                  (((4 * sub + g) ^ turn(n)) << 4));
+        } else if constexpr (!BF16) {
+            i4v v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 4 * g + e;
+                v[e] = *reinterpret_cast<const int*>(tile + (16 * sub + k) * kRowBytes +
+                                                     (((r0 / 4 + (n >> 2)) ^ turn(k)) << 4) + 4 * (n & 3));
+            }
+            return v;
         } else {
             const int i = lane & 15, k = 8 * g + (i >> 2);
             const int c = r0 / 8 + ((i >> 1) & 1);
@@ -368,7 +378,8 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
         for (int u = 0; u < kSubs; ++u)
 #pragma unroll
             for (int i = u == 0 ? 1 : 0; i < TI; ++i) row(now, u, i);
-        constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? 2 : 1) + TJ * (kDual ? 1 : 2));
+        constexpr int kEach = BF16 ? 2 : 4;   // of an operand stored across k
+        constexpr int kReads = kSubs * (TI * (OP == GATED_DW ? kEach : 1) + TJ * (kDual ? 1 : kEach));
         constexpr int kLeft = kSubs * TI * TJ - TJ;
         constexpr int kGroups = kReads < kLeft ? kReads : kLeft;
 #pragma unroll
@@ -693,33 +704,48 @@ constexpr GatedShape kForwardF32[] = {
     {64, 32, 128, 2, 4.0f, 0.59f, 1.03f},
     {32, 32, 128, 2, 3.7f, 0.36f, 0.59f},
 };
-constexpr GatedShape kDx[] = {
+constexpr GatedShape kDxBf16[] = {
     {256, 256, 64, 1, 8.0f, 0.81f, 0.81f},
     {128, 128, 64, 2, 5.5f, 0.38f, 0.52f},
     {64, 128, 128, 2, 5.0f, 0.46f, 0.65f},
     {64, 64, 128, 2, 5.5f, 0.27f, 0.47f},
     {32, 64, 128, 2, 5.5f, 0.17f, 0.36f},
 };
-constexpr GatedShape kDw[] = {
+constexpr GatedShape kDwBf16[] = {
     {256, 256, 64, 1, 9.0f, 0.76f, 0.76f},
     {128, 128, 64, 2, 5.5f, 0.33f, 0.46f},
     {64, 128, 128, 2, 5.5f, 0.37f, 0.67f},
     {64, 64, 128, 2, 6.5f, 0.18f, 0.46f},
 };
+constexpr GatedShape kDxF32[] = {
+    {128, 128, 64, 2, 8.0f, 1.13f, 1.90f},
+    {64, 128, 128, 2, 5.5f, 1.21f, 2.00f},
+    {64, 64, 128, 2, 4.5f, 0.74f, 1.16f},
+    {32, 64, 128, 2, 4.0f, 0.50f, 0.66f},
+};
+constexpr GatedShape kDwF32[] = {
+    {128, 256, 128, 1, 13.5f, 3.68f, 3.68f},
+    {128, 128, 64, 2, 8.0f, 1.09f, 1.95f},
+    {64, 128, 128, 2, 5.5f, 1.18f, 2.08f},
+    {64, 64, 128, 2, 4.5f, 0.72f, 1.16f},
+};
+
+struct Shapes {
+    const GatedShape* list;
+    int n;
+};
+template <int N>
+constexpr Shapes all_of(const GatedShape (&list)[N]) {
+    return {list, N};
+}
+constexpr Shapes kShapes[3][2] = {{all_of(kForwardF32), all_of(kForwardBf16)},
+                                  {all_of(kDxF32), all_of(kDxBf16)},
+                                  {all_of(kDwF32), all_of(kDwBf16)}};
 
 }  // namespace
 
-int gated_num_shapes(int op, bool bf16) {
-    if (op == GATED_FORWARD)
-        return bf16 ? (int)(sizeof kForwardBf16 / sizeof kForwardBf16[0])
-                    : (int)(sizeof kForwardF32 / sizeof kForwardF32[0]);
-    if (!bf16) return 0;
-    return op == GATED_DX ? (int)(sizeof kDx / sizeof kDx[0]) : (int)(sizeof kDw / sizeof kDw[0]);
-}
-GatedShape gated_shape(int op, bool bf16, int shape) {
-    if (op == GATED_FORWARD) return bf16 ? kForwardBf16[shape] : kForwardF32[shape];
-    return op == GATED_DX ? kDx[shape] : kDw[shape];
-}
+int gated_num_shapes(int op, bool bf16) { return kShapes[op][bf16].n; }
+GatedShape gated_shape(int op, bool bf16, int shape) { return kShapes[op][bf16].list[shape]; }
 
 hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
                              hipStream_t stream) {
@@ -754,6 +780,20 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
             case 2: return launch_tile<GATED_DW, true, 64, 128, 32, 64, 128, 3>(p, stream);
             case 3: return launch_tile<GATED_DW, true, 64, 64, 32, 32, 128, 4>(p, stream);
         }
+    } else if (op == GATED_DX) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_DX, false, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 1: return launch_tile<GATED_DX, false, 64, 128, 32, 32, 128, 3>(p, stream);
+            case 2: return launch_tile<GATED_DX, false, 64, 64, 32, 32, 128, 4>(p, stream);
+            case 3: return launch_tile<GATED_DX, false, 32, 64, 16, 32, 128, 6>(p, stream);
+        }
+    } else if (op == GATED_DW) {
+        switch (shape) {
+            case 0: return launch_tile<GATED_DW, false, 128, 256, 64, 64, 128, 3>(p, stream);
+            case 1: return launch_tile<GATED_DW, false, 128, 128, 64, 64, 64, 4>(p, stream);
+            case 2: return launch_tile<GATED_DW, false, 64, 128, 32, 32, 128, 3>(p, stream);
+            case 3: return launch_tile<GATED_DW, false, 64, 64, 32, 32, 128, 4>(p, stream);
+        }
     }
     return hipErrorInvalidValue;
 }
@@ -763,8 +803,10 @@ hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipS
     const dim3 grid((unsigned)((((int64_t)p.N + 127) / 128 + 7) / 8), (unsigned)(rows < 65535 ? rows : 65535));
     auto kernel = op == GATED_FORWARD ? (bf16 ? gated_finish_kernel<GATED_FORWARD, true>
                                               : gated_finish_kernel<GATED_FORWARD, false>)
-                : op == GATED_DX      ? gated_finish_kernel<GATED_DX, true>
-                                      : gated_finish_kernel<GATED_DW, true>;
+                : op == GATED_DX ? (bf16 ? gated_finish_kernel<GATED_DX, true>
+                                         : gated_finish_kernel<GATED_DX, false>)
+                                 : (bf16 ? gated_finish_kernel<GATED_DW, true>
+                                         : gated_finish_kernel<GATED_DW, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
     return hipGetLastError();
 }

@@ -169,9 +169,8 @@ fg_status fg_set_fp8_tile(int32_t tile);
 
 /*
  * Tiles of the products of fg_gated and fg_gated_backward (fp32gemm_gated.h).
- * product (argument 1): 0 the forward product, and with bfloat16 only 1 dx and 2
- * dgate and dup (binary32 gradients run fg_sgemm); type (2): FG_TYPE_F32 (0) or
- * FG_TYPE_BF16 (1). fg_gated_num_tiles: how many tiles there are (0 for another
+ * product (argument 1): 0 the forward product, 1 dx and 2 dgate and dup; type (2):
+ * FG_TYPE_F32 (0) or FG_TYPE_BF16 (1). fg_gated_num_tiles: how many tiles there are (0 for another
  * product or type). fg_gated_tile: rows (4) and columns (5) of the result of one
  * workgroup of tile `tile` (3). fg_select_gated: the tile (7) and the slices of the sum
  * (8) that a call with T, H and I (3 to 5, positive) and workspace_bytes (6)

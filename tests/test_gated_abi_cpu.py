@@ -115,21 +115,21 @@ assert int4() in NO_DEVICE and gated4() in NO_DEVICE and int4(K=0, x=0) in NO_DE
 
 
 def test_tile_hooks():
-    for product, ty, some in ((0, 0, True), (0, 1, True), (1, 1, True), (2, 1, True), (1, 0, False),
+    for product, ty, some in ((0, 0, True), (0, 1, True), (1, 1, True), (2, 1, True), (1, 0, True), (2, 0, True),
                               (3, 1, False), (0, 2, False)):
         assert (len(fg.fg_gated_tiles(product, ty)) > 0) == some
     r, c, lib = ctypes.c_int32(), ctypes.c_int32(), fg.load_library()
     ref = ctypes.byref
-    for args, bad in (((3, 1, 0, ref(r), ref(c)), 1), ((1, 0, 0, ref(r), ref(c)), 2),
+    for args, bad in (((3, 1, 0, ref(r), ref(c)), 1), ((1, 2, 0, ref(r), ref(c)), 2),
                       ((0, 1, 99, ref(r), ref(c)), 3), ((0, 1, 0, None, ref(c)), 4),
                       ((0, 1, 0, ref(r), None), 5)):
         assert lib.fg_gated_tile(*args) == fg.FG_ERR_INVALID_ARG and fg.fg_last_bad_arg() == bad
-    for args, bad in (((-1, 1, 1, 1, 1), 1), ((2, 0, 1, 1, 1), 2), ((0, 1, 0, 1, 1), 3),
+    for args, bad in (((-1, 1, 1, 1, 1), 1), ((2, 2, 1, 1, 1), 2), ((0, 1, 0, 1, 1), 3),
                       ((0, 1, 1, 0, 1), 4), ((0, 1, 1, 1, 0), 5)):
         with pytest.raises(fg.FgError) as e:
             fg.fg_select_gated(*args)
         assert e.value.bad_arg == bad
-    for args, bad in (((3, 1, 0, 1), 1), ((1, 0, 0, 1), 2), ((0, 1, 99, 1), 3), ((0, 1, -2, 1), 3),
+    for args, bad in (((3, 1, 0, 1), 1), ((1, 2, 0, 1), 2), ((0, 1, 99, 1), 3), ((0, 1, -2, 1), 3),
                       ((0, 1, 0, 17), 4), ((0, 1, 0, -1), 4)):
         assert fg.fg_set_gated_tile(*args) == fg.FG_ERR_INVALID_ARG and fg.fg_last_bad_arg() == bad
     assert fg.fg_select_gated(0, 1, 4, 4096, 4096) == (-1, 1)
@@ -144,7 +144,7 @@ def test_tile_hooks():
 
 def test_every_tile_is_chosen_somewhere():
     """No tile that no size would choose."""
-    for product, ty in ((0, 0), (0, 1), (1, 1), (2, 1)):
+    for product, ty in ((0, 0), (0, 1), (1, 0), (1, 1), (2, 0), (2, 1)):
         chosen = set()
         for T in (1, 65, 100, 130, 200, 300, 517, 1025, 2048, 4096, 8192):
             for H in (64, 300, 1024, 2048, 4096, 8192):

@@ -232,16 +232,18 @@ def test_backward_every_activation_and_part(ty):
         c.backward("e4m3", "silu", 0.0, parts=parts)
 
 
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
 @pytest.mark.parametrize("product", [1, 2])
-def test_backward_every_tile(product):
-    c = Case(150, 330, 300, "bf16", seed=8)
+def test_backward_every_tile(product, ty):
+    code = int(ty == "bf16")
+    c = Case(150, 330, 300, ty, seed=8)
     try:
-        for tile, slices in itertools.product(range(len(fg.fg_gated_tiles(product, 1))), (1, 2, 4)):
-            assert fg.fg_set_gated_tile(product, 1, tile, slices) == fg.FG_OK
+        for tile, slices in itertools.product(range(len(fg.fg_gated_tiles(product, code))), (1, 2, 3, 4)):
+            assert fg.fg_set_gated_tile(product, code, tile, slices) == fg.FG_OK
             c.backward("same", "silu", 0.0)
             c.backward("e4m3", "gelu", -1.5)
     finally:
-        fg.fg_set_gated_tile(product, 1)
+        fg.fg_set_gated_tile(product, code)
 
 
 @pytest.mark.parametrize("ty", ["f32", "bf16"])
@@ -256,12 +258,12 @@ def test_gate_and_up_of_different_strides(ty):
         code = int(ty == "bf16")
         try:
             for tile, slices in ((-1, 0), (0, 2), (1, 1), (2, 4)):
-                for product in (0, 1) if code else (0,):
+                for product in (0, 1):
                     fg.fg_set_gated_tile(product, code, tile, slices)
                 c.forward("same")
                 c.backward("same", parts=("dx",))
         finally:
-            for product in (0, 1) if code else (0,):
+            for product in (0, 1):
                 fg.fg_set_gated_tile(product, code)
 
 
