@@ -13,7 +13,7 @@ hipError_t FG_ROWS_NAME(FG_ROWS_INT4, FG_ROWS_BF16, FG_ROWS_MATRICES)(const Rows
 #if FG_ROWS_INT4
     return launch_int4<FG_ROWS_BF16 != 0, FG_ROWS_MATRICES>(p, stream);
 #else
-    return p.T <= 4 ? launch<FG_ROWS_BF16 != 0, 1>(p, stream) : launch<FG_ROWS_BF16 != 0, 4>(p, stream);
+    return launch<FG_ROWS_BF16 != 0>(p, stream);
 #endif
 }
 

@@ -39,8 +39,8 @@ struct RowsParams {
     int64_t ld_save[2];
 };
 // Rows of x beside weights of its type. More of them, or one tile of 32 rows: 4096 x 8192
-// in bfloat16, 16 rows 33 us here and 30 in a tile, 17 rows 51 and 30; 2048 x 1408 10 and 9,
-// 16 and 9; binary32 17 and 26, 29 and 26.
+// in bfloat16, 16 rows 33 us here and 30 in a tile, 17 rows 51 and 30; 2048 x 1408 7 and 9,
+// 16 and 9; binary32 11 and 26, 29 and 26.
 constexpr int kRowsMaxTokens = 16;
 constexpr int kInt4MaxRows = 64;   // FG_INT4_MAX_ROWS
 // launch_rows_<4-bit><bfloat16 x><matrices>, each a translation unit of few_rows.hip
