@@ -54,7 +54,8 @@ typedef struct fg_int4 {
  * Products with the codes are exact and sums binary32 for either type; the sum over a
  * group is taken of q x and of x, and its part of the result is s (sum q x - z sum x).
  * (Where that is not finite the group is summed again from (q - z) x.) Scales are
- * finite, and 0 or of a magnitude between 2^-100 and 2^100. T == 0 or N == 0: FG_OK,
+ * finite, and 0 or of a magnitude between 2^-100 and 2^100; scales and zero points of a
+ * matrix reach over less than 2 GiB each (else FG_ERR_UNSUPPORTED). T == 0 or N == 0: FG_OK,
  * nothing enqueued. K == 0: zeros. Repeated calls give identical bits. No workspace.
  */
 fg_status fg_gemm_int4(int64_t T, int64_t N, int64_t K, int32_t group, fg_type type,

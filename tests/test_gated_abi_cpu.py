@@ -200,6 +200,11 @@ def test_int4_limits_and_quick_returns():
     assert int4(T=0, x=0, out=0) == fg.FG_OK and int4(N=0, w=weights(q=0, s=0), out=0) == fg.FG_OK
     assert int4(ldx=BIG) == fg.FG_ERR_UNSUPPORTED and int4(w=weights(ldq=BIG)) == fg.FG_ERR_UNSUPPORTED
     assert int4(ldo=BIG) == fg.FG_ERR_UNSUPPORTED
+    # scales and zero points of 2 GiB: one group and two, 4 bytes, 2 and 1
+    for K, st, lds, ldz in ((16, 0, 1 << 29, 0), (64, 0, 1 << 28, 0), (16, 1, 1 << 30, 0),
+                            (64, 0, 8, 1 << 30)):
+        w = weights(s=16, lds=lds, z=16 if ldz else 0, ldz=ldz, ldq=32)
+        assert int4(K=K, ldx=64, st=st, w=w) == fg.FG_ERR_UNSUPPORTED and fg.fg_last_bad_arg() == 9
 
 
 def test_new_headers_declare_what_the_library_exports():

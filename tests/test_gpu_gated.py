@@ -268,6 +268,70 @@ def test_gate_and_up_of_different_strides(ty):
 
 
 @pytest.mark.parametrize("ty", ["f32", "bf16"])
+def test_as_many_rows_of_weights_as_change_the_kernel(ty):
+    for T, I in ((3, 2500), (9, 2500), (16, 4100), (17, 2500)):
+        c = Case(T, 70, I, ty, seed=I, extra=1)
+        c.forward("same")
+        c.forward("none", "gelu", ws=0)
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [4, 12, 40, 150])
+def test_a_token_touches_its_own_row_only(ty, T):
+    """Infinities and NaN in two tokens: the other rows' bits are what they were."""
+    import torch
+    c = Case(T, 130, 300, ty, seed=T)
+    bad = [1, T - 1]
+    good = [t for t in range(T) if t not in bad]
+
+    def run():
+        h, g, u = (torch.empty(T, 300, dtype=c.x.dtype, device="cuda") for _ in range(3))
+        fg.gated(c.x, c.gate, c.up, h, saved=(g, u), workspace=c.workspace(1 << 20))
+        dx = torch.empty(T, 130, dtype=c.x.dtype, device="cuda")
+        fg.gated_backward(h, c.x, c.gate, c.up, (g, u), dx=dx)
+        return h, g, u, dx
+
+    before = run()
+    c.x[1, 129] = float("inf")
+    c.x[T - 1, 0] = float("nan")
+    after = run()
+    for a, b in zip(before, after):
+        assert torch.equal(a[good], b[good])
+    for t in after[:3]:
+        assert torch.isnan(t[T - 1]).all()
+    assert not torch.isfinite(after[1][1]).any()
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+def test_long_rows(ty):
+    """Rows so far apart that offsets pass 32 bits: the bits of compact ones."""
+    import torch
+    T, H, I, far = 1100, 40, 48, 1 << 21
+    c = Case(T, H, I, ty, seed=3)
+
+    def apart(t):
+        out = torch.empty(t.shape[0], far, dtype=t.dtype, device="cuda")[:, :t.shape[1]]
+        out.copy_(t)
+        return out
+
+    def run(place):
+        x, gate, up = place(c.x), place(c.gate), place(c.up)
+        h, g, u = (place(torch.zeros(T, I, dtype=x.dtype, device="cuda")) for _ in range(3))
+        ws = c.workspace(1 << 24)
+        fg.gated(x, gate, up, h, saved=(g, u), workspace=ws)
+        few = place(torch.zeros(4, I, dtype=x.dtype, device="cuda"))
+        fg.gated(x[:4], gate, up, few)
+        dx = place(torch.zeros(T, H, dtype=x.dtype, device="cuda"))
+        dg, du = (place(torch.ones(I, H, dtype=x.dtype, device="cuda")) for _ in range(2))
+        fg.gated_backward(h, x, gate, up, (g, u), dx, dg, du, beta=0.5, workspace=ws)
+        return [t.contiguous() for t in (h, g, u, few, dx, dg, du)]
+
+    compact = run(lambda t: t)
+    for a, b in zip(compact, run(apart)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
 def test_empty_sizes(ty):
     import torch
     dt = dtype_of(ty)

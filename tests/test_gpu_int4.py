@@ -84,6 +84,33 @@ def test_strides_and_activations(ty):
     check(6, 3, 77, 32, ty, "bf16", True, False, pad=1)
 
 
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+def test_many_rows_of_weights(ty):
+    """As many rows of W as change how many of them a workgroup has."""
+    for T, N, K, gated in ((1, 8200, 130, False), (4, 8193, 100, False), (3, 4099, 260, False),
+                           (2, 8200, 70, True), (16, 8200, 40, False), (20, 8193, 33, True)):
+        check(T, N, K, 32, ty, "f32", True, gated)
+
+
+def test_long_rows():
+    """Rows so far apart that offsets pass 32 bits: the bits of compact ones."""
+    import torch
+    rng = np.random.default_rng(9)
+    N, K, group, far = 2100, 96, 32, 1 << 21
+    w = Weights(rng, N, K, group, "f32", True)
+    q = torch.empty(N, far, dtype=torch.uint8, device="cuda")[:, :K // 2]
+    q.copy_(w.t[0])
+    for T, ty in ((3, "bf16"), (16, "f32"), (64, "f32")):
+        x = aligned(rng.standard_normal((T, K)), ty)
+        xf = torch.empty(T, far, dtype=x.dtype, device="cuda")[:, :K]
+        xf.copy_(x)
+        out = torch.empty(T, N, dtype=x.dtype, device="cuda")
+        of = torch.empty(T, far, dtype=x.dtype, device="cuda")[:, :N]
+        fg.gemm_int4(x, w.t, out, group=group)
+        fg.gemm_int4(xf, (q, *w.t[1:]), of, group=group)
+        assert torch.equal(out, of)
+
+
 def test_every_code_times_one():
     """One column at a time: each code minus its zero point, exactly."""
     import torch
@@ -133,12 +160,39 @@ def test_infinities_nan_and_large_values():
         got = out.double().cpu().numpy()
         for t in range(T):
             fine = np.isfinite(y[t]) & (np.abs(y[t]) < 0.5 * top)
-            assert (np.abs(got[t] - y[t]) <= e[t])[fine].all(), t
+            with np.errstate(invalid="ignore"):
+                assert (np.abs(got[t] - y[t]) <= e[t])[fine].all(), t
             huge = np.isfinite(y[t]) & (np.abs(y[t]) > 2.0 * top)
             assert np.isinf(got[t][huge]).all()
             assert (np.isnan(got[t]) == np.isnan(y[t]))[~huge].all(), t
             inf = np.isinf(y[t])
             assert (got[t][inf] == y[t][inf]).all(), t
+
+
+@pytest.mark.parametrize("T", [2, 4, 16, 24, 50])
+def test_infinities_in_every_variant(T):
+    """The same where x has other numbers of rows: an infinity, two of them, a NaN."""
+    import torch
+    rng = np.random.default_rng(T)
+    N, K, group = 21, 290, 32
+    for ty in ("f32", "bf16"):
+        w = Weights(rng, N, K, group, "bf16", True)
+        x = rng.standard_normal((T, K))
+        special = [{4: np.inf}, {7: np.inf, 289: -np.inf}, {200: np.nan}, {288: -np.inf}]
+        for i, at in enumerate(special[:max(1, T // 2)]):
+            for col, v in at.items():
+                x[T - 1 - i, col] = v
+        x = aligned(x, ty)
+        out = torch.empty(T, N, dtype=dtype_of(ty), device="cuda")
+        fg.gemm_int4(x, w.t, out, group=group)
+        with np.errstate(invalid="ignore", over="ignore"):
+            y, e = og.int4_product(x.double().cpu().numpy(), w.v, w.most, ty == "bf16", group)
+        got = out.double().cpu().numpy()
+        fine = np.isfinite(y)
+        with np.errstate(invalid="ignore"):
+            assert (np.abs(got - y) <= e)[fine].all()
+        assert (np.isnan(got) == np.isnan(y)).all()
+        assert (got == y)[np.isinf(y)].all()
 
 
 def test_empty_sizes():
