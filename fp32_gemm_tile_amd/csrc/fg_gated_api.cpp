@@ -203,8 +203,10 @@ void fill_saved(const fg_gated_block& b, void* (&saved)[2], int64_t (&ld)[2]) {
     ld[1] = b.ldu;
 }
 
-// dG and dU: rows of a multiple of 64 elements.
-int64_t grad_ld(int64_t I) { return round_up(I, 64); }
+// dG and dU: rows of whole steps of any tile that reads them along their rows, with zeros
+// at their ends (what a step reads of the next row would meet zeros of gate and up, and may
+// be NaN).
+int64_t grad_ld(int64_t I) { return round_up(I, fg::kGradRow); }
 size_t grad_bytes(int64_t T, int64_t I, int type) {
     return (size_t)round_up(T * grad_ld(I) * type_size(type), 256);
 }
@@ -406,7 +408,7 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
 
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     void *dg = ws, *du = ws ? ws + each : nullptr;
-    const int64_t ldd = std::max<int64_t>(64, grad_ld(I));
+    const int64_t ldd = std::max<int64_t>(fg::kGradRow, grad_ld(I));
     if (want_grad) {
         fg::GatedGradParams p;
         memset(&p, 0, sizeof p);

@@ -69,6 +69,7 @@ inline hipError_t launch_rows(const RowsParams& p, hipStream_t stream) {
 //   DX       C[0] = A0 B0 + A1 B1; A (the gradients of G and U) T x I, B I x H
 //   DW       C[i] = Ai^T B0 + beta C[i]; A T x I, B0 (x) T x H
 enum : int32_t { GATED_FORWARD = 0, GATED_DX = 1, GATED_DW = 2 };
+constexpr int kGradRow = 128;   // rows of dG and dU are a multiple of it, and end with zeros
 struct GatedTileParams {
     const void* A[2];
     const void* B[2];
@@ -105,7 +106,7 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream);
 
 // Gradients of G and U from h's: du = dh * act(g), dg = dh * u * act'(g), both T x I
-// with rows of ld_d elements (a multiple of 64, zeros past I), and h = act(g) * u
+// with rows of ld_d elements (a multiple of kGradRow, zeros past I), and h = act(g) * u
 // (or null).
 struct GatedGradParams {
     int32_t T, I, act, save;   // SAVE_SAME or SAVE_E4M3

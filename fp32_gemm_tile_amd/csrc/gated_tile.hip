@@ -99,7 +99,8 @@ struct Tile {
     // (r >> 2) & 3 for 64-byte rows.
     // Else the eight rows that 32 lanes read together do, or the four of 64 lanes.
     static __device__ __forceinline__ int turn(int r) {
-        if constexpr (ALONG_K && KB == 128) return (r >> 1) & 7;
+        if constexpr (ALONG_K && KB == 256) return r & 15;
+        else if constexpr (ALONG_K && KB == 128) return (r >> 1) & 7;
         else if constexpr (ALONG_K) return (r >> 2) & 2;
         else if constexpr (!BF16) return 4 * ((r >> 2) & 3);
         else if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     };
     constexpr int kLoads = TA::kParts + TB::kParts;
     static_assert((NS - 1) * kLoads < 64, "loads left in flight must fit the vmcnt field");
+    static_assert(OP != GATED_DX || kGradRow % K1 == 0, "a step past K reads its own row's zeros");
     auto meet = [] {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * kLoads)
                      : "memory");
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
             }
         }
         // Row tile by row tile in one loop, whose code is fetched once (unrolled it was 130
-        // KB, and a tile's end took 23 us with codes, 11 with values, against ...).
+        // KB; 8192 tokens, 2048 x 8192 with codes, eight rounds of tiles: 597 us and 547).
         float* const own_u = own + NW * 16 * kPitch;
         constexpr int kTurns = 16 / kRows;
         auto codes_out = [&](int m, const f4& v, const Divisor& d, int64_t row, int64_t col) __attribute__((always_inline)) {
@@ -688,8 +690,8 @@ __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
 }
 
 // The tiles, with what one costs by estimate: the start and end of a round, and a step
-// for a workgroup alone on its CU and for as many as fit. From times
-// of 1 to 1024 workgroups of 16 and 64 steps (128 and 32 for binary32).
+// for a workgroup alone on its CU and for as many as fit, fitted to times of 8 to 1024
+// workgroups of 16 and 64 steps of 64 bytes (32 and 128 for binary32).
 constexpr GatedShape kForwardBf16[] = {
     {256, 128, 64, 1, 10.2f, 0.78f, 0.78f},
     {128, 128, 64, 2, 9.0f, 0.49f, 0.90f},
@@ -709,7 +711,7 @@ constexpr GatedShape kDxBf16[] = {
     {128, 128, 64, 2, 5.5f, 0.38f, 0.52f},
     {64, 128, 128, 2, 5.0f, 0.46f, 0.65f},
     {64, 64, 128, 2, 5.5f, 0.27f, 0.47f},
-    {32, 64, 128, 2, 5.5f, 0.17f, 0.36f},
+    {32, 64, 256, 1, 5.5f, 0.25f, 0.25f},
 };
 constexpr GatedShape kDwBf16[] = {
     {256, 256, 64, 1, 9.0f, 0.76f, 0.76f},
@@ -771,7 +773,7 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
             case 1: return launch_tile<GATED_DX, true, 128, 128, 64, 64, 64, 4>(p, stream);
             case 2: return launch_tile<GATED_DX, true, 64, 128, 32, 64, 128, 3>(p, stream);
             case 3: return launch_tile<GATED_DX, true, 64, 64, 32, 32, 128, 4>(p, stream);
-            case 4: return launch_tile<GATED_DX, true, 32, 64, 16, 32, 128, 6>(p, stream);
+            case 4: return launch_tile<GATED_DX, true, 32, 64, 16, 32, 256, 4>(p, stream);
         }
     } else if (op == GATED_DW && bf16) {
         switch (shape) {

@@ -70,7 +70,7 @@ def test_gated_workspaces_limits_and_quick_returns():
     assert fg.fg_gated_backward(block(save=0), grads(), 16, 1 << 20) == fg.FG_ERR_INVALID_ARG
     assert fg.fg_last_bad_arg() == 12
     need = fg.fg_gated_backward_min_workspace_size(3, 8, 0)
-    assert need == 2 * 3 * 64 * 4
+    assert need == 2 * 3 * 128 * 4
     for ws in (0, 24):
         assert fg.fg_gated_backward(block(save=1), grads(), ws, need) == fg.FG_ERR_INVALID_ARG
         assert fg.fg_last_bad_arg() == 32
