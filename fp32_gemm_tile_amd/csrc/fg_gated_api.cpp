@@ -211,21 +211,25 @@ size_t grad_bytes(int64_t T, int64_t I, int type) {
     return (size_t)round_up(T * grad_ld(I) * type_size(type), 256);
 }
 
-// One product of tiles, with its finish. p: everything but steps, slices and ws.
-fg_status run_tiles(int op, bool bf16, bool codes, const Sizes& z, fg::GatedTileParams& p,
-                    void* ws, size_t ws_bytes, hipStream_t stream) {
+void set_plan(const Sizes& z, const Plan& plan, fg::GatedTileParams& p) {
     p.M = (int32_t)z.M;
     p.N = (int32_t)z.N;
     p.K = (int32_t)z.K;
+    p.steps = (int32_t)plan.steps;
+    p.per_split = (int32_t)plan.per;
+    p.splits = (int32_t)plan.splits;
+}
+
+// One product of tiles, with its finish. p: everything but sizes, steps, slices and ws.
+fg_status run_tiles(int op, bool bf16, bool codes, const Sizes& z, fg::GatedTileParams& p,
+                    void* ws, size_t ws_bytes, hipStream_t stream) {
     if (z.K == 0) {   // empty sums
-        p.splits = 0;
+        set_plan(z, Plan{0, 0, 0, 0}, p);
         return launched(fg::launch_gated_finish(op, bf16, p, stream), "gated block kernel");
     }
     const Plan plan = plan_tiles(op, bf16, codes, z, ws ? ws_bytes : 0);
     if (plan.shape < 0) return fail(FG_ERR_UNSUPPORTED, 0, "2^23 or more output tiles");
-    p.steps = (int32_t)plan.steps;
-    p.per_split = (int32_t)plan.per;
-    p.splits = (int32_t)plan.splits;
+    set_plan(z, plan, p);
     p.ws = static_cast<float*>(ws);
     fg_status st = launched(fg::launch_gated_tile(op, bf16, plan.shape, p, stream), "gated block kernel");
     if (st == FG_OK && p.splits > 1)
@@ -436,37 +440,48 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
     }
     void* const more = ws ? ws + 2 * each : nullptr;
     const size_t more_bytes = workspace_bytes - 2 * each;
-    fg::GatedTileParams p;
-    if (want_dx) {
-        memset(&p, 0, sizeof p);
-        p.A[0] = dg;
-        p.A[1] = du;
-        p.lda = ldd;
-        p.B[0] = b.gate;
-        p.B[1] = b.up;
-        p.ldb[0] = b.ldgate;
-        p.ldb[1] = b.ldup;
-        p.C[0] = d.dx;
-        p.ldc[0] = d.lddx;
-        st = run_tiles(fg::GATED_DX, bf16, false, sizes_of(fg::GATED_DX, T, H, I), p, more,
-                       more_bytes, stream);
-        if (st != FG_OK) return st;
+    fg::GatedTileParams x, w;
+    memset(&x, 0, sizeof x);
+    x.A[0] = dg;
+    x.A[1] = du;
+    x.lda = ldd;
+    x.B[0] = b.gate;
+    x.B[1] = b.up;
+    x.ldb[0] = b.ldgate;
+    x.ldb[1] = b.ldup;
+    x.C[0] = d.dx;
+    x.ldc[0] = d.lddx;
+    memset(&w, 0, sizeof w);
+    w.A[0] = dg;
+    w.A[1] = du;
+    w.lda = ldd;
+    w.B[0] = b.x;
+    w.ldb[0] = b.ldx;
+    w.C[0] = d.dgate;
+    w.C[1] = d.dup;
+    w.ldc[0] = d.lddgate;
+    w.ldc[1] = d.lddup;
+    w.beta = d.beta;
+    const Sizes zx = sizes_of(fg::GATED_DX, T, H, I), zw = sizes_of(fg::GATED_DW, T, H, I);
+    // dx's smallest tiles beside dgate's and dup's, where those are of 128 x 128 and of one
+    // slice and dx has at most two to a CU: 200 tokens, 2048 x 1408 27.5 us together, 30.4
+    // apart; 1024 x 2816 26 and 34; 512 tokens, 2048 x 1408 37.6 and 39.6, 700 (704 tiles)
+    // 46.9 and 47.2.
+    const Forced& fx = g_forced[fg::GATED_DX][1];
+    const int only = fx.tile.load(), slices = fx.slices.load();
+    if (bf16 && want_dx && want_dw && I > 0 && (only < 0 || only == fg::kPairDx) && slices <= 1 &&
+        fg::gated_pair_tiles(zx.M, zx.N) <= 512) {
+        const Plan plan = plan_tiles(fg::GATED_DW, true, false, zw, more_bytes);
+        if (plan.shape == fg::kPairDw && plan.splits == 1) {
+            const int64_t steps = cdiv(zx.K * 2, fg::gated_shape(fg::GATED_DX, true, fg::kPairDx).kb) * zx.terms;
+            set_plan(zx, Plan{fg::kPairDx, steps, steps, 1}, x);
+            set_plan(zw, plan, w);
+            return launched(fg::launch_gated_pair(x, w, stream), "gated block's gradient kernel");
+        }
     }
-    if (want_dw && !(T == 0 && d.beta == 1.f)) {
-        memset(&p, 0, sizeof p);
-        p.A[0] = dg;
-        p.A[1] = du;
-        p.lda = ldd;
-        p.B[0] = b.x;
-        p.ldb[0] = b.ldx;
-        p.C[0] = d.dgate;
-        p.C[1] = d.dup;
-        p.ldc[0] = d.lddgate;
-        p.ldc[1] = d.lddup;
-        p.beta = d.beta;
-        st = run_tiles(fg::GATED_DW, bf16, false, sizes_of(fg::GATED_DW, T, H, I), p, more,
-                       more_bytes, stream);
-    }
+    if (want_dx) st = run_tiles(fg::GATED_DX, bf16, false, zx, x, more, more_bytes, stream);
+    if (st == FG_OK && want_dw && !(T == 0 && d.beta == 1.f))
+        st = run_tiles(fg::GATED_DW, bf16, false, zw, w, more, more_bytes, stream);
     return st;
 }
 

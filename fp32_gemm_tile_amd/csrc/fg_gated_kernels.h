@@ -102,6 +102,11 @@ int gated_num_shapes(int op, bool bf16);
 GatedShape gated_shape(int op, bool bf16, int shape);
 hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
                              hipStream_t stream);
+// dx in its smallest tile and dgate and dup in tile kPairDw, bfloat16, of one slice each, in
+// one launch: each alone is a chain of latencies on a part of the CUs. gated_pair_tiles: of dx.
+constexpr int kPairDx = 4, kPairDw = 1;
+int64_t gated_pair_tiles(int64_t M, int64_t N);
+hipError_t launch_gated_pair(const GatedTileParams& dx, const GatedTileParams& dw, hipStream_t stream);
 // What follows a launch with several slices.
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream);
 

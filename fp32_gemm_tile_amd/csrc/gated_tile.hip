@@ -196,8 +196,20 @@ struct Quad {
 
 // The operands of a step are in registers before it begins, those of the next are read
 // during it, and so a stage is free for its next load a step earlier.
+// A workgroup's LDS: the stages, or the results' way out (16 rows of every wave, of both
+// products, and what the codes of their rows are found with).
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kernel(GatedTileParams p) {
+constexpr int kLdsBytes = [] {
+    constexpr int NW = BM / WM * (BN / WN), kColumns = OP == GATED_FORWARD ? WN / 2 : WN;
+    constexpr int kStages = NS * (BM + BN) * KB, kRows = NW * 16 * (kColumns + 4) * 4;
+    constexpr int kOut = OP != GATED_FORWARD
+        ? kRows : 2 * kRows + 2 * (BN / WN) * BM * 4 + 2 * (BN / 2 / 128) * BM * 16;
+    return kStages > kOut ? kStages : kOut;
+}();
+
+// id: of n workgroups.
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+__device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds, int id, int n) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
     constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int SIZE = BF16 ? 2 : 4;
@@ -210,12 +222,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     using TB = Tile<BF16, OP == GATED_FORWARD, BN, KB, NW>;
     constexpr int kStage = TA::kBytes + TB::kBytes;
     constexpr int K1 = TA::kSteps;                   // k of a step
-    // (the results' way out: 16 rows of every wave, of both products, and what the
-    // codes of their rows are found with)
     constexpr int kPitch = kWaveCols + 4;
-    constexpr int kOut = kDual ? 2 * NW * 16 * kPitch * 4 + 2 * NWN * BM * 4 + 2 * (kCols / 128) * BM * 16
-                               : NW * 16 * kPitch * 4;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kOut ? NS * kStage : kOut];
 
     const int lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
     constexpr int kSubs = KB / 64;   // instructions along k in a step
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
     const int wi = (wave % NWM) * WM, wj = (wave / NWM) * kWaveCols;
     const int tiles_m = (p.M + BM - 1) / BM;
     int tm, tn;
-    tile_of(blockIdx.x, gridDim.x, OP == GATED_DW ? 2 * tiles_m : tiles_m,
+    tile_of(id, n, OP == GATED_DW ? 2 * tiles_m : tiles_m,
             (p.N + kCols - 1) / kCols, tm, tn);
     const int which = OP == GATED_DW && tm >= tiles_m ? 1 : 0;
     if (OP == GATED_DW && which) tm -= tiles_m;
@@ -588,6 +595,12 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kern
 }
 
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kernel(GatedTileParams p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes<OP, BF16, BM, BN, WM, WN, KB, NS>];
+    tile_body<OP, BF16, BM, BN, WM, WN, KB, NS>(p, lds, blockIdx.x, gridDim.x);
+}
+
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
     constexpr int threads = 64 * (BM / WM) * (BN / WN);
     constexpr int kCols = OP == GATED_FORWARD ? BN / 2 : BN;
@@ -598,6 +611,27 @@ hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
                        stream, p);
     return hipGetLastError();
 }
+
+// dx and dgate and dup in one launch.
+template <typename DX, typename DW>
+__global__ void __launch_bounds__(256, 2) gated_pair_kernel(GatedTileParams dx, GatedTileParams dw, int n) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[DX::kLds > DW::kLds ? DX::kLds : DW::kLds];
+    if ((int)blockIdx.x < n) DX::run(dx, lds, blockIdx.x, n);
+    else DW::run(dw, lds, blockIdx.x - n, gridDim.x - n);
+}
+template <int OP, int BM, int BN, int WM, int WN, int KB, int NS>
+struct Part {
+    static_assert(64 * (BM / WM) * (BN / WN) == 256, "threads of the launch");
+    static constexpr int kLds = kLdsBytes<OP, true, BM, BN, WM, WN, KB, NS>;
+    static __device__ __forceinline__ void run(const GatedTileParams& p, uint8_t* lds, int id, int n) {
+        tile_body<OP, true, BM, BN, WM, WN, KB, NS>(p, lds, id, n);
+    }
+    static int64_t tiles(int64_t M, int64_t N) {
+        return ((M + BM - 1) / BM) * ((N + BN - 1) / BN) * (OP == GATED_DW ? 2 : 1);
+    }
+};
+using PairDx = Part<GATED_DX, 32, 64, 16, 32, 256, 3>;
+using PairDw = Part<GATED_DW, 128, 128, 64, 64, 64, 4>;
 
 // Sums of the slices in ascending order, and what a launch with one slice does to
 // them: half a wave per 128 columns of a row, four columns per lane.
@@ -798,6 +832,15 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
         }
     }
     return hipErrorInvalidValue;
+}
+
+int64_t gated_pair_tiles(int64_t M, int64_t N) { return PairDx::tiles(M, N); }
+
+hipError_t launch_gated_pair(const GatedTileParams& dx, const GatedTileParams& dw, hipStream_t stream) {
+    const int64_t n = PairDx::tiles(dx.M, dx.N), all = n + PairDw::tiles(dw.M, dw.N);
+    hipLaunchKernelGGL((gated_pair_kernel<PairDx, PairDw>), dim3((unsigned)all), dim3(256), 0, stream, dx, dw,
+                       (int)n);
+    return hipGetLastError();
 }
 
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream) {
