@@ -75,6 +75,7 @@ bool known_product(int op, int type) {
 struct Plan {
     int shape;
     int64_t steps, per, splits;
+    double us;   // by estimate
 };
 
 // Rows and columns of the result, length of its sum, matrices of the result (times
@@ -89,19 +90,20 @@ Sizes sizes_of(int op, int64_t T, int64_t H, int64_t I) {
     return {I, H, T, 2, 1};
 }
 
+constexpr double kCUs = 256, kFinish = 4;                // us, of the kernel that joins slices
+constexpr double kPartial = 4e6;                         // bytes per us, of their sums
+constexpr int64_t kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+
 // The cheapest by estimate: rounds of as many workgroups as run together, the last of
 // which may have one to a CU; slices of the sum cost a kernel and their partial sums'
 // way to memory and back. codes: a block of 128 columns has to be in one workgroup,
 // or in the kernel that joins slices.
 Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) {
-    constexpr double kCUs = 256, kPartial = 4e6;  // bytes per us
-    constexpr double kFinish = 4;                 // us
     constexpr double kMaxTiles = 1 << 23;         // of 512 threads: a grid has fewer than 2^32
     Forced& forced = g_forced[op][bf16];
     const int only = forced.tile.load(), slices = forced.slices.load();
     const double slice = (double)z.M * (double)z.N * 4 * z.results;
-    Plan best{-1, 0, 0, 1};
-    double best_us = 0;
+    Plan best{-1, 0, 0, 1, 0};
     for (int pass = 0; pass < 2 && best.shape < 0; ++pass) {   // (1: the forced tile cannot)
         for (int s = 0; s < fg::gated_num_shapes(op, bf16); ++s) {
             const fg::GatedShape sh = fg::gated_shape(op, bf16, s);
@@ -110,7 +112,7 @@ Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) 
                                  (op == fg::GATED_DW ? 2 : 1);
             if (tiles >= kMaxTiles) continue;
             const int64_t steps = cdiv(z.K * (bf16 ? 2 : 4), sh.kb) * z.terms;
-            for (const int64_t n : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            for (const int64_t n : kSlices) {
                 const int64_t per = cdiv(steps, n), used = cdiv(steps, per);
                 if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
                 if (n == 1 && codes && sh.bn % 128) continue;
@@ -121,10 +123,7 @@ Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) 
                     us += sh.start_us + (double)per * (rest <= kCUs ? sh.step_us : sh.full_us);
                 if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
                 if (pass == 0 && slices > 0 && n == slices) us = -1;   // (as asked)
-                if (best.shape < 0 || us < best_us) {
-                    best = Plan{s, steps, per, n};
-                    best_us = us;
-                }
+                if (best.shape < 0 || us < best.us) best = Plan{s, steps, per, n, us};
             }
         }
         if (only < 0) break;
@@ -220,11 +219,56 @@ void set_plan(const Sizes& z, const Plan& plan, fg::GatedTileParams& p) {
     p.splits = (int32_t)plan.splits;
 }
 
+// dx (px) beside dgate and dup (pw) in one launch, where that is cheaper by estimate than
+// the plans they have; px.shape -1: apart.
+//
+// binary32: tiles of 64 x 128, two to a CU, which take the next as they end: the mean of what
+// the CUs get, and not less than seven tenths of the longest (alone on its CU it is faster).
+// 1025 tokens, 1536 x 2047: 246 us, apart 278; 517, 2047 x 3001: 243 and 264; 1000, 1000 x
+// 3000: 221 and 227; 700, 2048 x 1408: 150 and 162.
+// bfloat16: dx's smallest tiles beside tiles of 128 x 128, as long as they do not fill the CUs
+// by themselves. 64 tokens, 2048 x 1408: 18 us, apart 27; 200: 23 and 33; 300: 24 and 37; 512:
+// 37 and 40; 700 (not taken): 47 and 46.
+void plan_pair(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Plan& px, Plan& pw) {
+    for (int op : {fg::GATED_DX, fg::GATED_DW})
+        if (g_forced[op][bf16].tile.load() >= 0 || g_forced[op][bf16].slices.load() > 0) {
+            px.shape = -1;
+            return;
+        }
+    if (bf16) {
+        px.shape = pw.shape == fg::kPairDw && pw.splits == 1 ? fg::gated_pair(zx.M, zx.N, zw.M) : -1;
+        if (px.shape < 0) return;
+        px.steps = px.per = cdiv(zx.K * 2, fg::gated_shape(fg::GATED_DX, true, px.shape).kb) * zx.terms;
+        px.splits = 1;
+        return;
+    }
+    const fg::GatedShape x = fg::gated_shape(fg::GATED_DX, false, fg::kPairDxF32);
+    const fg::GatedShape w = fg::gated_shape(fg::GATED_DW, false, fg::kPairDwF32);
+    const double apart = px.us + pw.us;
+    const double nx = (double)cdiv(zx.M, x.bm) * (double)cdiv(zx.N, x.bn);
+    const double nw = (double)cdiv(zw.M, w.bm) * (double)cdiv(zw.N, w.bn) * 2;
+    const int64_t steps = cdiv(zx.K * 4, x.kb) * zx.terms, steps_w = cdiv(zw.K * 4, w.kb);
+    const double each_w = w.start_us + (double)steps_w * w.full_us, slots = kCUs * x.per_cu;
+    const double slice = (double)zx.M * (double)zx.N * 4;
+    px.shape = -1;
+    px.us = 0.95 * apart;   // (the estimates' error)
+    if (nx * 16 + nw >= (double)(1 << 22)) return;
+    for (const int64_t n : kSlices) {
+        const int64_t per = cdiv(steps, n);
+        if (cdiv(steps, per) != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
+        const double each = x.start_us + (double)per * x.full_us;
+        double us = std::max((nx * (double)n * each + nw * each_w) / slots, 0.7 * std::max(each, each_w));
+        if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
+        if (us < px.us) px = Plan{fg::kPairDxF32, steps, per, n, us};
+    }
+    pw = Plan{fg::kPairDwF32, steps_w, steps_w, 1, 0};
+}
+
 // One product of tiles, with its finish. p: everything but sizes, steps, slices and ws.
 fg_status run_tiles(int op, bool bf16, bool codes, const Sizes& z, fg::GatedTileParams& p,
                     void* ws, size_t ws_bytes, hipStream_t stream) {
     if (z.K == 0) {   // empty sums
-        set_plan(z, Plan{0, 0, 0, 0}, p);
+        set_plan(z, Plan{0, 0, 0, 0, 0}, p);
         return launched(fg::launch_gated_finish(op, bf16, p, stream), "gated block kernel");
     }
     const Plan plan = plan_tiles(op, bf16, codes, z, ws ? ws_bytes : 0);
@@ -463,20 +507,19 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
     w.ldc[1] = d.lddup;
     w.beta = d.beta;
     const Sizes zx = sizes_of(fg::GATED_DX, T, H, I), zw = sizes_of(fg::GATED_DW, T, H, I);
-    // dx's smallest tiles beside dgate's and dup's, where those are of 128 x 128 and of one
-    // slice and dx has at most two to a CU: 200 tokens, 2048 x 1408 27.5 us together, 30.4
-    // apart; 1024 x 2816 26 and 34; 512 tokens, 2048 x 1408 37.6 and 39.6, 700 (704 tiles)
-    // 46.9 and 47.2.
-    const Forced& fx = g_forced[fg::GATED_DX][1];
-    const int only = fx.tile.load(), slices = fx.slices.load();
-    if (bf16 && want_dx && want_dw && I > 0 && (only < 0 || only == fg::kPairDx) && slices <= 1 &&
-        fg::gated_pair_tiles(zx.M, zx.N) <= 512) {
-        const Plan plan = plan_tiles(fg::GATED_DW, true, false, zw, more_bytes);
-        if (plan.shape == fg::kPairDw && plan.splits == 1) {
-            const int64_t steps = cdiv(zx.K * 2, fg::gated_shape(fg::GATED_DX, true, fg::kPairDx).kb) * zx.terms;
-            set_plan(zx, Plan{fg::kPairDx, steps, steps, 1}, x);
-            set_plan(zw, plan, w);
-            return launched(fg::launch_gated_pair(x, w, stream), "gated block's gradient kernel");
+    if (want_dx && want_dw && I > 0) {
+        Plan px = plan_tiles(fg::GATED_DX, bf16, false, zx, more_bytes);
+        Plan pw = plan_tiles(fg::GATED_DW, bf16, false, zw, more_bytes);
+        if (px.shape >= 0 && pw.shape >= 0) plan_pair(bf16, zx, zw, more_bytes, px, pw);
+        if (px.shape >= 0 && pw.shape >= 0) {
+            set_plan(zx, px, x);
+            set_plan(zw, pw, w);
+            x.ws = static_cast<float*>(more);
+            st = launched(fg::launch_gated_pair(bf16, px.shape, x, w, stream), "gated block's gradient kernel");
+            if (st == FG_OK && px.splits > 1)
+                st = launched(fg::launch_gated_finish(fg::GATED_DX, bf16, x, stream),
+                              "gated block's reduction kernel");
+            return st;
         }
     }
     if (want_dx) st = run_tiles(fg::GATED_DX, bf16, false, zx, x, more, more_bytes, stream);

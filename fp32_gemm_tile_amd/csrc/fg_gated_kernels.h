@@ -102,11 +102,16 @@ int gated_num_shapes(int op, bool bf16);
 GatedShape gated_shape(int op, bool bf16, int shape);
 hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams& p,
                              hipStream_t stream);
-// dx in its smallest tile and dgate and dup in tile kPairDw, bfloat16, of one slice each, in
-// one launch: each alone is a chain of latencies on a part of the CUs. gated_pair_tiles: of dx.
-constexpr int kPairDx = 4, kPairDw = 1;
-int64_t gated_pair_tiles(int64_t M, int64_t N);
-hipError_t launch_gated_pair(const GatedTileParams& dx, const GatedTileParams& dw, hipStream_t stream);
+// dx and dgate and dup (one slice) in one launch. bfloat16: dx in one of its two smallest
+// tiles and one slice, dgate and dup in tile kPairDw; each alone is a chain of latencies on a
+// part of the CUs. binary32: tiles of 64 x 128.
+constexpr int kPairDx32 = 4, kPairDx64 = 3, kPairDw = 1;
+constexpr int kPairDxF32 = 1, kPairDwF32 = 2;
+// dx's tile in bfloat16, or -1: where all tiles are at most two to a CU, the smaller if
+// either leaves them so, or where dx's smallest are.
+int gated_pair(int64_t T, int64_t H, int64_t I);
+hipError_t launch_gated_pair(bool bf16, int dx_shape, const GatedTileParams& dx, const GatedTileParams& dw,
+                             hipStream_t stream);
 // What follows a launch with several slices.
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream);
 

@@ -207,9 +207,10 @@ constexpr int kLdsBytes = [] {
     return kStages > kOut ? kStages : kOut;
 }();
 
-// id: of n workgroups.
+// id: of n workgroups, which take slice `split` of the sums.
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
-__device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds, int id, int n) {
+__device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds, int id, int n,
+                                          int split) {
     constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
     constexpr int TI = WM / 16, TJ = WN / 16;
     constexpr int SIZE = BF16 ? 2 : 4;
@@ -237,7 +238,6 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kCols;
     const int rows = p.M - m0 < BM ? (int)(p.M - m0) : BM;
     const int cols = p.N - n0 < kCols ? (int)(p.N - n0) : kCols;
-    const int split = blockIdx.y;
     const int s0 = split * p.per_split;
     const int s1 = s0 + p.per_split < p.steps ? s0 + p.per_split : p.steps;
     const int half = OP == GATED_DX ? p.steps / 2 : p.steps;   // steps of one matrix
@@ -597,7 +597,7 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) gated_tile_kernel(GatedTileParams p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes<OP, BF16, BM, BN, WM, WN, KB, NS>];
-    tile_body<OP, BF16, BM, BN, WM, WN, KB, NS>(p, lds, blockIdx.x, gridDim.x);
+    tile_body<OP, BF16, BM, BN, WM, WN, KB, NS>(p, lds, blockIdx.x, gridDim.x, blockIdx.y);
 }
 
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
@@ -612,26 +612,39 @@ hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// dx and dgate and dup in one launch.
+// dx, its slices one after the other, and dgate and dup in one launch. n: tiles of dx.
 template <typename DX, typename DW>
-__global__ void __launch_bounds__(256, 2) gated_pair_kernel(GatedTileParams dx, GatedTileParams dw, int n) {
+__global__ void __launch_bounds__(DX::kThreads, 2) gated_pair_kernel(GatedTileParams dx, GatedTileParams dw, int n) {
+    static_assert(DX::kThreads == DW::kThreads, "threads of the launch");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[DX::kLds > DW::kLds ? DX::kLds : DW::kLds];
-    if ((int)blockIdx.x < n) DX::run(dx, lds, blockIdx.x, n);
-    else DW::run(dw, lds, blockIdx.x - n, gridDim.x - n);
+    const int id = blockIdx.x, all = n * dx.splits;
+    if (id < all) DX::run(dx, lds, id % n, n, id / n);
+    else DW::run(dw, lds, id - all, gridDim.x - all, 0);
 }
-template <int OP, int BM, int BN, int WM, int WN, int KB, int NS>
+template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 struct Part {
-    static_assert(64 * (BM / WM) * (BN / WN) == 256, "threads of the launch");
-    static constexpr int kLds = kLdsBytes<OP, true, BM, BN, WM, WN, KB, NS>;
-    static __device__ __forceinline__ void run(const GatedTileParams& p, uint8_t* lds, int id, int n) {
-        tile_body<OP, true, BM, BN, WM, WN, KB, NS>(p, lds, id, n);
+    static constexpr int kThreads = 64 * (BM / WM) * (BN / WN);
+    static constexpr int kLds = kLdsBytes<OP, BF16, BM, BN, WM, WN, KB, NS>;
+    static __device__ __forceinline__ void run(const GatedTileParams& p, uint8_t* lds, int id, int n, int split) {
+        tile_body<OP, BF16, BM, BN, WM, WN, KB, NS>(p, lds, id, n, split);
     }
     static int64_t tiles(int64_t M, int64_t N) {
         return ((M + BM - 1) / BM) * ((N + BN - 1) / BN) * (OP == GATED_DW ? 2 : 1);
     }
 };
-using PairDx = Part<GATED_DX, 32, 64, 16, 32, 256, 3>;
-using PairDw = Part<GATED_DW, 128, 128, 64, 64, 64, 4>;
+using PairDx32 = Part<GATED_DX, true, 32, 64, 16, 32, 256, 3>;
+using PairDx64 = Part<GATED_DX, true, 64, 64, 32, 32, 128, 4>;
+using PairDw = Part<GATED_DW, true, 128, 128, 64, 64, 64, 4>;
+using PairDxF32 = Part<GATED_DX, false, 64, 128, 32, 32, 128, 3>;
+using PairDwF32 = Part<GATED_DW, false, 64, 128, 32, 32, 128, 3>;
+
+template <typename DX, typename DW>
+hipError_t launch_pair(const GatedTileParams& dx, const GatedTileParams& dw, hipStream_t stream) {
+    const int64_t n = DX::tiles(dx.M, dx.N);
+    hipLaunchKernelGGL((gated_pair_kernel<DX, DW>), dim3((unsigned)(n * dx.splits + DW::tiles(dw.M, dw.N))),
+                       dim3(DX::kThreads), 0, stream, dx, dw, (int)n);
+    return hipGetLastError();
+}
 
 // Sums of the slices in ascending order, and what a launch with one slice does to
 // them: half a wave per 128 columns of a row, four columns per lane.
@@ -834,13 +847,18 @@ hipError_t launch_gated_tile(int op, bool bf16, int shape, const GatedTileParams
     return hipErrorInvalidValue;
 }
 
-int64_t gated_pair_tiles(int64_t M, int64_t N) { return PairDx::tiles(M, N); }
+int gated_pair(int64_t T, int64_t H, int64_t I) {
+    const int64_t dw = PairDw::tiles(I, H);
+    if (PairDx32::tiles(T, H) + dw <= 512) return kPairDx32;
+    if (PairDx64::tiles(T, H) + dw <= 512) return kPairDx64;
+    return PairDx32::tiles(T, H) <= 512 ? kPairDx32 : -1;
+}
 
-hipError_t launch_gated_pair(const GatedTileParams& dx, const GatedTileParams& dw, hipStream_t stream) {
-    const int64_t n = PairDx::tiles(dx.M, dx.N), all = n + PairDw::tiles(dw.M, dw.N);
-    hipLaunchKernelGGL((gated_pair_kernel<PairDx, PairDw>), dim3((unsigned)all), dim3(256), 0, stream, dx, dw,
-                       (int)n);
-    return hipGetLastError();
+hipError_t launch_gated_pair(bool bf16, int dx_shape, const GatedTileParams& dx, const GatedTileParams& dw,
+                             hipStream_t stream) {
+    if (!bf16) return launch_pair<PairDxF32, PairDwF32>(dx, dw, stream);
+    return dx_shape == kPairDx32 ? launch_pair<PairDx32, PairDw>(dx, dw, stream)
+                                 : launch_pair<PairDx64, PairDw>(dx, dw, stream);
 }
 
 hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipStream_t stream) {
