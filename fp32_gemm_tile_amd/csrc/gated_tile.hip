@@ -18,7 +18,18 @@
 // rows a wave reads together fall on different banks. One stored along m or n (the
 // weights in DX, all of DW) keeps its order in memory, a row of LDS per k, and is
 // transposed by the read (ds_read_b64_tr_b16: 4 k of 16 columns per 16 lanes), so no
-// transposed copy is ever made.
+// transposed copy is ever made. A binary32 one is read element by element.
+//
+// Large products are bound by the matrix cores: 4096 tokens, 4096 x 8192 in bfloat16, 256
+// x 256 of B's and A's rows to a workgroup of eight waves (64 x 128 each, as large as the
+// registers hold): forward 414 to 430 us (1280 to 1330 TFLOP/s), 460 with G and U kept, dx
+// 400, dgate and dup 393; the cores are busy 68 to 71 % and the clock is down to 1.65 GHz, and
+// with the 32 x 32 x 16 instruction both products give the same time. Short ones are bound by
+// latency, a step of a small tile taking as long as its barrier, its loads' issue and the next
+// reads: there a step is 128 or 256 bytes of k (32 tokens, 4096 x 8192: steps of 64 bytes 46
+// us in tiles of 64 x 64 and 33 of 32 x 32, of 128 bytes 30, 4.5 TB/s of weights). Binary32
+// reaches the instruction's rate where every CU has two workgroups (1024 tokens, 4096 x 4096:
+// 473 us, 145 TFLOP/s).
 #include "fg_device.h"
 #include "fg_e4m3.h"
 #include "fg_gated_kernels.h"
@@ -194,8 +205,6 @@ struct Quad {
     }
 };
 
-// The operands of a step are in registers before it begins, those of the next are read
-// during it, and so a stage is free for its next load a step earlier.
 // A workgroup's LDS: the stages, or the results' way out (16 rows of every wave, of both
 // products, and what the codes of their rows are found with).
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
@@ -207,7 +216,9 @@ constexpr int kLdsBytes = [] {
     return kStages > kOut ? kStages : kOut;
 }();
 
-// id: of n workgroups, which take slice `split` of the sums.
+// The operands of a step are in registers before it begins, those of the next are read
+// during it, and so a stage is free for its next load a step earlier. id: of n workgroups,
+// which take slice `split` of the sums.
 template <int OP, bool BF16, int BM, int BN, int WM, int WN, int KB, int NS>
 __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds, int id, int n,
                                           int split) {
@@ -612,7 +623,8 @@ hipError_t launch_tile(const GatedTileParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// dx, its slices one after the other, and dgate and dup in one launch. n: tiles of dx.
+// dx, its slices one after the other, and dgate and dup in one launch, dx first, whose sums
+// are longer. n: tiles of dx. (What it saves is in plan_pair's comment.)
 template <typename DX, typename DW>
 __global__ void __launch_bounds__(DX::kThreads, 2) gated_pair_kernel(GatedTileParams dx, GatedTileParams dw, int n) {
     static_assert(DX::kThreads == DW::kThreads, "threads of the launch");
@@ -647,7 +659,9 @@ hipError_t launch_pair(const GatedTileParams& dx, const GatedTileParams& dw, hip
 }
 
 // Sums of the slices in ascending order, and what a launch with one slice does to
-// them: half a wave per 128 columns of a row, four columns per lane.
+// them: half a wave per 128 columns of a row, four columns per lane, four slices' loads
+// at a time. Partial sums come from the caches; 200 tokens x 1408, two slices with codes: 4.4
+// us, most of it the launch and two dependent trips.
 template <int OP, bool BF16>
 __global__ void __launch_bounds__(256) gated_finish_kernel(GatedTileParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;
@@ -902,6 +916,8 @@ __device__ __forceinline__ void activate_both(float x, float& a, float& d) {
     }
 }
 
+// dG, dU and h in one pass, four columns per thread, so that a wave reads and writes whole
+// lines. Bound by HBM: 4096 x 8192 in bfloat16, five matrices, 61 us, 5.5 TB/s.
 template <bool BF16, bool CODES, int ACT>
 __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;
