@@ -314,6 +314,33 @@ def test_a_token_touches_its_own_row_only(ty, T):
 
 
 @pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [8, 300])
+@pytest.mark.parametrize("ws", [0, 1 << 24])
+def test_codes_beside_infinities_and_nan(ty, T, ws):
+    """A block's scale and its other codes are those it has with zeros in the place of sums
+    that are infinite or NaN, whose codes are NaN."""
+    import torch
+    c = Case(T, 130, 300, ty, seed=T)
+
+    def run():
+        saved = fg.empty_fp8(T, 300) + fg.empty_fp8(T, 300)
+        h = torch.empty(T, 300, dtype=c.x.dtype, device="cuda")
+        fg.gated(c.x, c.gate, c.up, h, saved=saved, workspace=c.workspace(ws) if ws else None)
+        return [t.view(torch.uint8) if t.element_size() == 1 else t for t in saved]
+
+    bad = [5, 64, 200]
+    c.gate[bad] = 0
+    clean = run()
+    c.gate[5, 3], c.gate[64, 129], c.gate[200, 0] = float("inf"), -float("inf"), float("nan")
+    dirty = run()
+    good = [n for n in range(300) if n not in bad]
+    assert torch.equal(clean[0][:, good], dirty[0][:, good])
+    for a, b in zip(clean[1:], dirty[1:]):
+        assert torch.equal(a, b)
+    assert ((dirty[0][:, bad] & 0x7F) == 0x7F).all()
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
 def test_long_rows(ty):
     """Rows so far apart that offsets pass 32 bits: the bits of compact ones."""
     import torch
