@@ -208,7 +208,7 @@ struct Quad {
 // codes4 for binary32 sums, whose quotients are seldom near a middle between codes: the
 // codes of x r with r off by 2^-21 to either side, which is more than r and the product are
 // off by (2^-23), agree unless one is in between. 15 instructions per four elements for 26
-// (8192 tokens, 2048 x 8192: the codes take half of FIG us).
+// (8192 tokens, 2048 x 8192: 553 us and 542).
 __device__ __forceinline__ uint32_t codes_of(const f4& x, const Divisor& d) {
     const float lo = fmaf(d[0], -0x1p-21f, d[0]), hi = fmaf(d[0], 0x1p-21f, d[0]);
     int a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * lo, x[1] * lo, 0, false);
@@ -511,7 +511,7 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < TI; ++i) {
-                        // (of all magnitudes, and again of the finite ones if need be)
+                        // (of all magnitudes, and again of the finite ones if need be: 546 us and 533)
                         uint32_t v = 0;
 #pragma unroll
                         for (int j = 0; j < PJ; ++j)
