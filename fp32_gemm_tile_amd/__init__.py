@@ -1087,6 +1087,8 @@ def gated_backward(dout, x, gate, up, saved, dx=None, dgate=None, dup=None, out=
 
 def _int4(torch, types, w, name, dev, N, K, group):
     """fg_type of the scales and the fg_int4 of (codes, scales, zero points or None)."""
+    if group not in (32, 64, 128):
+        _wrong("group", f"be 32, 64 or 128, is {group}")
     q, s, z = w
     if q.dtype != torch.uint8:
         raise TypeError(f"codes of {name} must be uint8")

@@ -188,7 +188,7 @@ fg_status fg_select_gated(int32_t product, int32_t type, int64_t T, int64_t H, i
  * Tile of every later product of that kind in this process, for tests and
  * measurements, and its slices: -1 and 0 (the default) the library's choice.
  * Slices need the workspace for them (else as many as fit). Where G and U are kept in
- * 8 bits, a tile of less than 128 columns is not used. FG_ERR_INVALID_ARG for
+ * 8 bits, a tile of less than 128 columns is used with slices only. FG_ERR_INVALID_ARG for
  * another number.
  */
 fg_status fg_set_gated_tile(int32_t product, int32_t type, int32_t tile, int32_t slices);

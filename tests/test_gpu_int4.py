@@ -249,6 +249,9 @@ def test_wrong_tensors_are_refused():
     for bad in ((q[:4], s, z), (q, s[:1], z), (q, s, z[:1]), (q, s.t().contiguous().t(), z)):
         with pytest.raises(ValueError):
             fg.gemm_int4(x, bad, out, group=32)
+    for group in (0, 48, -32):
+        with pytest.raises(ValueError):
+            fg.gemm_int4(x, w.t, out, group=group)
     with pytest.raises(TypeError):
         fg.gemm_int4(x, (q.float(), s, z), out, group=32)
     with pytest.raises(TypeError):
