@@ -97,11 +97,13 @@ constexpr int64_t kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
 // The cheapest by estimate: rounds of as many workgroups as run together, the last of
 // which may have one to a CU; slices of the sum cost a kernel and their partial sums'
 // way to memory and back. codes: a block of 128 columns has to be in one workgroup,
-// or in the kernel that joins slices.
+// or in the kernel that joins slices. (A number of slices by which the steps do not
+// divide into as many parts is none; a larger one may be.) A forced number: that many,
+// or the most below it that the steps and the workspace have.
 Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) {
     constexpr double kMaxTiles = 1 << 23;         // of 512 threads: a grid has fewer than 2^32
     Forced& forced = g_forced[op][bf16];
-    const int only = forced.tile.load(), slices = forced.slices.load();
+    const int only = forced.tile.load(), asked = forced.slices.load();
     const double slice = (double)z.M * (double)z.N * 4 * z.results;
     Plan best{-1, 0, 0, 1, 0};
     for (int pass = 0; pass < 2 && best.shape < 0; ++pass) {   // (1: the forced tile cannot)
@@ -112,18 +114,28 @@ Plan plan_tiles(int op, bool bf16, bool codes, const Sizes& z, size_t ws_bytes) 
                                  (op == fg::GATED_DW ? 2 : 1);
             if (tiles >= kMaxTiles) continue;
             const int64_t steps = cdiv(z.K * (bf16 ? 2 : 4), sh.kb) * z.terms;
-            for (const int64_t n : kSlices) {
-                const int64_t per = cdiv(steps, n), used = cdiv(steps, per);
-                if (used != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
-                if (n == 1 && codes && sh.bn % 128) continue;
+            auto fits = [&](int64_t n) {
+                return cdiv(steps, cdiv(steps, n)) == n && (n == 1 || (double)n * slice <= (double)ws_bytes) &&
+                       !(n == 1 && codes && sh.bn % 128);
+            };
+            auto consider = [&](int64_t n) {
+                const int64_t per = cdiv(steps, n);
                 const double slots = kCUs * sh.per_cu, full = std::floor(tiles * (double)n / slots);
                 const double rest = tiles * (double)n - full * slots;
                 double us = full * (sh.start_us + (double)per * sh.full_us);
                 if (rest > 0)
                     us += sh.start_us + (double)per * (rest <= kCUs ? sh.step_us : sh.full_us);
                 if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;
-                if (pass == 0 && slices > 0 && n == slices) us = -1;   // (as asked)
-                if (best.shape < 0 || us < best.us) best = Plan{s, steps, per, n, us};
+                const bool better = pass == 0 && asked > 0 && n != best.splits ? n > best.splits : us < best.us;
+                if (best.shape < 0 || better) best = Plan{s, steps, per, n, us};
+            };
+            if (pass == 0 && asked > 0) {
+                int64_t n = asked;
+                while (n > 0 && !fits(n)) --n;
+                if (n > 0) consider(n);
+            } else {
+                for (const int64_t n : kSlices)
+                    if (fits(n)) consider(n);
             }
         }
         if (only < 0) break;
@@ -255,7 +267,7 @@ void plan_pair(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Pla
     if (nx * 16 + nw >= (double)(1 << 22)) return;
     for (const int64_t n : kSlices) {
         const int64_t per = cdiv(steps, n);
-        if (cdiv(steps, per) != n || (n > 1 && (double)n * slice > (double)ws_bytes)) break;
+        if (cdiv(steps, per) != n || (n > 1 && (double)n * slice > (double)ws_bytes)) continue;
         const double each = x.start_us + (double)per * x.full_us;
         double us = std::max((nx * (double)n * each + nw * each_w) / slots, 0.7 * std::max(each, each_w));
         if (n > 1) us += kFinish + 2 * (double)n * slice / kPartial;

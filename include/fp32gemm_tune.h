@@ -186,10 +186,11 @@ fg_status fg_select_gated(int32_t product, int32_t type, int64_t T, int64_t H, i
 
 /*
  * Tile of every later product of that kind in this process, for tests and
- * measurements, and its slices: -1 and 0 (the default) the library's choice.
- * Slices need the workspace for them (else as many as fit). Where G and U are kept in
- * 8 bits, a tile of less than 128 columns is used with slices only. FG_ERR_INVALID_ARG for
- * another number.
+ * measurements, and its slices, 1 to 16: -1 and 0 (the default) the library's choice.
+ * Slices take whole steps of the sum and need the workspace for them: where the steps do
+ * not divide into as many parts, or the workspace is too small, the most below it that
+ * fit. Where G and U are kept in 8 bits, a tile of less than 128 columns is used with
+ * slices only. FG_ERR_INVALID_ARG for another number.
  */
 fg_status fg_set_gated_tile(int32_t product, int32_t type, int32_t tile, int32_t slices);
 
