@@ -277,6 +277,9 @@ def load_library(path: str = LIB_PATH):
     lib.fg_select_gated.argtypes = [i32, i32, i64, i64, i64, size, ctypes.POINTER(i32),
                                     ctypes.POINTER(i32)]
     lib.fg_select_gated.restype = i32
+    lib.fg_select_gated_pair.argtypes = [i32, i64, i64, i64, size, ctypes.POINTER(i32),
+                                         ctypes.POINTER(i32)]
+    lib.fg_select_gated_pair.restype = i32
     lib.fg_set_gated_tile.argtypes = [i32, i32, i32, i32]
     lib.fg_set_gated_tile.restype = i32
     lib.fg_estimate_seconds.argtypes = [i64, i64, i64, i32, i32, i32]
@@ -665,6 +668,15 @@ def fg_select_gated(product, type, T, H, I, workspace_bytes=0):
     t, s = ctypes.c_int32(), ctypes.c_int32()
     _raise_if(load_library().fg_select_gated(product, type, T, H, I, workspace_bytes,
                                              ctypes.byref(t), ctypes.byref(s)))
+    return t.value, s.value
+
+
+def fg_select_gated_pair(type, T, H, I, workspace_bytes=0):
+    """(dx's tile, its slices) where all gradients of the gated block are one launch, else
+    (-1, 0) (include/fp32gemm_tune.h)."""
+    t, s = ctypes.c_int32(), ctypes.c_int32()
+    _raise_if(load_library().fg_select_gated_pair(type, T, H, I, workspace_bytes,
+                                                  ctypes.byref(t), ctypes.byref(s)))
     return t.value, s.value
 
 

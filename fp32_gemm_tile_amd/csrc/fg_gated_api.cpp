@@ -239,8 +239,11 @@ void set_plan(const Sizes& z, const Plan& plan, fg::GatedTileParams& p) {
 // 1025 tokens, 1536 x 2047: 246 us, apart 278; 517, 2047 x 3001: 243 and 264; 1000, 1000 x
 // 3000: 221 and 227; 700, 2048 x 1408: 150 and 162.
 // bfloat16: dx's smallest tiles beside tiles of 128 x 128, as long as they do not fill the CUs
-// by themselves. 64 tokens, 2048 x 1408: 18 us, apart 27; 200: 23 and 33; 300: 24 and 37; 512:
-// 37 and 40; 700 (not taken): 47 and 46.
+// by themselves. dx is one slice there, so its sum has to end before two launches, of which
+// the second costs 2 us, would have: a step takes 1.35 times what it does alone. 64 tokens, 2048 x
+// 1408: 16 us, apart 22; 200: 21 and 27; 300: 22 and 32; 200, 1024 x 4096 33 and 36; 200, 2048 x
+// 5632 51 and 67. Longer sums of few tiles (not taken): 300, 256 x 8192 55 and 37; 64, 512 x
+// 8192 53 and 27; 17, 512 x 4096 29 and 18. (Of 52 sizes three are chosen wrongly, by up to 9 %.)
 void plan_pair(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Plan& px, Plan& pw) {
     for (int op : {fg::GATED_DX, fg::GATED_DW})
         if (g_forced[op][bf16].tile.load() >= 0 || g_forced[op][bf16].slices.load() > 0) {
@@ -248,10 +251,13 @@ void plan_pair(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Pla
             return;
         }
     if (bf16) {
+        const double apart = px.us + pw.us + 2;
         px.shape = pw.shape == fg::kPairDw && pw.splits == 1 ? fg::gated_pair(zx.M, zx.N, zw.M) : -1;
         if (px.shape < 0) return;
-        px.steps = px.per = cdiv(zx.K * 2, fg::gated_shape(fg::GATED_DX, true, px.shape).kb) * zx.terms;
+        const fg::GatedShape x = fg::gated_shape(fg::GATED_DX, true, px.shape);
+        px.steps = px.per = cdiv(zx.K * 2, x.kb) * zx.terms;
         px.splits = 1;
+        if (x.start_us + 1.35 * (double)px.steps * x.step_us >= apart) px.shape = -1;
         return;
     }
     const fg::GatedShape x = fg::gated_shape(fg::GATED_DX, false, fg::kPairDxF32);
@@ -274,6 +280,16 @@ void plan_pair(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Pla
         if (us < px.us) px = Plan{fg::kPairDxF32, steps, per, n, us};
     }
     pw = Plan{fg::kPairDwF32, steps_w, steps_w, 1, 0};
+}
+
+// dx's part of the one launch that a call which wants all gradients makes; shape -1: it
+// makes two. pw: that of dgate and dup.
+Plan plan_gradients(bool bf16, const Sizes& zx, const Sizes& zw, size_t ws_bytes, Plan& pw) {
+    Plan px = plan_tiles(fg::GATED_DX, bf16, false, zx, ws_bytes);
+    pw = plan_tiles(fg::GATED_DW, bf16, false, zw, ws_bytes);
+    if (pw.shape < 0) px.shape = -1;
+    if (px.shape >= 0) plan_pair(bf16, zx, zw, ws_bytes, px, pw);
+    return px;
 }
 
 // One product of tiles, with its finish. p: everything but sizes, steps, slices and ws.
@@ -340,6 +356,25 @@ fg_status fg_select_gated(int32_t product, int32_t type, int64_t T, int64_t H, i
     if (plan.shape < 0) return fail(FG_ERR_UNSUPPORTED, 0, "2^23 or more output tiles");
     *tile = plan.shape;
     *slices = (int32_t)plan.splits;
+    return FG_OK;
+}
+
+fg_status fg_select_gated_pair(int32_t type, int64_t T, int64_t H, int64_t I,
+                               size_t workspace_bytes, int32_t* tile, int32_t* slices) {
+    clear_error();
+    if (!known_product(fg::GATED_DX, type)) return fail(FG_ERR_INVALID_ARG, 1, "no tiles for type %d", type);
+    if (T <= 0) return fail(FG_ERR_INVALID_ARG, 2, "T < 1");
+    if (H <= 0) return fail(FG_ERR_INVALID_ARG, 3, "H < 1");
+    if (I <= 0) return fail(FG_ERR_INVALID_ARG, 4, "I < 1");
+    if (!tile) return fail(FG_ERR_INVALID_ARG, 6, "tile is NULL");
+    if (!slices) return fail(FG_ERR_INVALID_ARG, 7, "slices is NULL");
+    if (!sizes_ok(T, H, I))
+        return fail(FG_ERR_UNSUPPORTED, 0, "tokens, hidden and inner are limited to 2^30");
+    Plan pw;
+    const Plan px = plan_gradients(type == FG_TYPE_BF16, sizes_of(fg::GATED_DX, T, H, I),
+                                   sizes_of(fg::GATED_DW, T, H, I), workspace_bytes, pw);
+    *tile = px.shape;
+    *slices = px.shape < 0 ? 0 : (int32_t)px.splits;
     return FG_OK;
 }
 
@@ -520,10 +555,9 @@ fg_status fg_gated_backward(const fg_gated_block* block, const fg_gated_grads* g
     w.beta = d.beta;
     const Sizes zx = sizes_of(fg::GATED_DX, T, H, I), zw = sizes_of(fg::GATED_DW, T, H, I);
     if (want_dx && want_dw && I > 0) {
-        Plan px = plan_tiles(fg::GATED_DX, bf16, false, zx, more_bytes);
-        Plan pw = plan_tiles(fg::GATED_DW, bf16, false, zw, more_bytes);
-        if (px.shape >= 0 && pw.shape >= 0) plan_pair(bf16, zx, zw, more_bytes, px, pw);
-        if (px.shape >= 0 && pw.shape >= 0) {
+        Plan pw;
+        const Plan px = plan_gradients(bf16, zx, zw, more_bytes, pw);
+        if (px.shape >= 0) {
             set_plan(zx, px, x);
             set_plan(zw, pw, w);
             x.ws = static_cast<float*>(more);

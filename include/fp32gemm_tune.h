@@ -175,14 +175,19 @@ fg_status fg_set_fp8_tile(int32_t tile);
  * workgroup of tile `tile` (3). fg_select_gated: the tile (7) and the slices of the sum
  * (8) that a call with T, H and I (3 to 5, positive) and workspace_bytes (6)
  * for its partial sums runs; tile -1: not a tile kernel (forward products of few
- * tokens stream the weights); a call that wants dx, dgate and dup may run other tiles,
- * all in one launch, where that is cheaper and no tile was set; FG_ERR_UNSUPPORTED where the call would be. Host only.
+ * tokens stream the weights); FG_ERR_UNSUPPORTED where the call would be.
+ * fg_select_gated_pair: a call that wants dx, dgate and dup may make one launch for all three,
+ * where that is cheaper and no tile was set. For type, T, H, I and workspace_bytes (1 to 5) the
+ * tile of dx in it (6) and dx's slices (7); tile -1 and slices 0: it makes two, of the tiles that
+ * fg_select_gated tells. Host only.
  */
 int32_t fg_gated_num_tiles(int32_t product, int32_t type);
 fg_status fg_gated_tile(int32_t product, int32_t type, int32_t tile, int32_t* rows,
                         int32_t* columns);
 fg_status fg_select_gated(int32_t product, int32_t type, int64_t T, int64_t H, int64_t I,
                           size_t workspace_bytes, int32_t* tile, int32_t* slices);
+fg_status fg_select_gated_pair(int32_t type, int64_t T, int64_t H, int64_t I,
+                               size_t workspace_bytes, int32_t* tile, int32_t* slices);
 
 /*
  * Tile of every later product of that kind in this process, for tests and
