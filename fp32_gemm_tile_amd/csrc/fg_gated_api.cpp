@@ -407,9 +407,14 @@ size_t fg_gated_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t 
     if (!sizes_ok(tokens, hidden, inner)) return 0;
     size_t n = fg_gated_backward_min_workspace_size(tokens, inner, type);
     const bool bf16 = type == FG_TYPE_BF16;
-    if (n > 0 && hidden > 0)
-        n += std::max(partial_bytes(fg::GATED_DX, bf16, tokens, hidden, inner),
-                      partial_bytes(fg::GATED_DW, bf16, tokens, hidden, inner));
+    if (n > 0 && hidden > 0) {
+        Plan pw;   // (dx's slices in one launch may be more than it has in its own)
+        const Plan px = plan_gradients(bf16, sizes_of(fg::GATED_DX, tokens, hidden, inner),
+                                       sizes_of(fg::GATED_DW, tokens, hidden, inner), (size_t)-1 / 2, pw);
+        n += std::max({partial_bytes(fg::GATED_DX, bf16, tokens, hidden, inner),
+                       partial_bytes(fg::GATED_DW, bf16, tokens, hidden, inner),
+                       px.shape >= 0 && px.splits > 1 ? (size_t)(px.splits * tokens * hidden) * 4 : (size_t)0});
+    }
     return n;
 }
 

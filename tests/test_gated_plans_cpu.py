@@ -79,3 +79,19 @@ def test_the_pair_s_arguments():
     finally:
         for product in (1, 2):
             fg.fg_set_gated_tile(product, 1)
+
+
+def test_no_workspace_beyond_the_reported_one_changes_a_plan():
+    for T in (17, 64, 65, 100, 130, 300, 517, 1025):
+        for H in (64, 300, 1000, 1536, 4096):
+            for I in (48, 300, 1408, 2047, 8192):
+                for ty in (0, 1):
+                    room = fg.fg_gated_workspace_size(T, H, I, ty)
+                    assert fg.fg_select_gated(0, ty, T, H, I, room) == fg.fg_select_gated(0, ty, T, H, I, BIG)
+                    room = (fg.fg_gated_backward_workspace_size(T, H, I, ty)
+                            - fg.fg_gated_backward_min_workspace_size(T, I, ty))
+                    pair = fg.fg_select_gated_pair(ty, T, H, I, BIG)
+                    assert fg.fg_select_gated_pair(ty, T, H, I, room) == pair, (T, H, I, ty)
+                    for product in (1, 2):
+                        assert (fg.fg_select_gated(product, ty, T, H, I, room)
+                                == fg.fg_select_gated(product, ty, T, H, I, BIG))
