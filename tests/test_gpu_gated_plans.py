@@ -35,3 +35,20 @@ def test_every_tile_in_as_many_slices_as_asked_for(product, T, H, I, ty):
                     c.backward("same", beta=0.5, more_ws=ws, parts=("dx",) if product == 1 else ("dw",))
     finally:
         fg.fg_set_gated_tile(product, code)
+
+
+@pytest.mark.parametrize("ty,T,H,I,alone,sliced", [
+    ("f32", 517, 1001, 299, (64, 1), (64, 1)), ("f32", 333, 2047, 301, (64, 1), (64, 2)),
+    ("f32", 130, 1000, 1500, None, (64, 8)), ("f32", 65, 1000, 2047, None, (64, 12)),
+    ("bf16", 33, 999, 1501, (32, 1), (32, 1)), ("bf16", 130, 1000, 1500, (32, 1), (32, 1)),
+    ("bf16", 300, 2047, 901, (64, 1), (64, 1))])
+def test_the_launch_of_all_gradients(ty, T, H, I, alone, sliced):
+    """dx beside dgate and dup, in one slice and in several: (rows of dx's tile, slices) with and
+    without room for partial sums, None: two launches."""
+    code = int(ty == "bf16")
+    c = Case(T, H, I, ty, seed=T, extra=1)
+    for more, want in ((0, alone), (1 << 25, sliced)):
+        tile, slices = fg.fg_select_gated_pair(code, T, H, I, more)
+        assert (None if tile < 0 else (fg.fg_gated_tiles(1, code)[tile][0], slices)) == want
+        c.backward("same", "silu", 0.0, more_ws=more)
+        c.backward("e4m3", "gelu", 1.0, more_ws=more)
