@@ -915,7 +915,8 @@ hipError_t launch_gated_finish(int op, bool bf16, const GatedTileParams& p, hipS
 namespace {
 
 // act(x) and act'(x). Where sigma or Phi has run out (x far below 0) both are 0, and
-// far above 0 the derivative is 1, also at the infinities.
+// far above 0 the derivative is 1. At the infinities the derivative is 0 and 1, too; act is
+// what the forward product has there, -inf times 0: NaN for silu and gelu of -inf.
 template <int ACT>
 __device__ __forceinline__ void activate_both(float x, float& a, float& d) {
     if constexpr (ACT == ACT_RELU) {

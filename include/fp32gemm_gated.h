@@ -25,6 +25,9 @@
  * the activation binary32, every output is rounded once. The gradients of G and U
  * are rounded to the block's type before they meet gate, up and x, as tensors
  * of that type would be.
+ *
+ * Infinities and NaN follow the formulas: silu and gelu of -inf are NaN (-inf times 0) and
+ * their slopes 0, of +inf infinite and 1.
  */
 #ifndef FP32GEMM_GATED_H
 #define FP32GEMM_GATED_H

@@ -52,3 +52,30 @@ def test_the_launch_of_all_gradients(ty, T, H, I, alone, sliced):
         assert (None if tile < 0 else (fg.fg_gated_tiles(1, code)[tile][0], slices)) == want
         c.backward("same", "silu", 0.0, more_ws=more)
         c.backward("e4m3", "gelu", 1.0, more_ws=more)
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu", "none"])
+def test_activations_of_the_infinities(ty, act):
+    """G = -inf, +inf and NaN: h forward (weights streamed and tiles) and again backward, and
+    the gradients, as the formulas say."""
+    import torch
+    inf, nan = float("inf"), float("nan")
+    dt = torch.float32 if ty == "f32" else torch.bfloat16
+    below = nan if act in ("silu", "gelu") else 0.0 if act == "relu" else -inf
+    want = torch.tensor([below, inf, nan, 0.0], dtype=torch.float64)
+    slope = torch.tensor([1.0 if act == "none" else 0.0, 1.0, 1.0 if act == "none" else nan,
+                          {"silu": 0.5, "gelu": 0.5, "relu": 0.0, "none": 1.0}[act]], dtype=torch.float64)
+    same = lambda a, b: torch.equal(torch.nan_to_num(a.double().cpu(), nan=7.0), torch.nan_to_num(b, nan=7.0))  # noqa: E731
+    for T in (1, 40):
+        x = torch.ones(T, 8, dtype=dt, device="cuda")
+        gate, up = torch.zeros(4, 8, dtype=dt, device="cuda"), torch.zeros(4, 8, dtype=dt, device="cuda")
+        gate[0, 0], gate[1, 0], gate[2, 0], up[:, 0] = -inf, inf, nan, 1.0
+        h, g, u, again = (torch.empty(T, 4, dtype=dt, device="cuda") for _ in range(4))
+        fg.gated(x, gate, up, h, activation=act, saved=(g, u))
+        one = torch.ones_like(h)
+        dgate, dup = torch.empty_like(gate), torch.empty_like(up)
+        fg.gated_backward(one, x, gate, up, (g, u), None, dgate, dup, out=again, activation=act)
+        for t in range(T):
+            assert same(h[t], want) and same(again[t], want)
+        assert same(dgate[:, 1], slope * T) and same(dup[:, 1], want * T)
