@@ -3,11 +3,20 @@
 //   out = x W^T          or          out = act(x W0^T) * (x W1^T)
 //
 // A byte 0x0q is the e4m3 number q 2^-9 for every q from 0 to 15, so the hardware's
-// conversion of e4m3 with a scale of 2^9 makes two codes bfloat16 at a time, exactly.
-// With t = sum q x over a group of columns and X = sum x, the group's part of the result
-// is s (t - z X), where X is one more matrix instruction, shared by all rows of W. Sums
-// are binary32; a binary32 x is three bfloat16 terms that hold its 24 bits. The
-// instruction's rows are x's, its columns W's, as in few_rows.h.
+// conversion of e4m3 with a scale of 2^9 makes two codes values at a time, exactly.
+// Sums are binary32; a binary32 x is three bfloat16 terms that hold its 24 bits (down to
+// 2^-133, bfloat16's smallest number). The instruction's rows are x's, its columns W's, as
+// in few_rows.h.
+//
+// bfloat16 x: with t = sum q x over a group of columns and X = sum x, the group's part of
+// the result is s (t - z X), where X is one more matrix instruction, shared by all rows of
+// W, and codes need no arithmetic. Where q is near z the two cancel, and what their roundings
+// leave is relative to (q + z) |x|: less than the result's own rounding as long as no x is
+// some 10^5 times the others at its zero point. Not so for binary32 x (a column 3000 times
+// the others: results off by 2 10^-5), where codes become q - z first, 12 more
+// instructions for eight of them (results off by 5 10^-8; one row, 8192 x 8192 in groups of
+// 64: 15.4 us, and 14.1 with the sums apart; 16 rows 20.0 and 19.4, 64 rows 55 both. bfloat16:
+// 11.2 and 9.9, 13.3 and 12.9, 23.5 and 24.2).
 //
 // A workgroup owns 16 or 32 rows of W, its waves share the columns. Everything a wave
 // reads goes straight to its own part of the LDS, up to four units (128 columns) ahead: 64
@@ -64,16 +73,21 @@ __device__ __forceinline__ int lower_halves(uint32_t lo, uint32_t hi) {
     return (int)((lo & 0xFFFFu) | (hi << 16));
 #endif
 }
-// The codes minus the row's zero point, exactly (whole numbers of at most 255).
+// The codes minus the row's zero point, exactly (whole numbers of at most 255), in that order.
 __device__ __forceinline__ i4v codes_minus(int w, float z) {
     i4v v{};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = i < 2 ? 4 * i : 4 * (i - 2) + 1;   // columns e and e + 2
-        const float a = (float)((w >> (4 * e)) & 15) - z;
-        const float b = (float)((w >> (4 * (e + 2))) & 15) - z;
-        v[i] = upper_halves(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
-    }
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int lo = w & 0x0F0F0F0F, hi = (int)(((unsigned)w >> 4) & 0x0F0F0F0Fu);
+    auto two = [&](f2 q) {
+        return upper_halves(__builtin_bit_cast(uint32_t, q[0] - z), __builtin_bit_cast(uint32_t, q[1] - z));
+    };
+    v[0] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, false));
+    v[1] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, true));
+    v[2] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, false));
+    v[3] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, true));
+#else
+    (void)w, (void)z;
+#endif
     return v;
 }
 
@@ -166,6 +180,7 @@ __global__ void __launch_bounds__(64 * W)
     constexpr int kS = L::kS, kZ = L::kZ, kX = L::kX, kSlot = L::kSlot, kLoads = L::kLoads;
     constexpr int kTermsAt = L::kTermsAt, kWave = L::kWave;
     constexpr int kXLanes = kXRow / 16;         // lanes of a row
+    constexpr bool kApart = XB;                 // sum q x and sum x, not sum (q - z) x
     static_assert((UN - 1) * kLoads < 64, "loads left in flight must fit the vmcnt field");
     static_assert(NM * RT * CT * NE * 256 <= kTermsAt, "the wave's sums take the place of its units");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[W * kWave];
@@ -309,7 +324,8 @@ __global__ void __launch_bounds__(64 * W)
             for (int k = 0; k < kTerms; ++k) term_at[k * 64 + g * 16 + (n16 ^ (4 * g))] = xt[k];
             asm volatile("" ::: "memory");   // (other lanes read them)
         }
-        f4 t[NM][RT][CT], sum[CT];
+        f4 t[NM][RT][CT], sum[CT];   // (sum: kApart)
+        auto zero_point = [&](int m, int r, int k) { return p.w[m].z ? (float)b.z[m][r][k] : 8.f; };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool begins = i % GP == 0, ends = i % GP == GP - 1;
@@ -317,7 +333,8 @@ __global__ void __launch_bounds__(64 * W)
 #pragma unroll
             for (int m = 0; m < NM; ++m)
 #pragma unroll
-                for (int r = 0; r < RT; ++r) a[m][r] = codes_to_bf16(b.w[m][r][i]);
+                for (int r = 0; r < RT; ++r)
+                    a[m][r] = kApart ? codes_to_bf16(b.w[m][r][i]) : codes_minus(b.w[m][r][i], zero_point(m, r, i / GP));
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 i4v xt[kTerms];
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(64 * W)
 #pragma unroll
                         for (int r = 0; r < RT; ++r)
                             t[m][r][c] = mfma_bf16(xt[k], a[m][r], fresh ? zero : t[m][r][c]);
-                    sum[c] = mfma_bf16(xt[k], ones, fresh ? zero : sum[c]);
+                    if constexpr (kApart) sum[c] = mfma_bf16(xt[k], ones, fresh ? zero : sum[c]);
                 }
             }
             if (ends) {
@@ -350,12 +367,15 @@ __global__ void __launch_bounds__(64 * W)
                     for (int r = 0; r < RT; ++r) {
                         const uint32_t code = b.s[m][r][i / GP];
                         const float s = __builtin_bit_cast(float, KIND::SB ? code << 16 : code);
-                        const float z = p.w[m].z ? (float)b.z[m][r][i / GP] : 8.f;
+                        const float z = kApart ? zero_point(m, r, i / GP) : 0.f;
 #pragma unroll
                         for (int c = 0; c < CT; ++c)
 #pragma unroll
-                            for (int e = 0; e < NE; ++e)
-                                acc[m][r][c][e] = fmaf(s, fmaf(-z, sum[c][e], t[m][r][c][e]), acc[m][r][c][e]);
+                            for (int e = 0; e < NE; ++e) {
+                                float v = t[m][r][c][e];
+                                if constexpr (kApart) v = fmaf(-z, sum[c][e], v);
+                                acc[m][r][c][e] = fmaf(s, v, acc[m][r][c][e]);
+                            }
                     }
                 if constexpr (CT > 1) __builtin_amdgcn_sched_barrier(0);   // (few registers)
             }

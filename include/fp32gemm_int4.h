@@ -51,11 +51,15 @@ typedef struct fg_int4 {
  *   12 out       : T rows of N elements, no overlap with the inputs
  *   13 ldo       : >= N
  *   14 stream
- * Products with the codes are exact and sums binary32 for either type; the sum over a
- * group is taken of q x and of x, and its part of the result is s (sum q x - z sum x).
- * (Where that is not finite the group is summed again from (q - z) x.) Scales are
- * finite, and 0 or of a magnitude between 2^-100 and 2^100; scales and zero points of a
- * matrix reach over less than 2 GiB each (else FG_ERR_UNSUPPORTED). T == 0 or N == 0: FG_OK,
+ * Products with the codes are exact and sums binary32 for either type. FG_TYPE_F32: the
+ * sum over a group is of (q - z) x, and its part of the result s times that; of an x below
+ * 2^-109 in magnitude the bits under 2^-133 do not count. FG_TYPE_BF16: the sum is taken of
+ * q x and of x, and its part is s (sum q x - z sum x); errors are binary32 roundings of
+ * s (q + z) |x|, below those of a bfloat16 result unless an x some 10^5 times the others
+ * meets its zero point. (Where a sum is not finite it is taken again, of (q - z) x times
+ * 2^-20.) Scales are finite, and 0 or of a magnitude between 2^-100 and 2^100; scales and
+ * zero points of a matrix reach over less than 2 GiB each (else FG_ERR_UNSUPPORTED).
+ * T == 0 or N == 0: FG_OK,
  * nothing enqueued. K == 0: zeros. Repeated calls give identical bits. No workspace.
  */
 fg_status fg_gemm_int4(int64_t T, int64_t N, int64_t K, int32_t group, fg_type type,
