@@ -516,16 +516,34 @@ hipError_t launch_staged(const RowsParams& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// 16 rows of each matrix to a workgroup, or 32, which share their rows of x: by the rows
+// that the busiest of the 256 CUs gets. A row costs a ninth more with 16 for up to four rows of
+// x, two fifths more for many. One matrix, K 4096 (8192 for N 8192), groups of 64, 16 and 32
+// rows: one row of x, bfloat16, N 4096 5.2 and 6.2 us, 6144 7.3 and 6.6, 8192 11.6 and 10.4, 12288 10.3 and
+// 11.1, 16384 13.9 and 12.0 (binary32 7.2 and 9.0, 10.0 and 9.3, 16.5 and 15.2, 14.5 and 16.8, 18.0 and
+// 17.7); 16 rows N 1024 5.0 and 6.3, 4096 6.3 and 7.6, 6144 10.0 and 8.0, 8192 16.8 and 13.4,
+// 12288 14.0 and 13.3; 64 rows in binary32 N 1024 22 and 29, 4096 26 and 31, 6144 47 and 32, 12288 71 and
+// 60. Two matrices, 16 rows: N 4096 9.2 and 11.7, 8192 25 and 22 (binary32 12.6 and 15.6, 37 and
+// 29); of them with up to four rows of x 32 gain nothing (N 8192 19.5 and 19.3, 12288 16.5 and 18.7), and
+// with more than 32 bfloat16 rows they have no room.
 template <typename KIND, bool XB, int NM>
 hipError_t launch_few(const RowsParams& p, hipStream_t stream) {
+    const int of16 = (p.N + 16 * 256 - 1) / (16 * 256), of32 = (p.N + 32 * 256 - 1) / (32 * 256);
     if (p.T <= 4) {
         if constexpr (NM == 1)
-            if (p.N >= 8192) return launch_staged<KIND, XB, NM, 2, 1, 1, 4, 4>(p, stream);
+            if (2 * of32 * 8 <= of16 * 9) return launch_staged<KIND, XB, NM, 2, 1, 1, 4, 4>(p, stream);
         return launch_staged<KIND, XB, NM, 1, 1, 1, NM == 2 ? 2 : 4, 4>(p, stream);
     }
-    if (p.T <= 16) return launch_staged<KIND, XB, NM, NM == 2 ? 1 : 2, 1, 4, XB ? 2 : 1, XB ? 4 : 8>(p, stream);
-    if (p.T <= 32) return launch_staged<KIND, XB, NM, 2, 2, 4, 1, XB ? 8 : 6>(p, stream);
-    return launch_staged<KIND, XB, NM, XB && NM == 2 ? 1 : 2, 4, 4, 1, XB ? 8 : 4>(p, stream);
+    const bool wide = 2 * of32 * 5 <= of16 * 7;
+    if (p.T <= 16)
+        return wide ? launch_staged<KIND, XB, NM, 2, 1, 4, XB ? 2 : 1, XB ? 4 : 8>(p, stream)
+                    : launch_staged<KIND, XB, NM, 1, 1, 4, XB ? 2 : 1, XB ? 4 : 8>(p, stream);
+    if (p.T <= 32)
+        return wide ? launch_staged<KIND, XB, NM, 2, 2, 4, 1, XB ? 8 : 6>(p, stream)
+                    : launch_staged<KIND, XB, NM, 1, 2, 4, 1, XB ? 8 : 6>(p, stream);
+    if constexpr (!(XB && NM == 2))
+        if (wide) return launch_staged<KIND, XB, NM, 2, 4, 4, 1, XB ? 8 : 4>(p, stream);
+    return launch_staged<KIND, XB, NM, 1, 4, 4, 1, XB ? 8 : 4>(p, stream);
 }
 
 template <bool XB, int NM>

@@ -4,6 +4,8 @@ import pytest
 
 import fp32_gemm_tile_amd as fg
 
+from test_gpu_int4 import check
+
 pytestmark = pytest.mark.gpu
 
 
@@ -79,3 +81,12 @@ def test_small_values_of_x(T):
         # K + 26 roundings of a binary32 sum, each also of at most half of 2^-149
         bound = (K + 26) * (2.0 ** -23 * (np.abs(x).astype(np.float64) @ np.abs(v).T) + 2.0 ** -149) + 2.0 ** -133 * size
         assert (np.abs(out.double().cpu().numpy() - want) <= bound).all(), e
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 13, 27, 64])
+def test_both_numbers_of_rows_of_a_workgroup(T, ty):
+    """4096 rows of W are 256 workgroups of 16; 4100 have 32 each where that is quicker."""
+    for N in (4096, 4100):
+        for gated in (False, True):
+            check(T, N, 200, 64, ty, "bf16", True, gated, pad=1)
