@@ -8,8 +8,8 @@
 // One kernel for all: B's rows are the instruction's rows and A's its columns, so a
 // lane holds one row of C and four consecutive columns of it. FORWARD's tile of B
 // is half gate and half up, divided so that a wave has both products of the same columns and
-// the activation needs no exchange. DX runs through gate's steps and then up's into
-// the same sums. bfloat16 products are exact and their sums binary32
+// the activation needs no exchange. DX runs through gate's steps and then up's, in bfloat16
+// into the same sums. bfloat16 products are exact and their sums binary32
 // (v_mfma_f32_16x16x32_bf16); binary32 uses v_mfma_f32_16x16x4_f32.
 //
 // Tiles go from memory straight to LDS, NS stages, the next ones in flight while
@@ -362,6 +362,12 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
+    // DX in binary32: gate's sum, while up's is taken. (One sum of both is 2 I roundings long
+    // where two products and an addition have I: 1025 tokens, 1536 x 2047, errors 1.15 10^-6
+    // and 8.1 10^-7, 248 us both. bfloat16 results round far above either.)
+    constexpr bool kApart = OP == GATED_DX && !BF16;
+    f4 of_gate[kApart ? TI : 1][kApart ? TJ : 1] = {};
+
     // row of B's tile that column tile j of the wave starts at
     auto b_row = [&](int j) {
         return kDual ? (j < PJ ? 0 : BN / 2) + wj + 16 * (j % PJ) : wj + 16 * j;
@@ -428,13 +434,31 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 1) * kLoads) : "memory");
     read(0, o[0]);
     int s = s0;
-    for (; s + 2 <= whole_end; s += 2) {
-        step(s, o[0], o[1]);
-        step(s + 1, o[1], o[0]);
-    }
-    if (s < whole_end) {
-        step(s, o[0], o[1]);
-        if constexpr (kDual) o[0] = o[1];
+    auto steps_to = [&](int end) __attribute__((always_inline)) {
+        for (; s + 2 <= end; s += 2) {
+            step(s, o[0], o[1]);
+            step(s + 1, o[1], o[0]);
+        }
+        if (s < end) {
+            step(s++, o[0], o[1]);
+            if constexpr (kDual || kApart) o[0] = o[1];
+        }
+    };
+    if constexpr (kApart) {
+#pragma unroll 1
+        for (int k = s0 < half && half < s1 ? 0 : 1; k < 2; ++k) {
+            steps_to(k == 0 ? half : s1);
+            if (k == 1) break;
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) {
+                    of_gate[i][j] = acc[i][j];
+                    acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+                }
+        }
+    } else {
+        steps_to(whole_end);
     }
     if constexpr (kDual) {
         if (partial) {
@@ -449,6 +473,12 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
                 for (int i = 0; i < TI; ++i) row(o[0], u, i);
             }
         }
+    }
+    if constexpr (kApart) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) acc[i][j] += of_gate[i][j];
     }
     auto all_done = [] { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     all_done();

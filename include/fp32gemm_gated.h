@@ -26,6 +26,10 @@
  * are rounded to the block's type before they meet gate, up and x, as tensors
  * of that type would be.
  *
+ * Activations are binary32 with the hardware's exponential and reciprocal: act(v) of silu
+ * and gelu is off by at most (|v| + 8) 2^-23 max(|act(v)|, |v| / 4), their slopes by
+ * (2 |v| + 16) 2^-23 (gelu's erf is a polynomial, off by 4e-7). Sums of the products are
+ * binary32, n roundings of a sum of n terms at most; dx in binary32 is two sums, added.
  * Infinities and NaN follow the formulas: silu and gelu of -inf are NaN (-inf times 0) and
  * their slopes 0, of +inf infinite and 1.
  */

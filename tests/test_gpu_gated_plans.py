@@ -79,3 +79,28 @@ def test_activations_of_the_infinities(ty, act):
         for t in range(T):
             assert same(h[t], want) and same(again[t], want)
         assert same(dgate[:, 1], slope * T) and same(dup[:, 1], want * T)
+
+
+def test_dx_in_binary32_adds_two_sums():
+    """dG gate is 2^24 and dU up 256 times 2^-3: whole beside each other, lost in one running
+    sum. Every tile, in one slice and in several, and the launch of all gradients."""
+    import torch
+    I = 256
+
+    def run(T, H, all_three):
+        x, ones = torch.zeros(T, H, device="cuda"), torch.ones(T, I, device="cuda")
+        gate, up = torch.full((I, H), 2.0 ** 24 / I, device="cuda"), torch.full((I, H), 2.0 ** -3, device="cuda")
+        dx = torch.empty(T, H, device="cuda")
+        dw = [torch.empty_like(gate) for _ in range(2)] if all_three else [None, None]
+        fg.gated_backward(ones, x, gate, up, (ones, ones), dx, *dw, activation="none")
+        assert (dx == 2.0 ** 24 + 32).all()
+
+    try:
+        for tile in range(len(fg.fg_gated_tiles(1, 0))):
+            for slices in (1, 2, 3):
+                assert fg.fg_set_gated_tile(1, 0, tile, slices) == fg.FG_OK
+                run(70, 40, False)
+    finally:
+        fg.fg_set_gated_tile(1, 0)
+    assert fg.fg_select_gated_pair(0, 517, 1000, I, 0)[0] >= 0
+    run(517, 1000, True)
