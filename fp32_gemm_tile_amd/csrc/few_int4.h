@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(64 * W)
             if constexpr (decltype(edge)::value) {
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j)
-                    b.x[0][0][j] = keep<XS>(b.x[0][0][j], p.K - u * 128 - 8 * n16 - 4 * j);
+                    b.x[0][0][j] = keep<XB>(b.x[0][0][j], p.K - u * 128 - 8 * n16 - 4 * j);
             }
             terms<XB, false>(b.x[0][0], xt);
 #pragma unroll
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(64 * W)
                     if constexpr (decltype(edge)::value) {
 #pragma unroll
                         for (int j = 0; j < kPieces; ++j)
-                            b.x[c][i][j] = keep<XS>(b.x[c][i][j], p.K - u * 128 - 32 * i - 8 * g - 4 * j);
+                            b.x[c][i][j] = keep<XB>(b.x[c][i][j], p.K - u * 128 - 32 * i - 8 * g - 4 * j);
                     }
                     terms<XB, false>(b.x[c][i], xt);
                 }
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(64 * W)
                     for (int m = 0; m < NM; ++m)
 #pragma unroll
                         for (int r = 0; r < RT; ++r)
-                            t[m][r][c] = mfma_bf16(xt[k], a[m][r], fresh ? zero : t[m][r][c]);
-                    if constexpr (kApart) sum[c] = mfma_bf16(xt[k], ones, fresh ? zero : sum[c]);
+                            t[m][r][c] = mfma16<true>(xt[k], a[m][r], fresh ? zero : t[m][r][c]);
+                    if constexpr (kApart) sum[c] = mfma16<true>(xt[k], ones, fresh ? zero : sum[c]);
                 }
             }
             if (ends) {
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(64 * W)
                 i4v x[kPieces], xt[kTerms];
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j)
-                    x[j] = keep<XS>(__builtin_amdgcn_raw_buffer_load_b128(
+                    x[j] = keep<XB>(__builtin_amdgcn_raw_buffer_load_b128(
                                         xagain, (uint32_t)((16 * c + t0) * p.ldx * XS) + xoff +
                                                     (uint32_t)i * (32 * XS) + 16 * j, 0, 0),
                                     p.K - 32 * i - 8 * g - 4 * j);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(64 * W)
                     for (int r = 0; r < RT; ++r) {
                         f4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int k = 0; k < kTerms; ++k) v = mfma_bf16(xt[k], a[m][r], v);
+                        for (int k = 0; k < kTerms; ++k) v = mfma16<true>(xt[k], a[m][r], v);
 #pragma unroll
                         for (int e = 0; e < NE; ++e) acc[m][r][c][e] = fmaf(s[m][r], v[e], acc[m][r][c][e]);
                     }

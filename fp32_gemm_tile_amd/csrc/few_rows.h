@@ -22,47 +22,10 @@
 
 #include "fg_device.h"
 #include "fg_gated_kernels.h"
-#include "fg_lds_tile.h"
+#include "fg_mfma16.h"
 
 namespace fg {
 namespace {
-
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f4 mfma_bf16(i4v a, i4v b, f4 c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
-                                                   __builtin_bit_cast(bf8, b), c, 0, 0, 0);
-#else
-    (void)a, (void)b;
-    return c;
-#endif
-}
-__device__ __forceinline__ f4 mfma_f32(i4v a, i4v b, f4 c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    const f4 fa = __builtin_bit_cast(f4, a), fb = __builtin_bit_cast(f4, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
-#else
-    (void)a, (void)b;
-#endif
-    return c;
-}
-
-// Elements [0, left) of a 16-byte piece, zeros after them.
-template <int SIZE>
-__device__ __forceinline__ i4v keep(i4v v, int left) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        if constexpr (SIZE == 4) {
-            if (d >= left) v[d] = 0;
-        } else {
-            if (2 * d >= left) v[d] = 0;
-            else if (2 * d + 1 >= left) v[d] &= 0xFFFF;
-        }
-    }
-    return v;
-}
 
 // XB: x, weights and results are bfloat16. NE rows of x per lane (rows 4 e + g, e < NE).
 // FOLD: 8 rows of gate and 8 of up make one tile, for twice the workgroups.
@@ -118,7 +81,7 @@ __global__ void __launch_bounds__(512) rows_kernel(RowsParams p) {
     auto use = [&](const Unit& b) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < NT; ++m)
-            acc[m] = XB ? mfma_bf16(b.x, b.w[m], acc[m]) : mfma_f32(b.x, b.w[m], acc[m]);
+            acc[m] = mfma16<XB>(b.x, b.w[m], acc[m]);
     };
 
     // No branch around a load, so that the wait before a unit's use counts the loads
@@ -151,13 +114,13 @@ __global__ void __launch_bounds__(512) rows_kernel(RowsParams p) {
         Unit b;
         if constexpr (FOLD) {
             // (a chunk past K may be past the matrix)
-            b.w[0] = keep<XS>(*reinterpret_cast<const i4v*>(own_row + (left > 0 ? at + 16 * g : 0)), left);
+            b.w[0] = keep<XB>(*reinterpret_cast<const i4v*>(own_row + (left > 0 ? at + 16 * g : 0)), left);
         } else {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-                b.w[m] = keep<XS>(__builtin_amdgcn_raw_buffer_load_b128(wbuf[m], woff[m] + at, 0, 2), left);
+                b.w[m] = keep<XB>(__builtin_amdgcn_raw_buffer_load_b128(wbuf[m], woff[m] + at, 0, 2), left);
         }
-        b.x = keep<XS>(__builtin_amdgcn_raw_buffer_load_b128(xbuf, xoff + at, 0, 0), left);
+        b.x = keep<XB>(__builtin_amdgcn_raw_buffer_load_b128(xbuf, xoff + at, 0, 0), left);
         use(b);
     }
 

@@ -5,7 +5,7 @@
 //   DX       dx = dG Wg + dU Wu
 //   DW       dWg = dG^T x, dWu = dU^T x (+ beta times what was there)
 //
-// One kernel for all: B's rows are the instruction's rows and A's its columns, so a
+// One kernel for all: B's rows are the instruction's rows and A's its columns, so that a
 // lane holds one row of C and four consecutive columns of it. FORWARD's tile of B
 // is half gate and half up, divided so that a wave has both products of the same columns and
 // the activation needs no exchange. DX runs through gate's steps and then up's, in bfloat16
@@ -33,33 +33,12 @@
 #include "fg_device.h"
 #include "fg_e4m3.h"
 #include "fg_gated_kernels.h"
-#include "fg_lds_tile.h"
+#include "fg_mfma16.h"
 
 namespace fg {
 namespace {
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
-
-// 16 x 16 products: lane (n, g) = (lane % 16, lane / 16) gives row n of both operands
-// and gets columns 4 g to 4 g + 3 of row n of C (the operands are exchanged, so that a
-// lane's sums are neighbours in a row).
-template <bool BF16>
-__device__ __forceinline__ void mfma(i4v a, i4v b, f4& c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (BF16) {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
-                                                    __builtin_bit_cast(bf8, b), c, 0, 0, 0);
-    } else {
-        const f4 fa = __builtin_bit_cast(f4, a), fb = __builtin_bit_cast(f4, b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[e], fb[e], c, 0, 0, 0);
-    }
-#else
-    (void)a, (void)b, (void)c;
-#endif
-}
 
 // 4 k of 16 columns per 16 lanes: lane l gives the address of row l / 4, columns
 // 4 (l % 4), and gets column l of the four rows.
@@ -73,21 +52,6 @@ __device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
     (void)p;
     return uint2{0, 0};
 #endif
-}
-
-// Elements [0, left) of a 16-byte chunk, zeros after them.
-template <bool BF16>
-__device__ __forceinline__ i4v keep(i4v v, int left) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        if constexpr (!BF16) {
-            v[d] = d < left ? v[d] : 0;
-        } else {
-            const int n = left - 2 * d;
-            v[d] &= n >= 2 ? -1 : (n == 1 ? 0xFFFF : 0);
-        }
-    }
-    return v;
 }
 
 // A tile of R rows (of m or n) and KB bytes of k, and how it gets to LDS and back.
@@ -398,7 +362,7 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
     };
     auto row = [&](const Operands& o, int u, int i) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) mfma<BF16>(o.b[u][j], o.a[u][i], acc[i][j]);
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma16<BF16>(o.b[u][j], o.a[u][i], acc[i][j]);
     };
     // Step s, its operands in `now`: stage s + 1 is there for everyone and everyone
     // has read stage s, which is loaded again. The matrix instructions begin at
