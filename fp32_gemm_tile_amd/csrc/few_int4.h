@@ -32,8 +32,8 @@
 // and go back to the LDS; more rows have as many terms as the instructions take.
 //
 // Bound by memory for one row of x (8192 x 8192, 4-bit gate and up in groups of 32 with
-// binary32 scales and zero points, 89 MB: 22 us, 4.0 TB/s; one such matrix in groups of 128
-// 9.8 us, 3.5 TB/s, of which 3 us are the launch and the first trip to memory), by the
+// binary32 scales and zero points, 89 MB past the caches: 22.7 us, 3.9 TB/s; one such matrix in groups
+// of 128 10.0 us, 3.4 TB/s, of which 3 us are the launch and the first trip to memory), by the
 // vector unit for many: a binary32 x costs 6 instructions per element to be made terms, in
 // every workgroup anew (16 rows, 8192 x 8192 in groups of 64: 19 us, 12 of them these; 64
 // rows 55 us, and 24 in bfloat16).

@@ -22,8 +22,9 @@
 //
 // Large products are bound by the matrix cores: 4096 tokens, 4096 x 8192 in bfloat16, 256
 // x 256 of B's and A's rows to a workgroup of eight waves (64 x 128 each, as large as the
-// registers hold): forward 414 to 430 us (1280 to 1330 TFLOP/s), 460 with G and U kept, dx
-// 400, dgate and dup 393; the cores are busy 68 to 71 % and the clock is down to 1.65 GHz, and
+// registers hold), one set of inputs again and again: forward 400 us (1370 TFLOP/s), 460 with
+// G and U kept (475 on inputs that change), dx, and dgate and dup, 400 to 405 each; the cores
+// are busy 58 % with G and U kept, 68 in dx, dgate and dup, the clock is down to 1.65 GHz, and
 // with the 32 x 32 x 16 instruction both products give the same time. Short ones are bound by
 // latency, a step of a small tile taking as long as its barrier, its loads' issue and the next
 // reads: there a step is 128 or 256 bytes of k (32 tokens, 4096 x 8192: steps of 64 bytes 46
@@ -172,7 +173,7 @@ struct Quad {
 // codes4 for binary32 sums, whose quotients are seldom near a middle between codes: the
 // codes of x r with r off by 2^-21 to either side, which is more than r and the product are
 // off by (2^-23), agree unless one is in between. 15 instructions per four elements for 26
-// (8192 tokens, 2048 x 8192: 553 us and 542).
+// (8192 tokens, 2048 x 8192, one set of inputs: 533 us, and 541 with codes4 alone).
 __device__ __forceinline__ uint32_t codes_of(const f4& x, const Divisor& d) {
     const float lo = fmaf(d[0], -0x1p-21f, d[0]), hi = fmaf(d[0], 0x1p-21f, d[0]);
     int a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * lo, x[1] * lo, 0, false);
@@ -505,7 +506,7 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < TI; ++i) {
-                        // (of all magnitudes, and again of the finite ones if need be: 546 us and 533)
+                        // (of all magnitudes, and again of the finite ones if need be: 533 us, at once 538)
                         uint32_t v = 0;
 #pragma unroll
                         for (int j = 0; j < PJ; ++j)
@@ -540,7 +541,7 @@ __device__ __forceinline__ void tile_body(const GatedTileParams& p, uint8_t* lds
             }
         }
         // Row tile by row tile in one loop, whose code is fetched once (unrolled it was 130
-        // KB; 8192 tokens, 2048 x 8192 with codes, eight rounds of tiles: 597 us and 547).
+        // KB; 8192 tokens, 2048 x 8192 with codes, eight rounds of tiles: 597 us before, 547 then).
         float* const own_u = own + NW * 16 * kPitch;
         constexpr int kTurns = 16 / kRows;
         auto codes_out = [&](int m, const f4& v, const Divisor& d, int64_t row, int64_t col) __attribute__((always_inline)) {
@@ -934,7 +935,10 @@ __device__ __forceinline__ void activate_both(float x, float& a, float& d) {
 }
 
 // dG, dU and h in one pass, four columns per thread, so that a wave reads and writes whole
-// lines. Bound by HBM: 4096 x 8192 in bfloat16, five matrices, 61 us, 5.5 TB/s.
+// lines. bfloat16: dG and dU are rounded before the products that read them, as a tensor of
+// that type between two layers is; dx, dgate and dup are off by 0.0024 of their size where
+// binary32 dG and dU would leave 0.0017, as two bfloat16 terms each and twice the matrix
+// instructions. Bound by HBM: 4096 x 8192 in bfloat16, five matrices, 61 us, 5.5 TB/s.
 template <bool BF16, bool CODES, int ACT>
 __global__ void __launch_bounds__(256) gated_grad_kernel(GatedGradParams p) {
     constexpr int SIZE = BF16 ? 2 : 4;

@@ -105,7 +105,8 @@ def int4_weights(codes, scales, zeros, K, group):
 
 
 def int4_product(x, w, most, bf16, group, rounded=True):
-    """(x w^T, bound): sums of q x and of x apart, so magnitudes are those of q + z."""
+    """(x w^T, bound): sums of q x and of x apart, so magnitudes are those of q + z (sums of
+    (q - z) x are within it)."""
     n = x.shape[1] + 2 * cdiv(x.shape[1], group) + 24
     y, e = x @ w.T, n * U * (np.abs(x) @ most.T)
     return y, (e + half_step(np.abs(y) + e, bf16) if rounded else e)
