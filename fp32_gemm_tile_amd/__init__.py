@@ -1073,7 +1073,8 @@ def gated_backward(dout, x, gate, up, saved, dx=None, dgate=None, dup=None, out=
     None, dgate and dup together. workspace: a contiguous GPU tensor of at least
     fg_gated_backward_min_workspace_size(T, I, type) bytes (more is used up to
     fg_gated_backward_workspace_size) that no call running at the same time uses; None
-    allocates one with torch (with a raw stream handle it has to be given). Enqueued on ``stream`` (default: torch's current stream)."""
+    allocates one with torch (with a raw stream handle it has to be given). Enqueued on
+    ``stream`` (default: torch's current stream)."""
     torch, types = _torch_types()
     dev = _gpu(dout, "dout")
     ty, dt = _value_type(types, dout, "dout"), dout.dtype
